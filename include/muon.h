@@ -485,6 +485,72 @@ size_t dion_workspace_bytes(const muon_dion_problem* probs, int count, int rank)
 int dion_step(const muon_dion_problem* probs, int count, int rank, float mu, float eta,
               void* workspace, size_t ws_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * 8-bit floating point matrices with a scale for each block of 128, and their
+ * product: the forward, input-gradient and weight-gradient products of the
+ * weight matrices that this library updates.
+ *
+ * Format.  A matrix [rows][cols] is a pair of device arrays:
+ *   q  codes, one byte per entry, row-major with a row pitch ldq (a multiple
+ *      of 16, at least cols rounded up to MUON_FP8_GROUP); OCP e4m3 or e5m2.
+ *      Columns from cols up to the next multiple of 128 hold zeros.
+ *   s  scale bytes (E8M0: byte b stands for 2^(b - 127); 255 is NaN), one per
+ *      row and group of 128 columns.  Byte (row, group g) is at
+ *          s[((g / 4) * R4 + row) * 4 + g % 4],  R4 = rows rounded up to 4,
+ *      fp8_scale_bytes(rows, cols) bytes in all.
+ * Entry (i, j) has the value q[i][j] * 2^(s(i, j / 128) - 127).  A block of
+ * 128 x 128 under one scale is 128 rows with equal bytes.
+ *
+ * fp8_quantize  x [rows][cols] (row pitch ldx entries, F32 or BF16) -> (q, s)
+ *               and/or (qt, st), the same matrix transposed: qt [cols][ldqt]
+ *               with groups along the rows of x, exactly what fp8_quantize
+ *               gives for x^T.  Either pair may be NULL.  x is read once.
+ *               block_rows 1: a scale for each row's group of 128 columns;
+ *               block_rows 128: one for each 128 x 128 block (then q and qt
+ *               hold the same values).
+ *               A group's scale is 2^e with the smallest e for which its
+ *               largest finite |x| is at most MAX 2^e (MAX = 448 for e4m3,
+ *               57344 for e5m2), e >= -126; 2^0 for a group of zeros.  Its
+ *               codes are x 2^-e rounded to nearest even (a single rounding).
+ *               Infinities and NaN take no part in the scale; NaN becomes
+ *               NaN, an infinity NaN in e4m3 and an infinity in e5m2.
+ *               Unused scale bytes are written as 127.
+ *
+ * fp8_gemm      C <- beta C + alpha A B^T, A [m][K] in a_fmt, B [n][K] in
+ *               b_fmt, both with K columns stored (a multiple of 128, zeros
+ *               past the matrix), C [m][n] with row pitch ldc, F32 or BF16.
+ *               a_fmt: e4m3 or e5m2; b_fmt: e4m3.
+ *               Sums are fp32 over the whole contraction, and C is rounded
+ *               once.  For an F32 C every product of two entries is exact; for
+ *               a BF16 C it goes through the fp8 matrix instructions, which
+ *               drop, of eight neighbouring products, what lies more than 13
+ *               bits below the largest (1.5e-5 of a Gaussian product's norm,
+ *               against bf16's own 2^-9).  With beta = 0, C is not read.
+ *               K = 0 gives beta C.
+ *               Uses: y = x W^T (A = x, B = W); dx = dy W (A = dy, B = W^T
+ *               from qt); the weight gradient straight into the momentum,
+ *               M <- beta M + alpha dy^T x (A = dy^T, B = x^T, both from qt).
+ *   workspace   fp8_gemm_workspace_bytes(m, n, K) bytes (may be 0), 16-byte
+ *               aligned; contents on entry do not matter.  Calls that share
+ *               one must not overlap in time.
+ *
+ * Sides are at most MUON_FP8_MAX_SIDE (MUON_EINVAL).  Pointers 16-byte
+ * aligned (MUON_EALIGN); unknown formats and dtypes give MUON_EDTYPE, a
+ * missing or short workspace MUON_EWORKSPACE.  A zero rows, cols, m or n is
+ * MUON_OK and launches nothing.
+ * ------------------------------------------------------------------------- */
+#define MUON_FP8_GROUP 128
+#define MUON_FP8_MAX_SIDE 4194240
+enum muon_fp8_format { MUON_FP8_E4M3 = 0, MUON_FP8_E5M2 = 1 };
+
+size_t fp8_scale_bytes(int64_t rows, int64_t cols);
+int fp8_quantize(const void* x, int x_dtype, int64_t rows, int64_t cols, int64_t ldx, int fmt, int block_rows,
+                 void* q, int64_t ldq, void* s, void* qt, int64_t ldqt, void* st, void* stream);
+size_t fp8_gemm_workspace_bytes(int64_t m, int64_t n, int64_t K);
+int fp8_gemm(const void* A, int a_fmt, int64_t lda, const void* sa, const void* B, int b_fmt, int64_t ldb,
+             const void* sb, void* C, int c_dtype, int64_t ldc, int64_t m, int64_t n, int64_t K, float alpha,
+             float beta, void* workspace, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

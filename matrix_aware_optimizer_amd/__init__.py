@@ -17,3 +17,5 @@ from ._abi import MUON_DION_MAX_RANK, dion_step, dion_workspace_bytes  # noqa: F
 from ._abi import ns_bf16_min_side, ns_residual_iterations, ns_workspace_status, set_split_wait_limit  # noqa: F401
 from ._abi import muon_momentum_noalloc, time_next_launch  # noqa: F401
 from .signmuon import SignMuonStep  # noqa: F401
+from ._abi import MUON_FP8_GROUP, MUON_FP8_MAX_SIDE, fp8_buffers, fp8_gemm, fp8_gemm_workspace_bytes  # noqa: F401
+from ._abi import fp8_quantize, fp8_scale_shape  # noqa: F401

@@ -85,6 +85,13 @@ SIGNATURES = {
     "dion_workspace_bytes": (_c_size, [ctypes.c_void_p, _c_int, _c_int]),
     "dion_step": (_c_int, [ctypes.c_void_p, _c_int, _c_int, _c_float, _c_float, _c_void_p, _c_size,
                            _c_void_p]),
+    "fp8_scale_bytes": (_c_size, [_c_i64, _c_i64]),
+    "fp8_quantize": (_c_int, [_c_void_p, _c_int, _c_i64, _c_i64, _c_i64, _c_int, _c_int, _c_void_p, _c_i64,
+                              _c_void_p, _c_void_p, _c_i64, _c_void_p, _c_void_p]),
+    "fp8_gemm_workspace_bytes": (_c_size, [_c_i64, _c_i64, _c_i64]),
+    "fp8_gemm": (_c_int, [_c_void_p, _c_int, _c_i64, _c_void_p, _c_void_p, _c_int, _c_i64, _c_void_p, _c_void_p,
+                          _c_int, _c_i64, _c_i64, _c_i64, _c_i64, _c_float, _c_float, _c_void_p, _c_size,
+                          _c_void_p]),
 }
 
 _LIB: Optional[ctypes.CDLL] = None
@@ -561,3 +568,95 @@ def dion_step(problems, rank: int, mu: float, eta: float, workspace: Optional[to
     _check("dion_step", lib().dion_step(ctypes.cast(arr, ctypes.c_void_p), len(problems), int(rank),
                                         float(mu), float(eta), _dev(ws, "workspace"),
                                         ws.numel() * ws.element_size(), _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
+# fp8 matrices with a scale for each block of 128
+# ---------------------------------------------------------------------------
+
+MUON_FP8_GROUP = 128
+MUON_FP8_MAX_SIDE = 4194240
+_FP8 = {torch.float8_e4m3fn: 0, torch.float8_e5m2: 1}
+_FP8_BY_NAME = {"e4m3": torch.float8_e4m3fn, "e5m2": torch.float8_e5m2}
+
+
+def _ceil_to(n: int, m: int) -> int:
+    return -(-n // m) * m
+
+
+def fp8_scale_shape(rows: int, cols: int) -> Tuple[int, int, int]:
+    """Shape of the scale bytes of a rows x cols matrix: [words of four groups][rows][4]."""
+    return _ceil_to(cols, 4 * MUON_FP8_GROUP) // (4 * MUON_FP8_GROUP), _ceil_to(rows, 4), 4
+
+
+def fp8_buffers(rows: int, cols: int, fmt: str = "e4m3", device="cuda") -> Tuple[torch.Tensor, torch.Tensor]:
+    """Uninitialised (codes [rows, cols rounded up to 128], scales) for a rows x cols matrix."""
+    q = torch.empty((rows, _ceil_to(cols, MUON_FP8_GROUP)), dtype=_FP8_BY_NAME[fmt], device=device)
+    return q, torch.empty(fp8_scale_shape(rows, cols), dtype=torch.uint8, device=device)
+
+
+def _rows2(t: torch.Tensor, name: str) -> Tuple[int, int]:
+    """(pointer, row pitch) of a 2-D device tensor whose rows are contiguous."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be 2-D with contiguous rows")
+    if t.shape[0] > 1 and t.shape[1] > 0 and t.stride(0) < t.shape[1]:
+        raise ValueError(f"{name} must not overlap itself")
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+
+
+def _fp8_operand(q: torch.Tensor, s: torch.Tensor, rows: int, cols: int, name: str):
+    """(codes, pitch, scales) of an fp8 matrix that holds rows x cols."""
+    if q.dtype not in _FP8:
+        raise TypeError(f"{name} must be float8_e4m3fn or float8_e5m2")
+    ptr, ld = _rows2(q, name)
+    if q.shape[0] != rows or q.shape[1] < _ceil_to(cols, MUON_FP8_GROUP):
+        raise ValueError(f"{name} must hold {rows} rows of at least {_ceil_to(cols, MUON_FP8_GROUP)} codes")
+    if s.dtype != torch.uint8 or tuple(s.shape) != fp8_scale_shape(rows, cols):
+        raise ValueError(f"the scales of {name} must be uint8 of shape {fp8_scale_shape(rows, cols)}")
+    if rows <= 1 or cols == 0:      # no second row: the pitch is not used, the library wants a multiple of 16
+        ld = _ceil_to(q.shape[1], 16)
+    return ptr, ld, _dev(s, f"scales of {name}")
+
+
+def fp8_quantize(x: torch.Tensor, q: Optional[torch.Tensor], s: Optional[torch.Tensor],
+                 qt: Optional[torch.Tensor] = None, st: Optional[torch.Tensor] = None, block_rows: int = 1,
+                 stream=None) -> None:
+    """Codes and scales of ``x`` into (q, s), and those of its transpose into (qt, st); either may be None.
+
+    ``block_rows`` 1: a scale for each row's group of 128 columns; 128: one for each 128 x 128 block."""
+    if (q is None) != (s is None) or (qt is None) != (st is None) or (q is None and qt is None):
+        raise ValueError("give (q, s), (qt, st) or both")
+    xp, ldx = _rows2(x, "x")
+    rows, cols = x.shape
+    if q is not None and qt is not None and q.dtype != qt.dtype:
+        raise TypeError("q and qt must have one format")
+    qp = _fp8_operand(q, s, rows, cols, "q") if q is not None else (None, 0, None)
+    tp = _fp8_operand(qt, st, cols, rows, "qt") if qt is not None else (None, 0, None)
+    fmt = _FP8[(q if q is not None else qt).dtype]
+    _check("fp8_quantize", lib().fp8_quantize(xp, dtype_code(x), rows, cols, max(ldx, cols), fmt, int(block_rows),
+                                              qp[0], qp[1], qp[2], tp[0], tp[1], tp[2], _stream(stream)))
+
+
+def fp8_gemm_workspace_bytes(m: int, n: int, K: int) -> int:
+    return int(lib().fp8_gemm_workspace_bytes(m, n, K))
+
+
+def fp8_gemm(A: torch.Tensor, sa: torch.Tensor, B: torch.Tensor, sb: torch.Tensor, C: torch.Tensor,
+             alpha: float = 1.0, beta: float = 0.0, workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    """``C <- beta C + alpha A B^T`` for fp8 operands (codes, scales) with K = ``A.shape[1]`` columns."""
+    m, K = A.shape
+    n = B.shape[0]
+    if B.shape[1] != K or tuple(C.shape) != (m, n):
+        raise ValueError("A is m x K, B n x K and C m x n")
+    ap, lda, sap = _fp8_operand(A, sa, m, K, "A")
+    bp, ldb, sbp = _fp8_operand(B, sb, n, K, "B")
+    cp, ldc = _rows2(C, "C")
+    need = fp8_gemm_workspace_bytes(m, n, K)
+    ws, nbytes = None, 0
+    if need > 0:
+        workspace = _workspace(need, C, workspace)
+        ws, nbytes = _dev(workspace, "workspace"), workspace.numel() * workspace.element_size()
+    _check("fp8_gemm", lib().fp8_gemm(ap, _FP8[A.dtype], lda, sap, bp, _FP8[B.dtype], ldb, sbp, cp, dtype_code(C),
+                                      max(ldc, n), m, n, K, float(alpha), float(beta), ws, nbytes, _stream(stream)))

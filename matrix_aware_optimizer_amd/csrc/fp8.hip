@@ -1,0 +1,454 @@
+// 8-bit floating point matrices with a power-of-two scale for each row's group
+// of 128 columns: the quantiser and the product C = beta C + alpha A B^T.
+//
+// Format.  A matrix [rows][cols] is held as codes q [rows][ldq] (one byte, OCP
+// e4m3 or e5m2, zero from cols up to the next multiple of 128) and scale bytes
+// (E8M0: byte s stands for 2^(s - 127)).  The scale bytes of four consecutive
+// groups of one row form a 32-bit word, and the words lie group-major:
+// byte (row, group g) at ((g / 4) * R4 + row) * 4 + g % 4, R4 = rows rounded up
+// to 4.  A tile of a product then reads the words of its rows as one contiguous
+// run per 512 columns, and the matrix instruction takes the byte as it is.
+#include <algorithm>
+
+#include "common.h"
+#include "gemm.h"
+
+namespace muon {
+namespace {
+
+typedef int i32x8_t __attribute__((ext_vector_type(8)));
+
+constexpr int kGroup = MUON_FP8_GROUP;   // columns under one scale
+
+inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+inline int64_t scale_rows(int64_t rows) { return ceil_div(rows, 4) * 4; }
+
+// ---------------------------------------------------------------------------
+// Quantiser
+// ---------------------------------------------------------------------------
+// amax = m 2^E (1 <= m < 2): the smallest e with amax <= MAX 2^e, MAX = 1.75 2^8
+// (e4m3) or 1.75 2^15 (e5m2), is E - 8 (or 15), plus one when m > 1.75.  In bits:
+// the biased exponent field less that, plus one when the fraction is over 0x600000.
+// The byte is held to 1 .. 254 so that its inverse 2^-e is a normal fp32.
+template <int FMT>
+__device__ __forceinline__ uint32_t scale_byte(uint32_t amax_bits) {
+  constexpr int drop = FMT == MUON_FP8_E4M3 ? 8 : 15;
+  if (amax_bits == 0) return 127;
+  const int b = int(amax_bits >> 23) - drop + ((amax_bits & 0x7fffffu) > 0x600000u ? 1 : 0);
+  return uint32_t(b < 1 ? 1 : b);
+}
+__device__ __forceinline__ float inverse_scale(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }
+
+// |x| as bits, 0 for infinities and NaN: they take no part in a group's scale
+__device__ __forceinline__ uint32_t finite_abs_bits(float x) {
+  const uint32_t u = __float_as_uint(x) & 0x7fffffffu;
+  return u < 0x7f800000u ? u : 0u;
+}
+
+__device__ __forceinline__ uint32_t max_u32(uint32_t a, uint32_t b) { return a > b ? a : b; }
+
+// maximum over the 16 lanes of a DPP row, in every lane (rotations by 8, 4, 2, 1)
+__device__ __forceinline__ uint32_t row16_max(uint32_t v) {
+  v = max_u32(v, uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x128, 0xf, 0xf, true)));
+  v = max_u32(v, uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x124, 0xf, 0xf, true)));
+  v = max_u32(v, uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x122, 0xf, 0xf, true)));
+  v = max_u32(v, uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x121, 0xf, 0xf, true)));
+  return v;
+}
+
+// Four codes of x 2^-e in one word.  The product with a power of two is exact (or
+// far below the format's smallest step), so each entry is rounded once, to
+// nearest even, by the conversion.  e4m3 has no infinity: an infinite entry
+// becomes NaN there, as NaN does.
+template <int FMT>
+__device__ __forceinline__ uint32_t pack4(float a, float b, float c, float d) {
+  if (FMT == MUON_FP8_E4M3) {
+    const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+    return uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(c, d, lo, true));
+  }
+  const int lo = __builtin_amdgcn_cvt_pk_bf8_f32(a, b, 0, false);
+  return uint32_t(__builtin_amdgcn_cvt_pk_bf8_f32(c, d, lo, true));
+}
+
+struct QuantArgs {
+  const void* x;
+  int64_t rows, cols, ldx;
+  uint8_t *q, *s, *qt, *st;   // q/s or qt/st may be null
+  int64_t ldq, ldqt;
+  int vec;                    // rows of x can be read 8 entries at a time
+};
+
+// One workgroup per 128 x 128 tile, read once: each thread holds an 8 x 8 block
+// (rows 8 (t / 16) .., columns 8 (t % 16) ..), so that row groups, column groups
+// and the whole tile's maximum all come from registers (16 lanes of one wave share
+// a row; columns meet in 2 KB of LDS), and the transposed codes leave through a
+// 16 KB tile of LDS whose 8-byte chunks are XOR-swizzled.  Bound by memory: 2 (bf16)
+// or 4 bytes read and 1 or 2 written per entry.
+template <typename T, int FMT, bool BLOCK>
+__global__ __launch_bounds__(256) void fp8_quantize_kernel(QuantArgs g) {
+  __shared__ __attribute__((aligned(16))) char tile[128 * 128];
+  __shared__ uint32_t colmax[4][128];
+  const int t = threadIdx.x, cg = t & 15, rg = t >> 4, wave = t >> 6;
+  const int64_t kb = blockIdx.x, rb = blockIdx.y;
+  const int64_t c0 = kb * 128 + 8 * cg, r0 = rb * 128 + 8 * rg;
+  float v[8][8];
+#pragma unroll
+  for (int p = 0; p < 8; ++p) {
+    const T* src = static_cast<const T*>(g.x) + (r0 + p) * g.ldx + c0;
+    if (r0 + p < g.rows && c0 + 8 <= g.cols && g.vec) {
+      Vec8<T>::load(src, v[p]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[p][j] = (r0 + p < g.rows && c0 + j < g.cols) ? to_f32(src[j]) : 0.0f;
+    }
+  }
+  const bool rows_out = g.q != nullptr, cols_out = g.qt != nullptr;
+  uint32_t all = 0;
+  if (BLOCK) {
+#pragma unroll
+    for (int p = 0; p < 8; ++p)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) all = max_u32(all, finite_abs_bits(v[p][j]));
+    all = row16_max(all);
+    all = max_u32(all, uint32_t(__shfl_xor(int(all), 16, kWave)));
+    all = max_u32(all, uint32_t(__shfl_xor(int(all), 32, kWave)));
+    if ((t & 63) == 0) colmax[wave][0] = all;
+    __syncthreads();
+    all = max_u32(max_u32(colmax[0][0], colmax[1][0]), max_u32(colmax[2][0], colmax[3][0]));
+  }
+  const int64_t kbs = (g.cols + 127) / 128, rbs = (g.rows + 127) / 128;
+  if (rows_out) {
+    const int64_t R4 = (g.rows + 3) / 4 * 4;
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+      uint32_t m = all;
+      if (!BLOCK) {
+        m = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) m = max_u32(m, finite_abs_bits(v[p][j]));
+        m = row16_max(m);
+      }
+      const uint32_t byte = scale_byte<FMT>(m);
+      const float inv = inverse_scale(byte);
+      const int64_t r = r0 + p;
+      if (r < g.rows) {
+        const uint2 w = make_uint2(pack4<FMT>(v[p][0] * inv, v[p][1] * inv, v[p][2] * inv, v[p][3] * inv),
+                                   pack4<FMT>(v[p][4] * inv, v[p][5] * inv, v[p][6] * inv, v[p][7] * inv));
+        *reinterpret_cast<uint2*>(g.q + r * g.ldq + c0) = w;
+      }
+      if (cg == 0 && r < R4) {
+        uint8_t* dst = g.s + ((kb >> 2) * R4 + r) * 4;
+        dst[kb & 3] = r < g.rows ? byte : 127;
+        if (kb == kbs - 1)   // the last word's unused bytes
+          for (int64_t f = (kb & 3) + 1; f < 4; ++f) dst[f] = 127;
+      }
+    }
+  }
+  if (!cols_out) return;
+  uint32_t m[8];
+  if (!BLOCK) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      uint32_t c = 0;
+#pragma unroll
+      for (int p = 0; p < 8; ++p) c = max_u32(c, finite_abs_bits(v[p][j]));
+      c = max_u32(c, uint32_t(__shfl_xor(int(c), 16, kWave)));
+      c = max_u32(c, uint32_t(__shfl_xor(int(c), 32, kWave)));
+      if ((t & 63) < 16) colmax[wave][8 * cg + j] = c;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      m[j] = max_u32(max_u32(colmax[0][8 * cg + j], colmax[1][8 * cg + j]),
+                     max_u32(colmax[2][8 * cg + j], colmax[3][8 * cg + j]));
+  }
+  const int64_t C4 = (g.cols + 3) / 4 * 4;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const uint32_t byte = scale_byte<FMT>(BLOCK ? all : m[j]);
+    const float inv = inverse_scale(byte);
+    const uint2 w = make_uint2(pack4<FMT>(v[0][j] * inv, v[1][j] * inv, v[2][j] * inv, v[3][j] * inv),
+                               pack4<FMT>(v[4][j] * inv, v[5][j] * inv, v[6][j] * inv, v[7][j] * inv));
+    *reinterpret_cast<uint2*>(tile + (8 * cg + j) * 128 + ((rg ^ cg) << 3)) = w;
+    const int64_t c = c0 + j;
+    if (rg == 0 && c < C4) {
+      uint8_t* dst = g.st + ((rb >> 2) * C4 + c) * 4;
+      dst[rb & 3] = c < g.cols ? byte : 127;
+      if (rb == rbs - 1)
+        for (int64_t f = (rb & 3) + 1; f < 4; ++f) dst[f] = 127;
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int h = 0; h < 4; ++h) {
+    const int c = (t >> 3) + 32 * h, ch = 2 * (t & 7), sw = (c >> 3) & 15;
+    if (kb * 128 + c < g.cols) {
+      const uint2 a = *reinterpret_cast<const uint2*>(tile + c * 128 + ((ch ^ sw) << 3));
+      const uint2 b = *reinterpret_cast<const uint2*>(tile + c * 128 + (((ch + 1) ^ sw) << 3));
+      *reinterpret_cast<uint4*>(g.qt + (kb * 128 + c) * g.ldqt + rb * 128 + 8 * ch) = make_uint4(a.x, a.y, b.x, b.y);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Product
+// ---------------------------------------------------------------------------
+struct Fp8GemmArgs {
+  const uint8_t *A, *B;     // codes: A [m][lda], B [n][ldb]
+  const uint8_t *sa, *sb;   // scale words
+  void* C;
+  int64_t m, n, K, lda, ldb, ldc;
+  int64_t ra4, rb4;         // rows of the scale arrays
+  float alpha, beta;
+  int vec;                  // rows of C can be written 4 entries at a time
+};
+
+// C[row][col .. col + 3] <- beta C + alpha acc, one rounding to the stored type
+template <typename TC>
+__device__ __forceinline__ void store4(const Fp8GemmArgs& g, int64_t row, int64_t col, const float acc[4]) {
+  TC* dst = static_cast<TC*>(g.C) + row * g.ldc + col;
+  if (g.vec && col + 4 <= g.n) {
+    float o[4];
+    if constexpr (sizeof(TC) == 2) {
+      if (g.beta != 0.0f) {
+        const uint2 z = *reinterpret_cast<const uint2*>(dst);
+        o[0] = fmaf(g.beta, __uint_as_float(z.x << 16), g.alpha * acc[0]);
+        o[1] = fmaf(g.beta, __uint_as_float(z.x & 0xffff0000u), g.alpha * acc[1]);
+        o[2] = fmaf(g.beta, __uint_as_float(z.y << 16), g.alpha * acc[2]);
+        o[3] = fmaf(g.beta, __uint_as_float(z.y & 0xffff0000u), g.alpha * acc[3]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = g.alpha * acc[i];
+      }
+      *reinterpret_cast<uint2*>(dst) =
+          make_uint2(uint32_t(f32_to_bf16(o[0])) | (uint32_t(f32_to_bf16(o[1])) << 16),
+                     uint32_t(f32_to_bf16(o[2])) | (uint32_t(f32_to_bf16(o[3])) << 16));
+    } else {
+      if (g.beta != 0.0f) {
+        const float4 z = *reinterpret_cast<const float4*>(dst);
+        o[0] = fmaf(g.beta, z.x, g.alpha * acc[0]);
+        o[1] = fmaf(g.beta, z.y, g.alpha * acc[1]);
+        o[2] = fmaf(g.beta, z.z, g.alpha * acc[2]);
+        o[3] = fmaf(g.beta, z.w, g.alpha * acc[3]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = g.alpha * acc[i];
+      }
+      *reinterpret_cast<float4*>(dst) = make_float4(o[0], o[1], o[2], o[3]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (col + i < g.n) {
+        float o = g.alpha * acc[i];
+        if (g.beta != 0.0f) o = fmaf(g.beta, to_f32(dst[i]), o);
+        dst[i] = from_f32<TC>(o);
+      }
+  }
+}
+
+// Two ways to multiply.  The fp8 matrix instructions (scaled or not) line up the
+// eight products of eight neighbouring k-values at the largest of them and drop
+// what lies more than 13 bits below it, before anything is added in fp32: measured
+// on MI355X, a Gaussian product is off by 1.5e-5 of its norm, against 2.5e-7 for
+// the bf16 instructions.  For a bf16 C that is a hundredth of its own rounding
+// (2^-9), and the fp8 instructions run at twice the bf16 rate, so they are used.  An
+// fp32 C (a momentum that gradients are summed into) keeps what fp32 holds: its
+// codes are widened to bf16 with their scale (v_cvt_scalef32_pk_bf16_*, exact) and
+// multiplied on the bf16 instructions.
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+
+// eight codes times their scale, as bf16 (exact: at most four significant bits)
+template <int FMT>
+__device__ __forceinline__ bf16x8_t widen8(uint32_t lo, uint32_t hi, float scale) {
+  uint32_t w[4];
+  if constexpr (FMT == MUON_FP8_E4M3) {
+    w[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, false));
+    w[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, true));
+    w[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, false));
+    w[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, true));
+  } else {
+    w[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(lo, scale, false));
+    w[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(lo, scale, true));
+    w[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(hi, scale, false));
+    w[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(hi, scale, true));
+  }
+  return __builtin_bit_cast(bf16x8_t, make_uint4(w[0], w[1], w[2], w[3]));
+}
+// 2^(s - 127) for the scale byte in the low bits of `word`
+__device__ __forceinline__ float scale_value(uint32_t word) { return __uint_as_float((word & 255u) << 23); }
+
+// Products straight from memory: no tile is staged, each wave reads 32 bytes per
+// lane of 16 rows of B and of MT x 16 rows of A and multiplies them on
+// v_mfma_scale_f32_16x16x128 (one instruction spans a whole group of 128, so the
+// group's scales go in with it), or widened on four v_mfma_f32_16x16x32_bf16.  The waves of a workgroup take the groups of the
+// contraction in turn and their sums meet in LDS, added in the order of the waves.
+// B is the first operand: a lane holds four consecutive columns of one row of C.
+template <int FA, typename TC, int MT>
+__global__ __launch_bounds__(1024) void fp8_gemm_direct_kernel(Fp8GemmArgs g) {
+  constexpr bool EXACT = sizeof(TC) == 4;
+  extern __shared__ __attribute__((aligned(16))) float red[];   // [waves][MT * 4][64]
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+  const int r = lane & 15, kq = lane >> 4;
+  const int64_t n0 = int64_t(blockIdx.x) * 16, m0 = int64_t(blockIdx.y) * (16 * MT);
+  const int64_t brow = min(n0 + r, g.n - 1);
+  const uint8_t* pb = g.B + brow * g.ldb + 32 * kq;
+  const uint8_t* psb = g.sb + brow * 4;
+  const uint8_t* pa[MT];
+  const uint8_t* psa[MT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i) {
+    const int64_t arow = min(m0 + 16 * i + r, g.m - 1);
+    pa[i] = g.A + arow * g.lda + 32 * kq;
+    psa[i] = g.sa + arow * 4;
+  }
+  f32x4_t acc[MT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i) acc[i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+  const int64_t groups = g.K / kGroup;
+  for (int64_t kb = wave; kb < groups; kb += waves) {
+    const i32x8_t fb = *reinterpret_cast<const i32x8_t*>(pb + kb * kGroup);
+    const int sb = psb[(kb >> 2) * g.rb4 * 4 + (kb & 3)];
+    bf16x8_t wb[4];
+    if constexpr (EXACT) {
+#pragma unroll
+      for (int h = 0; h < 4; ++h) wb[h] = widen8<MUON_FP8_E4M3>(fb[2 * h], fb[2 * h + 1], scale_value(sb));
+    }
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      const i32x8_t fa = *reinterpret_cast<const i32x8_t*>(pa[i] + kb * kGroup);
+      const int sa = psa[i][(kb >> 2) * g.ra4 * 4 + (kb & 3)];
+      if constexpr (EXACT) {
+#pragma unroll
+        for (int h = 0; h < 4; ++h)
+          acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+              wb[h], widen8<FA>(fa[2 * h], fa[2 * h + 1], scale_value(sa)), acc[i], 0, 0, 0);
+      } else {
+        acc[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fb, fa, acc[i], 0, FA, 0, sb, 0, sa);
+      }
+    }
+  }
+  if (waves > 1) {
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) red[((wave * MT + i) * 4 + v) * 64 + lane] = acc[i][v];
+    __syncthreads();
+    if (wave >= MT) return;
+  }
+  // wave i finishes row block i (a single wave finishes all)
+#pragma unroll
+  for (int i = 0; i < MT; ++i) {
+    if (waves > 1 && i % waves != wave) continue;
+    float o[4];
+#pragma unroll
+    for (int v = 0; v < 4; ++v) o[v] = acc[i][v];
+    if (waves > 1) {
+#pragma unroll
+      for (int v = 0; v < 4; ++v) o[v] = 0.0f;
+      for (int w = 0; w < waves; ++w)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) o[v] += red[((w * MT + i) * 4 + v) * 64 + lane];
+    }
+    const int64_t row = m0 + 16 * i + r, col = n0 + 4 * kq;
+    if (row < g.m && col < g.n) store4<TC>(g, row, col, o);
+  }
+}
+
+template <int FA, typename TC, int MT>
+int launch_direct(const Fp8GemmArgs& g, hipStream_t st) {
+  const int64_t groups = g.K / kGroup;
+  const int waves = int(std::max<int64_t>(1, std::min<int64_t>(groups, 8)));
+  const uint32_t lds = waves > 1 ? uint32_t(waves) * MT * 4 * 64 * 4 : 0;
+  const dim3 grid(ceil_div(g.n, 16), ceil_div(g.m, 16 * MT));
+  launch_kernel(fp8_gemm_direct_kernel<FA, TC, MT>, grid, dim3(64 * waves), lds, st, g);
+  return launch_status();
+}
+
+template <int FA, typename TC>
+int launch_product(const Fp8GemmArgs& g, hipStream_t st) {
+  if (g.m <= 16) return launch_direct<FA, TC, 1>(g, st);
+  if (g.m <= 32) return launch_direct<FA, TC, 2>(g, st);
+  return launch_direct<FA, TC, 4>(g, st);
+}
+
+bool valid_fmt(int f) { return f == MUON_FP8_E4M3 || f == MUON_FP8_E5M2; }
+
+}  // namespace
+}  // namespace muon
+
+using namespace muon;
+
+extern "C" {
+
+size_t fp8_scale_bytes(int64_t rows, int64_t cols) {
+  if (rows < 0 || cols < 0 || rows > MUON_FP8_MAX_SIDE || cols > MUON_FP8_MAX_SIDE) return 0;
+  return size_t(ceil_div(ceil_div(cols, kGroup), 4)) * size_t(scale_rows(rows)) * 4;
+}
+
+int fp8_quantize(const void* x, int x_dtype, int64_t rows, int64_t cols, int64_t ldx, int fmt, int block_rows,
+                 void* q, int64_t ldq, void* s, void* qt, int64_t ldqt, void* st, void* stream) {
+  if (rows < 0 || cols < 0 || rows > MUON_FP8_MAX_SIDE || cols > MUON_FP8_MAX_SIDE) return MUON_EINVAL;
+  if (block_rows != 1 && block_rows != kGroup) return MUON_EINVAL;
+  if (!valid_dtype(x_dtype) || !valid_fmt(fmt)) return MUON_EDTYPE;
+  if ((q == nullptr) != (s == nullptr) || (qt == nullptr) != (st == nullptr)) return MUON_EINVAL;
+  if (rows == 0 || cols == 0) return MUON_OK;
+  if (x == nullptr || (q == nullptr && qt == nullptr) || ldx < cols) return MUON_EINVAL;
+  if (q != nullptr && (ldq < ceil_div(cols, kGroup) * kGroup || ldq % 16 != 0)) return MUON_EINVAL;
+  if (qt != nullptr && (ldqt < ceil_div(rows, kGroup) * kGroup || ldqt % 16 != 0)) return MUON_EINVAL;
+  if (!aligned16(x) || !aligned16(q) || !aligned16(s) || !aligned16(qt) || !aligned16(st)) return MUON_EALIGN;
+  QuantArgs g{};
+  g.x = x; g.rows = rows; g.cols = cols; g.ldx = ldx;
+  g.q = static_cast<uint8_t*>(q); g.s = static_cast<uint8_t*>(s);
+  g.qt = static_cast<uint8_t*>(qt); g.st = static_cast<uint8_t*>(st);
+  g.ldq = ldq; g.ldqt = ldqt;
+  g.vec = ldx % 8 == 0;
+  const dim3 grid(ceil_div(cols, 128), ceil_div(rows, 128));
+  hipStream_t hs = static_cast<hipStream_t>(stream);
+  auto go = [&](auto t_c, auto f_c) {
+    using T = decltype(t_c);
+    constexpr int F = decltype(f_c)::value;
+    if (block_rows == 1) launch_kernel(fp8_quantize_kernel<T, F, false>, grid, dim3(256), 0, hs, g);
+    else launch_kernel(fp8_quantize_kernel<T, F, true>, grid, dim3(256), 0, hs, g);
+  };
+  using E4 = std::integral_constant<int, MUON_FP8_E4M3>;
+  using E5 = std::integral_constant<int, MUON_FP8_E5M2>;
+  if (x_dtype == MUON_F32) fmt == MUON_FP8_E4M3 ? go(float{}, E4{}) : go(float{}, E5{});
+  else fmt == MUON_FP8_E4M3 ? go(bf16_t{}, E4{}) : go(bf16_t{}, E5{});
+  return launch_status();
+}
+
+size_t fp8_gemm_workspace_bytes(int64_t m, int64_t n, int64_t K) {
+  (void)m; (void)n; (void)K;
+  return 0;
+}
+
+int fp8_gemm(const void* A, int a_fmt, int64_t lda, const void* sa, const void* B, int b_fmt, int64_t ldb,
+             const void* sb, void* C, int c_dtype, int64_t ldc, int64_t m, int64_t n, int64_t K, float alpha,
+             float beta, void* workspace, size_t ws_bytes, void* stream) {
+  if (m < 0 || n < 0 || K < 0 || m > MUON_FP8_MAX_SIDE || n > MUON_FP8_MAX_SIDE || K > MUON_FP8_MAX_SIDE)
+    return MUON_EINVAL;
+  if (K % kGroup != 0) return MUON_EINVAL;
+  if (!valid_fmt(a_fmt) || b_fmt != MUON_FP8_E4M3 || !valid_dtype(c_dtype)) return MUON_EDTYPE;
+  if (m == 0 || n == 0) return MUON_OK;
+  if (C == nullptr || ldc < n) return MUON_EINVAL;
+  if (K > 0 && (A == nullptr || B == nullptr || sa == nullptr || sb == nullptr)) return MUON_EINVAL;
+  if (lda < K || ldb < K || lda % 16 != 0 || ldb % 16 != 0) return MUON_EINVAL;
+  if (!aligned16(A) || !aligned16(B) || !aligned16(sa) || !aligned16(sb) || !aligned16(C)) return MUON_EALIGN;
+  const size_t need = fp8_gemm_workspace_bytes(m, n, K);
+  if (need > 0 && (workspace == nullptr || ws_bytes < need)) return MUON_EWORKSPACE;
+  if (need > 0 && !aligned16(workspace)) return MUON_EALIGN;
+  Fp8GemmArgs g{};
+  g.A = static_cast<const uint8_t*>(A); g.B = static_cast<const uint8_t*>(B);
+  g.sa = static_cast<const uint8_t*>(sa); g.sb = static_cast<const uint8_t*>(sb);
+  g.C = C; g.m = m; g.n = n; g.K = K; g.lda = lda; g.ldb = ldb; g.ldc = ldc;
+  g.ra4 = scale_rows(m); g.rb4 = scale_rows(n);
+  g.alpha = alpha; g.beta = beta;
+  g.vec = ldc % 4 == 0;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  if (a_fmt == MUON_FP8_E4M3)
+    return c_dtype == MUON_F32 ? launch_product<0, float>(g, st) : launch_product<0, bf16_t>(g, st);
+  return c_dtype == MUON_F32 ? launch_product<1, float>(g, st) : launch_product<1, bf16_t>(g, st);
+}
+
+}  // extern "C"
