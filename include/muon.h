@@ -551,6 +551,67 @@ int fp8_gemm(const void* A, int a_fmt, int64_t lda, const void* sa, const void* 
              const void* sb, void* C, int c_dtype, int64_t ldc, int64_t m, int64_t n, int64_t K, float alpha,
              float beta, void* workspace, size_t ws_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Newton-Schulz orthogonalisation of many small blocks: the heads of attention
+ * projections, each orthogonalised by itself, with the plain Muon update.
+ * Complements ns_orthogonalize, which pads both sides to MUON_NS_PAD and wants
+ * contiguous matrices: here a block's short side is 1 .. MUON_BLOCKS_MAX_SHORT,
+ * nothing is padded in memory, and rows have a pitch.
+ *
+ * A problem is `count` blocks of rows x cols; block i of M starts stride_m * i
+ * entries after M and has rows ld_m entries apart (out likewise).  Heads along
+ * the rows of a projection W [H d][D] are blocks d x D with ld = D, stride =
+ * d D; heads along its columns W [D][H d] are blocks D x d with ld = H d,
+ * stride = d.
+ *
+ * Per block: X0 = M / |M|_F (a block of zeros gives zeros), then `steps` times
+ * X <- a X + (b A + c A A) X, A = X X^T on the short side; U = X.
+ *   ns_blocks         out = U (F32 or BF16)
+ *   ns_blocks_update  out <- (1 - eta decay) out - eta scale U, the decoupled
+ *                     weight decay and the step in one pass (out = W)
+ * M is F32 or BF16 and read only.  The iterations run on T with U = T M, in
+ * fp32 (polynomials of A commute, so the long side is read only twice); U is
+ * rounded once, to the type of out.  Sums of squares must lie within fp32's
+ * normal range.  NaN or infinity in a block make that block's U NaN.
+ *
+ *   workspace  ns_blocks_workspace_bytes(probs, nprobs) bytes, 16-byte
+ *              aligned; contents on entry do not matter.  Calls that share one
+ *              must not overlap in time.  The query returns 0 for a problem
+ *              list that the calls refuse.
+ *   Blocks of one call must not overlap each other in out, nor out the M of
+ *   another block.
+ * At most MUON_BLOCKS_MAX_PROBLEMS problems, MUON_BLOCKS_MAX_COUNT blocks each,
+ * long sides up to MUON_BLOCKS_MAX_LONG, strides positive where count > 1, ld
+ * at least cols, and under 2^31 units of 64 long-side entries over all blocks
+ * (MUON_EINVAL).  M and out 16-byte aligned; blocks whose pitch or stride is
+ * not a multiple of 16 bytes are read entry by entry.  Empty problems (count,
+ * rows or cols 0) are skipped.
+ * ------------------------------------------------------------------------- */
+#define MUON_BLOCKS_MAX_SHORT 128
+#define MUON_BLOCKS_MAX_LONG (1 << 24)
+#define MUON_BLOCKS_MAX_COUNT (1 << 20)
+#define MUON_BLOCKS_MAX_PROBLEMS 512
+
+typedef struct muon_block_problem {
+  const void* M;
+  void* out;
+  int64_t rows;
+  int64_t cols;
+  int64_t count;
+  int64_t ld_m;
+  int64_t stride_m;
+  int64_t ld_out;
+  int64_t stride_out;
+  int32_t m_dtype;
+  int32_t out_dtype;
+} muon_block_problem;
+
+size_t ns_blocks_workspace_bytes(const muon_block_problem* probs, int nprobs);
+int ns_blocks(const muon_block_problem* probs, int nprobs, float a, float b, float c, int steps, void* workspace,
+              size_t ws_bytes, void* stream);
+int ns_blocks_update(const muon_block_problem* probs, int nprobs, float a, float b, float c, int steps, float eta,
+                     float decay, float scale, void* workspace, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -19,3 +19,5 @@ from ._abi import muon_momentum_noalloc, time_next_launch  # noqa: F401
 from .signmuon import SignMuonStep  # noqa: F401
 from ._abi import MUON_FP8_GROUP, MUON_FP8_MAX_SIDE, fp8_buffers, fp8_gemm, fp8_gemm_workspace_bytes  # noqa: F401
 from ._abi import fp8_quantize, fp8_scale_shape  # noqa: F401
+from ._abi import MUON_BLOCKS_MAX_SHORT, PreparedNSBlocks, ns_blocks, ns_blocks_update  # noqa: F401
+from ._abi import ns_blocks_workspace_bytes  # noqa: F401

@@ -92,6 +92,10 @@ SIGNATURES = {
     "fp8_gemm": (_c_int, [_c_void_p, _c_int, _c_i64, _c_void_p, _c_void_p, _c_int, _c_i64, _c_void_p, _c_void_p,
                           _c_int, _c_i64, _c_i64, _c_i64, _c_i64, _c_float, _c_float, _c_void_p, _c_size,
                           _c_void_p]),
+    "ns_blocks_workspace_bytes": (_c_size, [_c_void_p, _c_int]),
+    "ns_blocks": (_c_int, [_c_void_p, _c_int, _c_float, _c_float, _c_float, _c_int, _c_void_p, _c_size, _c_void_p]),
+    "ns_blocks_update": (_c_int, [_c_void_p, _c_int, _c_float, _c_float, _c_float, _c_int, _c_float, _c_float,
+                                  _c_float, _c_void_p, _c_size, _c_void_p]),
 }
 
 _LIB: Optional[ctypes.CDLL] = None
@@ -660,3 +664,86 @@ def fp8_gemm(A: torch.Tensor, sa: torch.Tensor, B: torch.Tensor, sb: torch.Tenso
         ws, nbytes = _dev(workspace, "workspace"), workspace.numel() * workspace.element_size()
     _check("fp8_gemm", lib().fp8_gemm(ap, _FP8[A.dtype], lda, sap, bp, _FP8[B.dtype], ldb, sbp, cp, dtype_code(C),
                                       max(ldc, n), m, n, K, float(alpha), float(beta), ws, nbytes, _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
+# Newton-Schulz on many small blocks (attention heads)
+# ---------------------------------------------------------------------------
+
+MUON_BLOCKS_MAX_SHORT = 128
+
+
+class BlockProblem(ctypes.Structure):
+    """Mirror of ``struct muon_block_problem``."""
+
+    _fields_ = [("M", _c_void_p), ("out", _c_void_p), ("rows", _c_i64), ("cols", _c_i64), ("count", _c_i64),
+                ("ld_m", _c_i64), ("stride_m", _c_i64), ("ld_out", _c_i64), ("stride_out", _c_i64),
+                ("m_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32)]
+
+
+def _block_view(t: torch.Tensor, name: str):
+    """(pointer, count, rows, cols, row pitch, block stride) of a 2-D or 3-D view with contiguous rows."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if t.dim() == 2:
+        t = t.unsqueeze(0)
+    if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1):
+        raise ValueError(f"{name} must be [count, rows, cols] (or [rows, cols]) with contiguous rows")
+    count, rows, cols = t.shape
+    return t.data_ptr(), count, rows, cols, t.stride(1) if rows > 1 else max(cols, 1), t.stride(0) if count > 1 else 0
+
+
+def _block_problems(problems):
+    arr = (BlockProblem * len(problems))()
+    for i, (M, out) in enumerate(problems):
+        if M.shape != out.shape:
+            raise ValueError("each problem needs an M and an output of the same shape")
+        mp, count, rows, cols, ld_m, stride_m = _block_view(M, "M")
+        op, _, _, _, ld_o, stride_o = _block_view(out, "out")
+        arr[i] = BlockProblem(mp, op, rows, cols, count, ld_m, stride_m, ld_o, stride_o, dtype_code(M), dtype_code(out))
+    return arr
+
+
+def ns_blocks_workspace_bytes(problems) -> int:
+    arr = _block_problems(problems)
+    return int(lib().ns_blocks_workspace_bytes(ctypes.cast(arr, _c_void_p), len(problems)))
+
+
+class PreparedNSBlocks:
+    """One ns_blocks or ns_blocks_update call whose problem array is marshalled once.
+
+    ``problems``: (M, out) pairs of strided views [count, rows, cols] (or [rows, cols]).  Without
+    ``eta`` the directions are written to ``out``; with it ``out <- (1 - eta decay) out - eta scale U``.
+    Calling the object only enqueues the work, on ``stream`` (default: the current one)."""
+
+    def __init__(self, problems, a: float, b: float, c: float, steps: int, eta: Optional[float] = None,
+                 decay: float = 0.0, scale: float = 1.0, workspace: Optional[torch.Tensor] = None):
+        if len(problems) == 0:
+            raise ValueError("no problems")
+        self._problems = list(problems)     # keeps the tensors alive
+        self._arr = _block_problems(self._problems)
+        self._ptr = ctypes.cast(self._arr, _c_void_p)
+        need = int(lib().ns_blocks_workspace_bytes(self._ptr, len(self._problems)))
+        self.workspace = _workspace(need, self._problems[0][0], workspace)
+        self._name = "ns_blocks" if eta is None else "ns_blocks_update"
+        self._fn = getattr(lib(), self._name)
+        extra = () if eta is None else (float(eta), float(decay), float(scale))
+        self._args = (self._ptr, len(self._problems), float(a), float(b), float(c), int(steps), *extra,
+                      _dev(self.workspace, "workspace"), self.workspace.numel() * self.workspace.element_size())
+
+    def __call__(self, stream=None) -> None:
+        _check(self._name, self._fn(*self._args, _stream(stream)))
+
+
+def ns_blocks(problems, a: float, b: float, c: float, steps: int, workspace: Optional[torch.Tensor] = None,
+              stream=None) -> None:
+    """Newton-Schulz directions of every block of every (M, U) problem, each block by itself."""
+    if len(problems) > 0:
+        PreparedNSBlocks(problems, a, b, c, steps, workspace=workspace)(stream)
+
+
+def ns_blocks_update(problems, a: float, b: float, c: float, steps: int, eta: float, decay: float = 0.0,
+                     scale: float = 1.0, workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    """``W <- (1 - eta decay) W - eta scale U`` for every block of every (M, W) problem, U as in ns_blocks."""
+    if len(problems) > 0:
+        PreparedNSBlocks(problems, a, b, c, steps, eta, decay, scale, workspace)(stream)
