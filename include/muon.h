@@ -526,7 +526,7 @@ int dion_step(const muon_dion_problem* probs, int count, int rank, float mu, flo
  *               drop, of eight neighbouring products, what lies more than 13
  *               bits below the largest (1.5e-5 of a Gaussian product's norm,
  *               against bf16's own 2^-9).  With beta = 0, C is not read.
- *               K = 0 gives beta C.
+ *               K = 0 gives beta C.  lda and ldb are under 2^24.
  *               Uses: y = x W^T (A = x, B = W); dx = dy W (A = dy, B = W^T
  *               from qt); the weight gradient straight into the momentum,
  *               M <- beta M + alpha dy^T x (A = dy^T, B = x^T, both from qt).

@@ -18,6 +18,17 @@ namespace {
 
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
 
+// 32 bytes of a matrix operand from two 16-byte reads
+__device__ __forceinline__ i32x8_t join(const u32x4_t (&v)[2]) {
+  i32x8_t r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    r[i] = int(v[0][i]);
+    r[4 + i] = int(v[1][i]);
+  }
+  return r;
+}
+
 constexpr int kGroup = MUON_FP8_GROUP;   // columns under one scale
 
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -365,12 +376,256 @@ int launch_direct(const Fp8GemmArgs& g, hipStream_t st) {
   return launch_status();
 }
 
+// Tiled product.  A workgroup of four waves computes BM x BN of C.  Both operands
+// come through a ring of S stages in LDS, each 64 k-values (half a group) of every
+// row: 64-byte rows of four 16-byte chunks, chunk c of row r at slot
+// c ^ ((r / 4) % 4), filled by global -> LDS DMA (16 bytes per lane), followed by the
+// rows' scale words (4 bytes per lane).  A lane's operand is 32 bytes of one row: chunks
+// h and 2 + h for half-wave h, the same k-values for both operands, so their order
+// does not matter.  Per step: wait until this wave's copies of the next stage have
+// landed, s_barrier (everybody's have, and everybody is done with the stage before),
+// start the copy S - 1 steps ahead, read the next operands, multiply the current ones.
+template <int BM_, int BN_, int WM_, int WN_, int S_>
+struct Fp8Tile {
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, S = S_;
+  static constexpr int W = (BM / WM) * (BN / WN), NT = W * kWave;
+  static constexpr int FM = WM / 32, FN = WN / 32;
+  static constexpr int A_BYTES = BM * 64, B_BYTES = BN * 64;
+  static constexpr int STAGE = A_BYTES + B_BYTES + (BM + BN) * 4;
+  static constexpr int LDS_BYTES = S * STAGE;
+  static constexpr int A_DMA = A_BYTES / 1024 / W, B_DMA = B_BYTES / 1024 / W, S_DMA = (BM + BN) / 64 / W;
+  static constexpr int D = A_DMA + B_DMA + S_DMA;   // DMA instructions per wave and stage
+  static_assert(A_BYTES % (1024 * W) == 0 && B_BYTES % (1024 * W) == 0 && (BM + BN) % (64 * W) == 0, "DMA split");
+  static_assert(BM % 64 == 0, "one DMA of scale words lies in one operand");
+  static_assert(S >= 3 && D * (S - 2) <= 63 && LDS_BYTES <= 160 * 1024, "ring");
+};
+
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+// 4 bytes per lane to LDS bytes [lds_addr + 4 * lane), as gemm::dma16
+__device__ __forceinline__ void dma4(const void* g, uint32_t lds_addr) {
+  asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dword %0, off" ::"v"(g),
+               "s"(__builtin_amdgcn_readfirstlane(lds_addr))
+               : "memory", "m0");
+}
+#pragma clang diagnostic pop
+
+// This wave's copies but the last N have landed and all its LDS reads are done (those
+// were issued a whole step earlier), then all waves meet: what lands next may
+// overwrite the stage that was read before.
+template <int N>
+__device__ __forceinline__ void ring_barrier() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
+constexpr int kGroupRows = 8;   // tile rows walked together, column by column
+
+template <int FA, typename TC, int BM, int BN, int WM, int WN, int S>
+__global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void fp8_gemm_tile_kernel(Fp8GemmArgs g) {
+  using C_ = Fp8Tile<BM, BN, WM, WN, S>;
+  constexpr bool EXACT = sizeof(TC) == 4;
+  constexpr int FM = C_::FM, FN = C_::FN;
+  extern __shared__ __attribute__((aligned(1024))) char lds[];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int fr = lane & 31, h = lane >> 5;
+  const int wm0 = (wave / (BN / WN)) * WM, wn0 = (wave % (BN / WN)) * WN;
+  const int64_t TM = (g.m + BM - 1) / BM, TN = (g.n + BN - 1) / BN;
+  int64_t tm, tn;
+  {
+    const int64_t t = gemm::xcd_remap(blockIdx.x, gridDim.x);
+    const int64_t per = int64_t(kGroupRows) * TN, first = (t / per) * kGroupRows;
+    const int64_t size = min(TM - first, int64_t(kGroupRows)), r = t % per;
+    tm = __builtin_amdgcn_readfirstlane(int(first + r % size));
+    tn = __builtin_amdgcn_readfirstlane(int(r / size));
+  }
+  const int64_t m0 = tm * BM, n0 = tn * BN;
+  // rows past the matrix read its last row; what they compute is not stored
+  const int mlast = int(min(g.m - 1 - m0, int64_t(BM - 1))), nlast = int(min(g.n - 1 - n0, int64_t(BN - 1)));
+  const uint8_t* At = g.A + m0 * g.lda;
+  const uint8_t* Bt = g.B + n0 * g.ldb;
+  uint32_t a_off[C_::A_DMA], b_off[C_::B_DMA];
+#pragma unroll
+  for (int i = 0; i < C_::A_DMA; ++i) {
+    const int r = 16 * (wave * C_::A_DMA + i) + (lane >> 2);
+    a_off[i] = uint32_t(min(r, mlast)) * uint32_t(g.lda) + (((lane & 3) ^ ((r >> 2) & 3)) << 4);
+  }
+#pragma unroll
+  for (int i = 0; i < C_::B_DMA; ++i) {
+    const int r = 16 * (wave * C_::B_DMA + i) + (lane >> 2);
+    b_off[i] = uint32_t(min(r, nlast)) * uint32_t(g.ldb) + (((lane & 3) ^ ((r >> 2) & 3)) << 4);
+  }
+  // scale words: 64 rows per DMA, of A for the first BM / 64 of them
+  const uint8_t* s_src[C_::S_DMA];
+  int64_t s_step[C_::S_DMA];
+#pragma unroll
+  for (int i = 0; i < C_::S_DMA; ++i) {
+    const int r = 64 * (wave * C_::S_DMA + i);
+    const bool of_a = r < BM;
+    const int row = of_a ? min(r + lane, mlast) : min(r - BM + lane, nlast);
+    s_src[i] = of_a ? g.sa + (m0 + row) * 4 : g.sb + (n0 + row) * 4;
+    s_step[i] = (of_a ? g.ra4 : g.rb4) * 4;
+  }
+  const uint32_t lds_base =
+      static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char*)lds));
+  auto issue = [&](int kt, uint32_t off) {
+    const uint32_t st = lds_base + off;
+    const uint8_t* ak = At + int64_t(kt) * 64;
+    const uint8_t* bk = Bt + int64_t(kt) * 64;
+#pragma unroll
+    for (int q = 0; q < C_::A_DMA; ++q) gemm::dma16(ak + a_off[q], st + (wave * C_::A_DMA + q) * 1024);
+#pragma unroll
+    for (int q = 0; q < C_::B_DMA; ++q) gemm::dma16(bk + b_off[q], st + C_::A_BYTES + (wave * C_::B_DMA + q) * 1024);
+#pragma unroll
+    for (int q = 0; q < C_::S_DMA; ++q)
+      dma4(s_src[q] + (kt >> 3) * s_step[q], st + C_::A_BYTES + C_::B_BYTES + (wave * C_::S_DMA + q) * 256);
+  };
+  auto ring_next = [](uint32_t o) {
+    o += C_::STAGE;
+    return o == uint32_t(S * C_::STAGE) ? 0u : o;
+  };
+  struct Frags {
+    u32x4_t a[FM][2], b[FN][2];
+    uint32_t sa[FM], sb[FN];
+  };
+  auto read = [&](const char* st, Frags& f) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+        f.b[j][c] = *reinterpret_cast<const u32x4_t*>(st + C_::A_BYTES + gemm::krow_off(wn0 + 32 * j + fr, 2 * c + h));
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+        f.a[i][c] = *reinterpret_cast<const u32x4_t*>(st + gemm::krow_off(wm0 + 32 * i + fr, 2 * c + h));
+    const char* sc = st + C_::A_BYTES + C_::B_BYTES;
+#pragma unroll
+    for (int i = 0; i < FM; ++i) f.sa[i] = *reinterpret_cast<const uint32_t*>(sc + (wm0 + 32 * i + fr) * 4);
+#pragma unroll
+    for (int j = 0; j < FN; ++j) f.sb[j] = *reinterpret_cast<const uint32_t*>(sc + (BM + wn0 + 32 * j + fr) * 4);
+  };
+  f32x16_t acc[FM][FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
+  auto mma = [&](int kt, const Frags& f) __attribute__((always_inline)) {
+    const int sh = 8 * ((kt >> 1) & 3);   // this group's byte of the scale words
+    if constexpr (EXACT) {
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        bf16x8_t wa[FM], wb[FN];
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+          wa[i] = widen8<FA>(f.a[i][p >> 1][2 * (p & 1)], f.a[i][p >> 1][2 * (p & 1) + 1], scale_value(f.sa[i] >> sh));
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+          wb[j] = widen8<MUON_FP8_E4M3>(f.b[j][p >> 1][2 * (p & 1)], f.b[j][p >> 1][2 * (p & 1) + 1],
+                                        scale_value(f.sb[j] >> sh));
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+          for (int j = 0; j < FN; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wb[j], wa[i], acc[i][j], 0, 0, 0);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+              join(f.b[j]), join(f.a[i]), acc[i][j], 0, FA, 0, int(f.sb[j] >> sh), 0, int(f.sa[i] >> sh));
+    }
+  };
+  // 64-value steps: an even number, at least two
+  const int nk = __builtin_amdgcn_readfirstlane(int(g.K / 64));
+#pragma unroll
+  for (int s = 0; s < S - 1; ++s)
+    if (s < nk) issue(s, uint32_t(s) * C_::STAGE);
+  if (nk >= S - 1) ring_barrier<C_::D * (S - 2)>();
+  else ring_barrier<0>();
+  Frags f0, f1;
+  read(lds, f0);
+  uint32_t o_cur = 0, o_iss = uint32_t(S - 1) * C_::STAGE;
+  int it = 0;
+  auto steady = [&](Frags& cur, Frags& nxt) __attribute__((always_inline)) {
+    const uint32_t o_nxt = ring_next(o_cur);
+    ring_barrier<C_::D * (S - 3)>();
+    issue(it + S - 1, o_iss);
+    read(lds + o_nxt, nxt);
+    mma(it, cur);
+    o_cur = o_nxt;
+    o_iss = ring_next(o_iss);
+    ++it;
+  };
+  auto drain = [&](Frags& cur, Frags& nxt) __attribute__((always_inline)) {
+    const uint32_t o_nxt = ring_next(o_cur);
+    if (it + 1 < nk) {
+      ring_barrier<0>();
+      read(lds + o_nxt, nxt);
+    }
+    mma(it, cur);
+    o_cur = o_nxt;
+    ++it;
+  };
+  while (it + S < nk) {   // two steps that both still copy a stage
+    steady(f0, f1);
+    steady(f1, f0);
+  }
+  if (it + S - 1 < nk) {
+    // one more copy is due: this step and the one after it
+    steady(f0, f1);
+    drain(f1, f0);
+  }
+  while (it < nk) {
+    drain(f0, f1);
+    drain(f1, f0);
+  }
+  // accumulator v of a lane: column 8 (v / 4) + 4 h + v % 4 of B's block, row fr of A's
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
+    const int64_t row = m0 + wm0 + 32 * i + fr;
+    if (row >= g.m) continue;
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int64_t col = n0 + wn0 + 32 * j + 8 * q + 4 * h;
+        const float v[4] = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+        if (col < g.n) store4<TC>(g, row, col, v);
+      }
+  }
+}
+
+template <int FA, typename TC, int BM, int BN, int WM, int WN, int S>
+int launch_tile(const Fp8GemmArgs& g, hipStream_t st) {
+  using C_ = Fp8Tile<BM, BN, WM, WN, S>;
+  auto kern = fp8_gemm_tile_kernel<FA, TC, BM, BN, WM, WN, S>;
+  static std::atomic<uint64_t> configured{0};   // devices with the LDS limit set
+  if (gemm::set_lds_limit(kern, C_::LDS_BYTES, configured) != MUON_OK) return MUON_ELAUNCH;
+  const int64_t tiles = ceil_div(g.m, BM) * ceil_div(g.n, BN);
+  if (tiles > INT32_MAX) return MUON_EINVAL;
+  launch_kernel(kern, dim3(tiles), dim3(C_::NT), C_::LDS_BYTES, st, g);
+  return launch_status();
+}
+
 template <int FA, typename TC>
 int launch_product(const Fp8GemmArgs& g, hipStream_t st) {
+  if (g.K > 0 && g.m > 64) {
+    // 256 x 256 tiles where they fill at least half of the CUs, else 128 x 128
+    const int64_t big = ceil_div(g.m, 256) * ceil_div(g.n, 256);
+    if (2 * big >= gemm::device_cus()) return launch_tile<FA, TC, 256, 256, 128, 128, 4>(g, st);
+    return launch_tile<FA, TC, 128, 128, 64, 64, 4>(g, st);
+  }
   if (g.m <= 16) return launch_direct<FA, TC, 1>(g, st);
   if (g.m <= 32) return launch_direct<FA, TC, 2>(g, st);
   return launch_direct<FA, TC, 4>(g, st);
 }
+
+// the tiles address their 256 rows with 32-bit offsets
+constexpr int64_t kMaxPitch = (int64_t(1) << 24) - 16;
 
 bool valid_fmt(int f) { return f == MUON_FP8_E4M3 || f == MUON_FP8_E5M2; }
 
@@ -433,7 +688,7 @@ int fp8_gemm(const void* A, int a_fmt, int64_t lda, const void* sa, const void* 
   if (m == 0 || n == 0) return MUON_OK;
   if (C == nullptr || ldc < n) return MUON_EINVAL;
   if (K > 0 && (A == nullptr || B == nullptr || sa == nullptr || sb == nullptr)) return MUON_EINVAL;
-  if (lda < K || ldb < K || lda % 16 != 0 || ldb % 16 != 0) return MUON_EINVAL;
+  if (lda < K || ldb < K || lda % 16 != 0 || ldb % 16 != 0 || lda > kMaxPitch || ldb > kMaxPitch) return MUON_EINVAL;
   if (!aligned16(A) || !aligned16(B) || !aligned16(sa) || !aligned16(sb) || !aligned16(C)) return MUON_EALIGN;
   const size_t need = fp8_gemm_workspace_bytes(m, n, K);
   if (need > 0 && (workspace == nullptr || ws_bytes < need)) return MUON_EWORKSPACE;
