@@ -402,9 +402,14 @@ struct Fp8Tile {
 
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
-// 4 bytes per lane to LDS bytes [lds_addr + 4 * lane), as gemm::dma16
-__device__ __forceinline__ void dma4(const void* g, uint32_t lds_addr) {
-  asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dword %0, off" ::"v"(g),
+// 16 (or 4) bytes per lane from base + off to LDS bytes [lds_addr + 16 (4) * lane), as gemm::dma16
+__device__ __forceinline__ void dma16_at(const uint8_t* base, uint32_t off, uint32_t lds_addr) {
+  asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base),
+               "s"(__builtin_amdgcn_readfirstlane(lds_addr))
+               : "memory", "m0");
+}
+__device__ __forceinline__ void dma4_at(const uint8_t* base, uint32_t off, uint32_t lds_addr) {
+  asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dword %0, %1" ::"v"(off), "s"(base),
                "s"(__builtin_amdgcn_readfirstlane(lds_addr))
                : "memory", "m0");
 }
@@ -458,27 +463,29 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void fp8_gemm_tile_kern
   // scale words: 64 rows per DMA, of A for the first BM / 64 of them
   const uint8_t* s_src[C_::S_DMA];
   int64_t s_step[C_::S_DMA];
+  uint32_t s_off[C_::S_DMA];
 #pragma unroll
   for (int i = 0; i < C_::S_DMA; ++i) {
     const int r = 64 * (wave * C_::S_DMA + i);
     const bool of_a = r < BM;
-    const int row = of_a ? min(r + lane, mlast) : min(r - BM + lane, nlast);
-    s_src[i] = of_a ? g.sa + (m0 + row) * 4 : g.sb + (n0 + row) * 4;
+    s_off[i] = uint32_t(of_a ? min(r + lane, mlast) : min(r - BM + lane, nlast)) * 4;
+    s_src[i] = of_a ? g.sa + m0 * 4 : g.sb + n0 * 4;
     s_step[i] = (of_a ? g.ra4 : g.rb4) * 4;
   }
   const uint32_t lds_base =
       static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char*)lds));
-  auto issue = [&](int kt, uint32_t off) {
+  // copy q (0 .. D - 1) of stage kt to ring offset `off`
+  auto issue_one = [&](int q, int kt, uint32_t off) __attribute__((always_inline)) {
     const uint32_t st = lds_base + off;
-    const uint8_t* ak = At + int64_t(kt) * 64;
-    const uint8_t* bk = Bt + int64_t(kt) * 64;
-#pragma unroll
-    for (int q = 0; q < C_::A_DMA; ++q) gemm::dma16(ak + a_off[q], st + (wave * C_::A_DMA + q) * 1024);
-#pragma unroll
-    for (int q = 0; q < C_::B_DMA; ++q) gemm::dma16(bk + b_off[q], st + C_::A_BYTES + (wave * C_::B_DMA + q) * 1024);
-#pragma unroll
-    for (int q = 0; q < C_::S_DMA; ++q)
-      dma4(s_src[q] + (kt >> 3) * s_step[q], st + C_::A_BYTES + C_::B_BYTES + (wave * C_::S_DMA + q) * 256);
+    if (q < C_::A_DMA) {
+      dma16_at(At + int64_t(kt) * 64, a_off[q], st + (wave * C_::A_DMA + q) * 1024);
+    } else if (q < C_::A_DMA + C_::B_DMA) {
+      const int b = q - C_::A_DMA;
+      dma16_at(Bt + int64_t(kt) * 64, b_off[b], st + C_::A_BYTES + (wave * C_::B_DMA + b) * 1024);
+    } else {
+      const int s = q - C_::A_DMA - C_::B_DMA;
+      dma4_at(s_src[s] + (kt >> 3) * s_step[s], s_off[s], st + C_::A_BYTES + C_::B_BYTES + (wave * C_::S_DMA + s) * 256);
+    }
   };
   auto ring_next = [](uint32_t o) {
     o += C_::STAGE;
@@ -488,22 +495,23 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void fp8_gemm_tile_kern
     u32x4_t a[FM][2], b[FN][2];
     uint32_t sa[FM], sb[FN];
   };
-  auto read = [&](const char* st, Frags& f) __attribute__((always_inline)) {
-#pragma unroll
-    for (int j = 0; j < FN; ++j)
-#pragma unroll
-      for (int c = 0; c < 2; ++c)
-        f.b[j][c] = *reinterpret_cast<const u32x4_t*>(st + C_::A_BYTES + gemm::krow_off(wn0 + 32 * j + fr, 2 * c + h));
-#pragma unroll
-    for (int i = 0; i < FM; ++i)
-#pragma unroll
-      for (int c = 0; c < 2; ++c)
-        f.a[i][c] = *reinterpret_cast<const u32x4_t*>(st + gemm::krow_off(wm0 + 32 * i + fr, 2 * c + h));
-    const char* sc = st + C_::A_BYTES + C_::B_BYTES;
-#pragma unroll
-    for (int i = 0; i < FM; ++i) f.sa[i] = *reinterpret_cast<const uint32_t*>(sc + (wm0 + 32 * i + fr) * 4);
-#pragma unroll
-    for (int j = 0; j < FN; ++j) f.sb[j] = *reinterpret_cast<const uint32_t*>(sc + (BM + wn0 + 32 * j + fr) * 4);
+  // LDS read q (0 .. READS - 1) of a step's operands: the scale words, then B's and A's blocks
+  constexpr int READS = 3 * (FM + FN);
+  const int a_at[2] = {gemm::krow_off(wm0 + fr, h), gemm::krow_off(wm0 + fr, 2 + h)};
+  const int b_at[2] = {C_::A_BYTES + gemm::krow_off(wn0 + fr, h), C_::A_BYTES + gemm::krow_off(wn0 + fr, 2 + h)};
+  const int sa_at = C_::A_BYTES + C_::B_BYTES + (wm0 + fr) * 4, sb_at = C_::A_BYTES + C_::B_BYTES + (BM + wn0 + fr) * 4;
+  auto read_one = [&](int q, const char* st, Frags& f) __attribute__((always_inline)) {
+    if (q < FN) {
+      f.sb[q] = *reinterpret_cast<const uint32_t*>(st + sb_at + 128 * q);
+    } else if (q < FN + FM) {
+      f.sa[q - FN] = *reinterpret_cast<const uint32_t*>(st + sa_at + 128 * (q - FN));
+    } else if (q < FM + 3 * FN) {
+      const int b = q - FN - FM;
+      f.b[b >> 1][b & 1] = *reinterpret_cast<const u32x4_t*>(st + b_at[b & 1] + 2048 * (b >> 1));
+    } else {
+      const int a = q - FM - 3 * FN;
+      f.a[a >> 1][a & 1] = *reinterpret_cast<const u32x4_t*>(st + a_at[a & 1] + 2048 * (a >> 1));
+    }
   };
   f32x16_t acc[FM][FN];
 #pragma unroll
@@ -512,62 +520,93 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void fp8_gemm_tile_kern
     for (int j = 0; j < FN; ++j)
 #pragma unroll
       for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
-  auto mma = [&](int kt, const Frags& f) __attribute__((always_inline)) {
+  // One step's products, in MFMAs 0 .. N - 1; `between(n)` is what the wave issues after
+  // MFMA n, while the matrix unit works (a wave issues in order, so copies and reads
+  // have to stand between the products, not in front of them).
+  constexpr int PHASES = EXACT ? 4 : 1, N = PHASES * FM * FN;
+  auto mma = [&](int kt, const Frags& f, auto&& between) __attribute__((always_inline)) {
     const int sh = 8 * ((kt >> 1) & 3);   // this group's byte of the scale words
     if constexpr (EXACT) {
+      float va[FM], vb[FN];
 #pragma unroll
-      for (int p = 0; p < 4; ++p) {
-        bf16x8_t wa[FM], wb[FN];
+      for (int i = 0; i < FM; ++i) va[i] = scale_value(f.sa[i] >> sh);
 #pragma unroll
-        for (int i = 0; i < FM; ++i)
-          wa[i] = widen8<FA>(f.a[i][p >> 1][2 * (p & 1)], f.a[i][p >> 1][2 * (p & 1) + 1], scale_value(f.sa[i] >> sh));
+      for (int j = 0; j < FN; ++j) vb[j] = scale_value(f.sb[j] >> sh);
+      // operand w (A's blocks, then B's) of phase p, widened while phase p - 1 multiplies
+      bf16x8_t w[2][FM + FN];
+      auto widen = [&](int p, int k) __attribute__((always_inline)) {
+        const int c = p >> 1, e = 2 * (p & 1);
+        w[p & 1][k] = k < FM ? widen8<FA>(f.a[k][c][e], f.a[k][c][e + 1], va[k])
+                             : widen8<MUON_FP8_E4M3>(f.b[k - FM][c][e], f.b[k - FM][c][e + 1], vb[k - FM]);
+      };
 #pragma unroll
-        for (int j = 0; j < FN; ++j)
-          wb[j] = widen8<MUON_FP8_E4M3>(f.b[j][p >> 1][2 * (p & 1)], f.b[j][p >> 1][2 * (p & 1) + 1],
-                                        scale_value(f.sb[j] >> sh));
+      for (int k = 0; k < FM + FN; ++k) widen(0, k);
 #pragma unroll
-        for (int i = 0; i < FM; ++i)
+      for (int p = 0; p < 4; ++p)
 #pragma unroll
-          for (int j = 0; j < FN; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wb[j], wa[i], acc[i][j], 0, 0, 0);
-      }
+        for (int t = 0; t < FM * FN; ++t) {
+          const int i = t / FN, j = t % FN;
+          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(w[p & 1][FM + j], w[p & 1][i], acc[i][j], 0, 0, 0);
+          if (p < 3 && t < FM + FN) widen(p + 1, t);
+          between(p * FM * FN + t);
+          __builtin_amdgcn_sched_barrier(0);
+        }
     } else {
+      uint32_t va[FM], vb[FN];
 #pragma unroll
-      for (int i = 0; i < FM; ++i)
+      for (int i = 0; i < FM; ++i) va[i] = f.sa[i] >> sh;
 #pragma unroll
-        for (int j = 0; j < FN; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-              join(f.b[j]), join(f.a[i]), acc[i][j], 0, FA, 0, int(f.sb[j] >> sh), 0, int(f.sa[i] >> sh));
+      for (int j = 0; j < FN; ++j) vb[j] = f.sb[j] >> sh;
+#pragma unroll
+      for (int t = 0; t < FM * FN; ++t) {
+        const int i = t / FN, j = t % FN;
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(join(f.b[j]), join(f.a[i]), acc[i][j], 0, FA, 0,
+                                                                    int(vb[j]), 0, int(va[i]));
+        between(t);
+        __builtin_amdgcn_sched_barrier(0);
+      }
     }
   };
   // 64-value steps: an even number, at least two
   const int nk = __builtin_amdgcn_readfirstlane(int(g.K / 64));
 #pragma unroll
   for (int s = 0; s < S - 1; ++s)
-    if (s < nk) issue(s, uint32_t(s) * C_::STAGE);
+    if (s < nk)
+#pragma unroll
+      for (int q = 0; q < C_::D; ++q) issue_one(q, s, uint32_t(s) * C_::STAGE);
   if (nk >= S - 1) ring_barrier<C_::D * (S - 2)>();
   else ring_barrier<0>();
   Frags f0, f1;
-  read(lds, f0);
+#pragma unroll
+  for (int q = 0; q < READS; ++q) read_one(q, lds, f0);
   uint32_t o_cur = 0, o_iss = uint32_t(S - 1) * C_::STAGE;
   int it = 0;
+  constexpr int RPM = (READS + N * 3 / 4 - 1) / (N * 3 / 4);   // reads per MFMA, done after three quarters of them
   auto steady = [&](Frags& cur, Frags& nxt) __attribute__((always_inline)) {
-    const uint32_t o_nxt = ring_next(o_cur);
+    const char* st = lds + ring_next(o_cur);
     ring_barrier<C_::D * (S - 3)>();
-    issue(it + S - 1, o_iss);
-    read(lds + o_nxt, nxt);
-    mma(it, cur);
-    o_cur = o_nxt;
+    mma(it, cur, [&](int n) __attribute__((always_inline)) {
+#pragma unroll
+      for (int r = 0; r < RPM; ++r)
+        if (RPM * n + r < READS) read_one(RPM * n + r, st, nxt);
+#pragma unroll
+      for (int q = 0; q < C_::D; ++q)
+        if (q * N / C_::D == n) issue_one(q, it + S - 1, o_iss);
+    });
+    o_cur = ring_next(o_cur);
     o_iss = ring_next(o_iss);
     ++it;
   };
   auto drain = [&](Frags& cur, Frags& nxt) __attribute__((always_inline)) {
-    const uint32_t o_nxt = ring_next(o_cur);
-    if (it + 1 < nk) {
+    const bool more = it + 1 < nk;
+    if (more) {
       ring_barrier<0>();
-      read(lds + o_nxt, nxt);
+      const char* st = lds + ring_next(o_cur);
+#pragma unroll
+      for (int q = 0; q < READS; ++q) read_one(q, st, nxt);
     }
-    mma(it, cur);
-    o_cur = o_nxt;
+    mma(it, cur, [](int) {});
+    o_cur = ring_next(o_cur);
     ++it;
   };
   while (it + S < nk) {   // two steps that both still copy a stage

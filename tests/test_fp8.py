@@ -302,6 +302,22 @@ def test_gemm_integers_are_exact(m, n, K):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("m,n,K", [(2100, 4001, 640), (2048, 4096, 128), (5000, 2050, 256), (4097, 2047, 512)])
+def test_gemm_large_tiles_are_exact(m, n, K, out):
+    """Ragged products of many tiles: entries in -1, 0, 1 under scale 1, sums under 256 are exact in bf16 too."""
+    rng = np.random.default_rng([m, n])
+    a, b = (rng.integers(-1, 2, (r, K)).astype(np.float32) for r in (m, n))
+    A, B = (torch.from_numpy(v).cuda().to(torch.float8_e4m3fn) for v in (a, b))
+    sa, sb = (torch.full(mao.fp8_scale_shape(r, K), 127, dtype=torch.uint8, device="cuda") for r in (m, n))
+    C = torch.full((m, n), float("nan"), dtype=torch.float32 if out == "f32" else torch.bfloat16, device="cuda")
+    mao.fp8_gemm(A, sa, B, sb, C)
+    ref = a @ b.T                      # sums of at most 640 ones: exact in fp32
+    assert np.abs(ref).max() < 256
+    np.testing.assert_array_equal(C.float().cpu().numpy(), ref)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("m", [1, 40, 200, 600])
 def test_gemm_repeats_bit_for_bit(m):
     A, sa, _ = operand(m, 4096, "e4m3", 31)
