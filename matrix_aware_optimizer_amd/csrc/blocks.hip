@@ -4,20 +4,28 @@
 // One iteration is X' = (a I + b A + c A A) X with A = X X^T on the short side.
 // With X = T X0, T starts as I and stays a polynomial of A0 = X0 X0^T, and so does
 // every later A; polynomials of one symmetric matrix are symmetric and commute:
-//     P = a I + b A + c A A,   T' = P T,   A' = X' X'^T = P A P.
+//     P = a I + b A + c A A,   T' = P T,   A' = X' X'^T = P (P A).
 // The long side is therefore touched twice only: once for A0, once for U = T X0.
-// All iterations between work on s x s matrices, in fp32 on matrix cores, one
-// workgroup per block with everything in LDS.  X0 = M / |M|_F, and |M|_F^2 is the
-// trace of M M^T.  Three launches serve every block of a call:
+// All iterations between work on s x s matrices, one workgroup per block.  A is made
+// symmetric again in every iteration: what rounding leaves in it that is not symmetric
+// would grow sevenfold per iteration where A has converged, while symmetric errors
+// shrink there.
+// X0 = M / |M|_F, and |M|_F^2 is the trace of M M^T.  Three launches serve every block
+// of a call:
 //   gram   partial M M^T over chunks of the long side (lower 32 x 32 tiles only)
 //   poly   sums the chunks in order, scales by the trace, iterates, writes T / |M|_F
 //   apply  U = T M, or W <- (1 - eta decay) W - eta scale U
 //
 // Rounding.  A relative error d of A0 grows by at most a^2 per iteration where A is
-// small, so A and T are held and multiplied in fp32 (products of bf16 splits would
-// not do: 2^-17 a^8 is 0.15 for a = 3.4445).  The products with a bf16 M are exact
-// in bf16 matrix instructions; T enters the last one as the sum of two bf16 parts
-// (error 2^-17, under half a step of a bf16 U or W) or three (fp32 outputs: 2^-25).
+// small, so A and T are held in fp32 and multiplied as such: every s x s product takes
+// its operands as sums of three bf16 parts (24 bits and the range of fp32), the six
+// products of parts that reach 2^-24, added in fp32: six matrix instructions where
+// fp32 ones would take the time of sixteen.  (Two fp16 parts, three products, were half
+// as exact as fp32: square blocks with small singular values showed it.)  An fp32 M is
+// split in the same way, a bf16 M is taken as it is.  T enters
+// the last product in two bf16 parts (2^-17 of U, under half a step of a bf16 output)
+// or three (fp32 outputs), M there in as many at most; products of parts beyond the
+// last one kept are left out.
 #include <algorithm>
 
 #include "common.h"
@@ -27,10 +35,6 @@ namespace muon {
 namespace {
 
 constexpr int kMaxRuns = 24;       // problems of one launch (by-value kernel argument)
-constexpr int kTile = 32;
-constexpr int kTilePitch = 33;     // floats per row of a tile in LDS
-constexpr int kTileFloats = kTile * kTilePitch;
-constexpr int kMaxTiles = 10;      // lower 32 x 32 tiles of a 128 x 128 matrix
 
 // One problem: `count` blocks of rows x cols, seen as s x l with s <= l (tall: transposed)
 struct Run {
@@ -74,54 +78,117 @@ __device__ __forceinline__ const Run& find_run(const Runs& runs, int& u, int uni
   return runs.r[k];
 }
 
-// Rows [r0, r0 + NR) and columns [c0, c0 + NC) of a row-major matrix into LDS rows of
-// `pitch` bytes; entries outside rows x cols become zero.
-template <typename T>
-__device__ __forceinline__ void load_region(const T* src, int64_t ld, int rows, int cols, int r0, int c0, int NR, int NC,
-                                            char* lds, int pitch, bool vec) {
-  constexpr int E = 16 / sizeof(T);
-  const int per = NC / E, n = NR * per;
-  for (int t = threadIdx.x; t < n; t += 256) {
-    const int r = t / per, c = (t % per) * E;
-    const T* p = src + int64_t(r0 + r) * ld + c0 + c;
-    uint4 w = make_uint4(0, 0, 0, 0);
-    if (r0 + r < rows) {
-      if (vec && c0 + c + E <= cols) {
-        w = *reinterpret_cast<const uint4*>(p);
-      } else {
-        T e[E];
+// A region of a row-major matrix on its way from memory to LDS: rows [r0, r0 + NR),
+// columns [c0, c0 + NC), entries outside rows x cols as zeros.  fetch() leaves it in
+// registers (LD 16-byte pieces per thread, 256 threads), so that it is under way while
+// the region before is multiplied; store() writes it as bf16 planes: a bf16 entry as it
+// is, an fp32 entry as its NP leading bf16 parts.
+template <typename T, int LD>
+struct Region {
+  static constexpr int E = 16 / sizeof(T);
+  uint4 w[LD];
+
+  __device__ __forceinline__ void fetch(const T* src, int64_t ld, int rows, int cols, int r0, int c0, int NR, int NC,
+                                        bool vec) {
+    const int per = NC / E, n = NR * per;
 #pragma unroll
-        for (int q = 0; q < E; ++q) e[q] = c0 + c + q < cols ? p[q] : T(0);
-        w = *reinterpret_cast<const uint4*>(e);
+    for (int q = 0; q < LD; ++q) {
+      const int t = threadIdx.x + 256 * q;
+      w[q] = make_uint4(0, 0, 0, 0);
+      if (t < n) {
+        const int r = t / per, c = (t % per) * E;
+        const T* p = src + int64_t(r0 + r) * ld + c0 + c;
+        if (r0 + r < rows) {
+          if (vec && c0 + c + E <= cols) {
+            w[q] = *reinterpret_cast<const uint4*>(p);
+          } else {
+            uint32_t e[E];
+#pragma unroll
+            for (int k = 0; k < E; ++k) {
+              e[k] = 0;
+              if (c0 + c + k < cols) {
+                if constexpr (sizeof(T) == 2) e[k] = p[k];
+                else e[k] = __float_as_uint(p[k]);
+              }
+            }
+            if constexpr (sizeof(T) == 2)
+              w[q] = make_uint4(e[0] | (e[1] << 16), e[2] | (e[3] << 16), e[4] | (e[5] << 16), e[6] | (e[7] << 16));
+            else
+              w[q] = make_uint4(e[0], e[1], e[2], e[3]);
+          }
+        }
       }
     }
-    *reinterpret_cast<uint4*>(lds + r * pitch + c * int(sizeof(T))) = w;
   }
-}
+
+  template <int NP>
+  __device__ __forceinline__ void store(char* lds, int pitch, int plane, int NR, int NC) const {
+    const int per = NC / E, n = NR * per;
+#pragma unroll
+    for (int q = 0; q < LD; ++q) {
+      const int t = threadIdx.x + 256 * q;
+      if (t < n) {
+        const int r = t / per, c = (t % per) * E;
+        char* dst = lds + r * pitch + c * 2;
+        if constexpr (sizeof(T) == 2) {
+          *reinterpret_cast<uint4*>(dst) = w[q];
+        } else {
+          float x[4] = {__uint_as_float(w[q].x), __uint_as_float(w[q].y), __uint_as_float(w[q].z), __uint_as_float(w[q].w)};
+#pragma unroll
+          for (int p = 0; p < NP; ++p) {
+            uint32_t b[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              b[k] = f32_to_bf16(x[k]);
+              x[k] -= __uint_as_float(b[k] << 16);
+            }
+            *reinterpret_cast<uint2*>(dst + p * plane) = make_uint2(b[0] | (b[1] << 16), b[2] | (b[3] << 16));
+          }
+        }
+      }
+    }
+  }
+};
 
 // LDS pitches (bytes), so that one access spreads over the 64 banks.  Rows read 16
-// bytes per lane along themselves: 16 over a multiple of 128 (eight rows start in
-// eight different groups of four banks).  bf16 rows read transposed, four rows at a
-// time: 64 over a multiple of 256.  fp32 rows read across by the two half-waves, four
-// rows apart: 32 over a multiple of 64 (four rows are half the banks).
-constexpr int kRowPitchTr = 320;
+// bytes per lane along themselves: an odd multiple of 16.  Rows read transposed, four
+// at a time: 64 over a multiple of 128 (the four rows start in four different quarters
+// of the banks).
+constexpr int row_pitch(int bytes) { return bytes + 16; }
+constexpr int tr_pitch(int bytes) { return bytes + 64; }
+
+// An operand's 32 x 16 fragment of one plane, the 32 index values along the rows
+// (contiguous k) or along the columns (k-major, transposed on the way)
+template <bool KMAJOR>
+__device__ __forceinline__ u32x4_t fragment(const char* plane, int pitch, int first, int ks, int lane) {
+  if constexpr (KMAJOR) {
+    const int gi = lane & 15, G = lane >> 4;
+    const char* base = plane + (ks * 16 + 8 * (G >> 1) + (gi >> 2)) * pitch + (first + 16 * (G & 1) + 4 * (gi & 3)) * 2;
+    return gemm::read_tr_pair(base, base + 4 * pitch);
+  } else {
+    return *reinterpret_cast<const u32x4_t*>(plane + (first + (lane & 31)) * pitch + (2 * ks + (lane >> 5)) * 16);
+  }
+}
 
 // ---------------------------------------------------------------------------
 // gram: tile t of M M^T over one chunk, as it lies in the accumulators: [t][16][64]
 // ---------------------------------------------------------------------------
+template <typename T> constexpr int gram_slab() { return 128 / sizeof(T); }   // k-values staged at a time
+
 template <typename T, bool TALL>
 __global__ __launch_bounds__(256) void blocks_gram_kernel(Runs runs, char* ws) {
-  constexpr int SLAB = 128 / sizeof(T);            // k-values staged at a time
-  constexpr int PITCH_W = 128 + 16;                // wide: [s][SLAB]
-  constexpr int PITCH_T = sizeof(T) == 2 ? kRowPitchTr : 544;   // tall: [SLAB][s]
-  __shared__ __attribute__((aligned(16))) char lds[TALL ? SLAB * PITCH_T : 128 * PITCH_W];
+  constexpr int SLAB = gram_slab<T>(), NP = sizeof(T) == 2 ? 1 : 3;
+  constexpr int PITCH = TALL ? tr_pitch(256) : row_pitch(2 * SLAB);   // tall [SLAB][s], wide [s][SLAB]
+  constexpr int PLANE = (TALL ? SLAB : 128) * PITCH;
+  __shared__ __attribute__((aligned(16))) char lds[NP * PLANE];
   int u = blockIdx.x;
   const Run& run = find_run(runs, u, 0);
   const int b = u / run.chunks, chunk = u % run.chunks;
   const int s = run.s, l = run.l, nt = (s + 31) / 32, sp = nt * 32;
   const T* M = static_cast<const T*>(run.M) + b * run.stride_m;
+  const int64_t ld = run.ld_m;
+  const bool vec = run.vec_m;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int fr = lane & 31, h = lane >> 5;
   const int nlow = tiles_of(nt);
   const int k0 = chunk * run.chunk, k1 = min(l, k0 + run.chunk);
   f32x16_t acc[3];
@@ -129,50 +196,36 @@ __global__ __launch_bounds__(256) void blocks_gram_kernel(Runs runs, char* ws) {
   for (int q = 0; q < 3; ++q)
 #pragma unroll
     for (int v = 0; v < 16; ++v) acc[q][v] = 0.0f;
+  Region<T, 4> reg;
+  auto fetch = [&](int k) __attribute__((always_inline)) {
+    if (TALL) reg.fetch(M, ld, k1, s, k, 0, SLAB, sp, vec);
+    else reg.fetch(M, ld, s, k1, 0, k, sp, SLAB, vec);
+  };
+  fetch(k0);
   for (int k = k0; k < k1; k += SLAB) {
     __syncthreads();
-    if (TALL) load_region<T>(M, run.ld_m, k1, s, k, 0, SLAB, sp, lds, PITCH_T, run.vec_m);
-    else load_region<T>(M, run.ld_m, s, k1, 0, k, sp, SLAB, lds, PITCH_W, run.vec_m);
+    if (TALL) reg.template store<NP>(lds, PITCH, PLANE, SLAB, sp);
+    else reg.template store<NP>(lds, PITCH, PLANE, sp, SLAB);
     __syncthreads();
+    if (k + SLAB < k1) fetch(k + SLAB);
 #pragma unroll
     for (int q = 0; q < 3; ++q) {
       const int t = wave + 4 * q;
       if (t < nlow) {
         int ti, tj;
         tile_rc(t, ti, tj);
-        if constexpr (sizeof(T) == 2) {
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks) {
-            u32x4_t fa, fb;
-            if constexpr (TALL) {
-              const int gi = lane & 15, G = lane >> 4;
-              const char* base = lds + (ks * 16 + 8 * (G >> 1) + (gi >> 2)) * PITCH_T + (16 * (G & 1) + 4 * (gi & 3)) * 2;
-              fa = gemm::read_tr_pair(base + ti * 64, base + ti * 64 + 4 * PITCH_T);
-              fb = gemm::read_tr_pair(base + tj * 64, base + tj * 64 + 4 * PITCH_T);
-            } else {
-              fa = *reinterpret_cast<const u32x4_t*>(lds + (ti * 32 + fr) * PITCH_W + (2 * ks + h) * 16);
-              fb = *reinterpret_cast<const u32x4_t*>(lds + (tj * 32 + fr) * PITCH_W + (2 * ks + h) * 16);
-            }
-            gemm::Mfma<bf16_t>::mma(fa, fb, acc[q]);
+        for (int ks = 0; ks < SLAB / 16; ++ks) {
+          u32x4_t fa[NP], fb[NP];
+#pragma unroll
+          for (int p = 0; p < NP; ++p) {
+            fa[p] = fragment<TALL>(lds + p * PLANE, PITCH, ti * 32, ks, lane);
+            fb[p] = fragment<TALL>(lds + p * PLANE, PITCH, tj * 32, ks, lane);
           }
-        } else {
 #pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            f32x4_t fa, fb;
-            if constexpr (TALL) {
+          for (int p = 0; p < NP; ++p)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const char* row = lds + (8 * g + 4 * h + e) * PITCH_T + fr * 4;
-                fa[e] = *reinterpret_cast<const float*>(row + ti * 128);
-                fb[e] = *reinterpret_cast<const float*>(row + tj * 128);
-              }
-            } else {
-              fa = *reinterpret_cast<const f32x4_t*>(lds + (ti * 32 + fr) * PITCH_W + (2 * g + h) * 16);
-              fb = *reinterpret_cast<const f32x4_t*>(lds + (tj * 32 + fr) * PITCH_W + (2 * g + h) * 16);
-            }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[q] = __builtin_amdgcn_mfma_f32_32x32x2f32(fa[e], fb[e], acc[q], 0, 0, 0);
-          }
+            for (int r = 0; p + r < NP; ++r) gemm::Mfma<bf16_t>::mma(fa[p], fb[r], acc[q]);
         }
       }
     }
@@ -188,147 +241,243 @@ __global__ __launch_bounds__(256) void blocks_gram_kernel(Runs runs, char* ws) {
 }
 
 // ---------------------------------------------------------------------------
-// poly: one workgroup per block, one wave per lower tile
+// poly: one workgroup per block, one wave per strip of 16 columns
 // ---------------------------------------------------------------------------
-// Fragment of symmetric matrix S (lower tiles in LDS): entry (row 32 X + r, column
-// 32 K + k), from the tile itself or, above the diagonal, from its mirror image.
-struct TileReader {
-  const float* p;
-  int step;   // floats from one k to the next
-};
-__device__ __forceinline__ TileReader tile_reader(const float* S, int X, int K, int r, int h) {
-  const bool low = X >= K;
-  const int t = low ? X * (X + 1) / 2 + K : K * (K + 1) / 2 + X;
-  const float* base = S + t * kTileFloats;
-  return low ? TileReader{base + r * kTilePitch + h, 1} : TileReader{base + r + h * kTilePitch, kTilePitch};
-}
+// A wave holds its strip of A, T and P as it comes out of v_mfma_f32_16x16x32_bf16:
+// lane (r, g = lane / 16) has rows 16 y + 4 g .. + 3 of column r of the strip, for every
+// y.  All matrices are symmetric, so that is also row r of the strip, and two of these
+// groups of four (y = 2 t, 2 t + 1) are eight of the 32 k-values of one matrix
+// instruction: a strip is its own second operand without leaving the registers, if the
+// first operand takes the k-values in the same order.  Only A (for A A) and P (for
+// P T, P A and P (P A)) are first operands, and go through LDS as rows.  17 products of
+// a block in five steps.
+constexpr int kParts = 3;
 
-// acc += tile (ti, tj) of L R, both symmetric
-__device__ __forceinline__ void sym_product(const float* L, const float* R, int ti, int tj, int nt, int r, int h,
-                                            f32x16_t& acc) {
-  for (int K = 0; K < nt; ++K) {
-    const TileReader a = tile_reader(L, ti, K, r, h), b = tile_reader(R, tj, K, r, h);
+template <int NY>
+struct SymOperand {
+  bf16x8_t p[kParts][NY / 2];
+};
+
+template <int NY>
+__device__ __forceinline__ void split_strip(const f32x4_t (&v)[NY], SymOperand<NY>& o) {
 #pragma unroll
-    for (int k = 0; k < 16; ++k)
-      acc = __builtin_amdgcn_mfma_f32_32x32x2f32(a.p[2 * k * a.step], b.p[2 * k * b.step], acc, 0, 0, 0);
+  for (int t = 0; t < NY / 2; ++t) {
+    float x[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) x[q] = v[2 * t + (q >> 2)][q & 3];
+#pragma unroll
+    for (int p = 0; p < kParts; ++p)
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const __bf16 h = static_cast<__bf16>(x[q]);
+        o.p[p][t][q] = h;
+        x[q] -= static_cast<float>(h);
+      }
   }
 }
 
-__device__ __forceinline__ void put_tile(float* S, int t, int r, int h, const f32x16_t& v) {
+template <int NY>
+struct SymLds {
+  static constexpr int PITCH = NY * 32 + 16;        // bytes per row: an odd multiple of 16
+  static constexpr int PLANE = NY * 16 * PITCH;
+  static constexpr int BYTES = kParts * PLANE;
+  static constexpr int BUFFERS = 2 * BYTES <= 150 * 1024 ? 2 : 1;   // two take turns, or one serves all
+};
+
+template <int NY>
+__device__ __forceinline__ void put_strip(char* buf, int wave, int lane, const SymOperand<NY>& o) {
+  char* row = buf + (16 * wave + (lane & 15)) * SymLds<NY>::PITCH + 16 * (lane >> 4);
 #pragma unroll
-  for (int q = 0; q < 16; ++q) S[t * kTileFloats + (8 * (q >> 2) + 4 * h + (q & 3)) * kTilePitch + r] = v[q];
+  for (int p = 0; p < kParts; ++p)
+#pragma unroll
+    for (int t = 0; t < NY / 2; ++t) *reinterpret_cast<bf16x8_t*>(row + 64 * t + p * SymLds<NY>::PLANE) = o.p[p][t];
 }
 
-__global__ __launch_bounds__(64 * kMaxTiles) void blocks_poly_kernel(Runs runs, char* ws, float a, float b, float c,
-                                                                     int steps) {
-  extern __shared__ __attribute__((aligned(16))) float sm[];
-  __shared__ double trace[4];
-  int u = blockIdx.x;
-  const Run& run = find_run(runs, u, 1);
-  const int s = run.s, nt = (s + 31) / 32, nlow = tiles_of(nt), sp = nt * 32;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int r = lane & 31, h = lane >> 5;
-  const bool busy = wave < nlow;
-  float* SA = sm;
-  float* ST = sm + nlow * kTileFloats;
-  float* SP = sm + 2 * nlow * kTileFloats;
-  int ti = 0, tj = 0;
-  tile_rc(busy ? wave : 0, ti, tj);
-  f32x16_t A, T, P;
+// the strip's transpose, from what put_strip left: four consecutive rows of one column per
+// transposing read
+template <int NY>
+__device__ __forceinline__ void get_transposed(const char* buf, int wave, int lane, f32x4_t (&out)[NY]) {
+  // lane 4 j + q of a group of 16 points at row j, columns 4 q .. + 3 of the strip
+  const char* at = buf + (4 * (lane >> 4) + ((lane & 15) >> 2)) * SymLds<NY>::PITCH + 64 * (wave >> 1) + 8 * (wave & 1) +
+                   16 * (lane & 3);
 #pragma unroll
-  for (int v = 0; v < 16; ++v) A[v] = T[v] = P[v] = 0.0f;
-  // entries of this lane on the matrix's diagonal
-  auto diag = [&](int v) { return ti == tj && 8 * (v >> 2) + 4 * h + (v & 3) == r; };
-  if (busy) {
-    const float* src = reinterpret_cast<const float*>(ws + run.partials) + int64_t(u) * run.chunks * nlow * 1024 +
-                       wave * 1024 + lane;
-    for (int k = 0; k < run.chunks; ++k)
+  for (int y = 0; y < NY; ++y) {
+    out[y] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int v = 0; v < 16; ++v) A[v] += src[int64_t(k) * nlow * 1024 + v * 64];
-    if (ti == tj) {
-      double t = 0.0;
+    for (int p = kParts - 1; p >= 0; --p) {
+      const gemm::lds_bf16x4_t w = __builtin_amdgcn_ds_read_tr16_b64_v4bf16(
+          (__attribute__((address_space(3))) gemm::lds_bf16x4_t*)(at + 16 * y * SymLds<NY>::PITCH + p * SymLds<NY>::PLANE));
 #pragma unroll
-      for (int v = 0; v < 16; ++v) t += diag(v) ? double(A[v]) : 0.0;
-      t = wave_sum(t);
-      if (lane == 0) trace[ti] = t;
+      for (int v = 0; v < 4; ++v) out[y][v] += static_cast<float>(w[v]);
     }
   }
+}
+
+// out = S o, S in LDS.  The parts of the next 16 x 32 piece of S are read while the
+// current one is multiplied.
+template <int NY>
+__device__ __forceinline__ void sym_product(const char* buf, int lane, const SymOperand<NY>& o, f32x4_t (&out)[NY]) {
+  constexpr int NT = NY / 2;
+  const char* row = buf + (lane & 15) * SymLds<NY>::PITCH + 16 * (lane >> 4);
+  bf16x8_t f[2][kParts];
+  auto read = [&](int k) __attribute__((always_inline)) {
+#pragma unroll
+    for (int p = 0; p < kParts; ++p)
+      f[k & 1][p] = *reinterpret_cast<const bf16x8_t*>(row + (k / NT) * 16 * SymLds<NY>::PITCH + (k % NT) * 64 +
+                                                       p * SymLds<NY>::PLANE);
+  };
+  read(0);
+#pragma unroll
+  for (int y = 0; y < NY; ++y) {
+    f32x4_t acc = {0.0f, 0.0f, 0.0f, 0.0f}, low = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const int k = y * NT + t;
+      if (k + 1 < NY * NT) read(k + 1);
+      const bf16x8_t(&s)[kParts] = f[k & 1];
+#pragma unroll
+      for (int p = 0; p < kParts; ++p)
+#pragma unroll
+        for (int r = 0; p + r < kParts; ++r) {
+          f32x4_t& to = (p + r) == 2 ? low : acc;   // two chains of three
+          to = __builtin_amdgcn_mfma_f32_16x16x32_bf16(s[p], o.p[r][t], to, 0, 0, 0);
+        }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    out[y] = acc + low;
+  }
+}
+
+template <int NY>
+__global__ __launch_bounds__(64 * NY) void blocks_poly_kernel(Runs runs, char* ws, float a, float b, float c, int steps) {
+  extern __shared__ __attribute__((aligned(16))) char sm[];
+  __shared__ double trace[NY];
+  constexpr bool SHARED = SymLds<NY>::BUFFERS == 1;
+  char* buf = sm;                                        // what is written next
+  char* other = SHARED ? sm : sm + SymLds<NY>::BYTES;
+  int u = blockIdx.x;
+  const Run& run = find_run(runs, u, 1);
+  constexpr int nlow = tiles_of(NY / 2), sp = 16 * NY;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 15, g = lane >> 4;
+  const int x = 16 * wave + r;                       // this lane's column
+  f32x4_t A[NY], T[NY];
+  {
+    // the partial Grams are lower 32 x 32 tiles as they lay in the accumulators: entry
+    // (row i, column j) of a tile is value 4 (i / 8) + i % 4 of lane j + 32 (i / 4 % 2)
+    const int chunks = run.chunks;
+    const float* src = reinterpret_cast<const float*>(ws + run.partials) + int64_t(u) * chunks * nlow * 1024;
+#pragma unroll
+    for (int y = 0; y < NY; ++y) A[y] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    const int X = wave >> 1, j = x & 31;
+    for (int k = 0; k < chunks; ++k) {
+#pragma unroll
+      for (int y = 0; y < NY; ++y) {
+        const int Y = y >> 1, i0 = 16 * (y & 1) + 4 * g;   // rows i0 .. i0 + 3 of tile row Y
+        f32x4_t w;
+        if (Y >= X) {
+          const float* at = src + (Y * (Y + 1) / 2 + X) * 1024 + 4 * (i0 >> 3) * 64 + j + 32 * ((i0 >> 2) & 1);
+#pragma unroll
+          for (int v = 0; v < 4; ++v) w[v] = at[64 * v];
+        } else {
+          // above the diagonal: the mirrored entry, row j of tile (X, Y), columns i0 ..
+          w = *reinterpret_cast<const f32x4_t*>(src + (X * (X + 1) / 2 + Y) * 1024 + (4 * (j >> 3) + (j & 3)) * 64 + i0 +
+                                                32 * ((j >> 2) & 1));
+        }
+        A[y] += w;
+      }
+      src += nlow * 1024;
+    }
+  }
+  // this lane's entry y, v lies on the diagonal
+  auto diag = [&](int y, int v) { return 16 * y + 4 * g + v == x; };
+  double mine = 0.0;
+#pragma unroll
+  for (int y = 0; y < NY; ++y)
+#pragma unroll
+    for (int v = 0; v < 4; ++v) mine += diag(y, v) ? double(A[y][v]) : 0.0;
+  mine = wave_sum(mine);
+  if (lane == 0) trace[wave] = mine;
   __syncthreads();
   double total = 0.0;
-  for (int i = 0; i < nt; ++i) total += trace[i];
+#pragma unroll
+  for (int i = 0; i < NY; ++i) total += trace[i];
   // a block of zeros gives U = 0
   const float inv = total == 0.0 ? 0.0f : float(1.0 / total);
   const float root = total == 0.0 ? 0.0f : float(1.0 / sqrt(total));
 #pragma unroll
-  for (int v = 0; v < 16; ++v) {
-    A[v] *= inv;
-    T[v] = diag(v) ? 1.0f : 0.0f;
-  }
-  if (busy && steps > 0) put_tile(SA, wave, r, h, A);
+  for (int y = 0; y < NY; ++y)
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      A[y][v] *= inv;
+      T[y][v] = diag(y, v) ? 1.0f : 0.0f;
+    }
+  // one buffer: everybody is done reading before it is written; two: the one written now
+  // was read before the last barrier
+  auto put = [&](const SymOperand<NY>& o) __attribute__((always_inline)) {
+    if (SHARED) __syncthreads();
+    put_strip<NY>(buf, wave, lane, o);
+    __syncthreads();
+    char* const w = buf;
+    buf = other;
+    other = w;
+  };
   for (int it = 0; it < steps; ++it) {
-    __syncthreads();
-    if (busy) {
-#pragma unroll
-      for (int v = 0; v < 16; ++v) P[v] = 0.0f;
-      if (c != 0.0f) sym_product(SA, SA, ti, tj, nt, r, h, P);
-#pragma unroll
-      for (int v = 0; v < 16; ++v) P[v] = fmaf(c, P[v], fmaf(b, A[v], diag(v) ? a : 0.0f));
-      put_tile(SP, wave, r, h, P);
-      if (it == 0) {
-        T = P;
-        put_tile(ST, wave, r, h, T);
-      }
-    }
-    __syncthreads();
     const bool last = it == steps - 1;
-    f32x16_t Y, T2;
-    if (busy) {
+    SymOperand<NY> oA;
+    f32x4_t P[NY];
+    split_strip<NY>(A, oA);
+    if (it > 0) {
+      put(oA);
+      get_transposed<NY>(other, wave, lane, P);
 #pragma unroll
-      for (int v = 0; v < 16; ++v) Y[v] = T2[v] = 0.0f;
-      if (it > 0) {
-        sym_product(SP, ST, ti, tj, nt, r, h, T2);
-        T = T2;
-      }
-      if (!last) sym_product(SP, SA, ti, tj, nt, r, h, Y);
+      for (int y = 0; y < NY; ++y) A[y] = 0.5f * (A[y] + P[y]);
+      split_strip<NY>(A, oA);
     }
-    if (last) break;
-    __syncthreads();
-    if (busy) {
-      put_tile(SA, wave, r, h, Y);
-      if (it > 0) put_tile(ST, wave, r, h, T);
-    }
-    __syncthreads();
-    if (busy) {
+    if (c != 0.0f) {
+      put(oA);
+      sym_product<NY>(other, lane, oA, P);               // A A
+    } else {
 #pragma unroll
-      for (int v = 0; v < 16; ++v) A[v] = 0.0f;
-      sym_product(SA, SP, ti, tj, nt, r, h, A);
+      for (int y = 0; y < NY; ++y) P[y] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
     }
-    __syncthreads();
-    if (busy) put_tile(SA, wave, r, h, A);
+#pragma unroll
+    for (int y = 0; y < NY; ++y)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) P[y][v] = fmaf(c, P[y][v], fmaf(b, A[y][v], diag(y, v) ? a : 0.0f));
+    SymOperand<NY> o;
+    split_strip<NY>(P, o);
+    if (it == 0) {
+#pragma unroll
+      for (int y = 0; y < NY; ++y) T[y] = P[y];
+      if (last) break;
+      put(o);
+    } else {
+      put(o);
+      split_strip<NY>(T, o);
+      sym_product<NY>(other, lane, o, T);                // T' = P T
+      if (last) break;
+    }
+    sym_product<NY>(other, lane, oA, P);                 // P A
+    split_strip<NY>(P, o);
+    sym_product<NY>(other, lane, o, A);                  // A' = P (P A)
   }
-  if (!busy) return;
-  // T / |M|_F, both triangles: fp32 [sp][sp], or two or three bf16 parts of it
-  char* base = ws + run.parts;
-  if (run.kind & kF32) {
-    float* dst = reinterpret_cast<float*>(base) + int64_t(u) * sp * sp;
+  // T / |M|_F in three bf16 parts, rows of [part][sp][sp]
+  bf16_t* dst = reinterpret_cast<bf16_t*>(ws + run.parts) + int64_t(u) * 3 * sp * sp + x * sp + 4 * g;
 #pragma unroll
-    for (int v = 0; v < 16; ++v) {
-      const int i = ti * 32 + 8 * (v >> 2) + 4 * h + (v & 3), j = tj * 32 + r;
-      dst[i * sp + j] = T[v] * root;
-      if (ti != tj) dst[j * sp + i] = T[v] * root;
-    }
-  } else {
-    bf16_t* dst = reinterpret_cast<bf16_t*>(base) + int64_t(u) * 3 * sp * sp;
+  for (int y = 0; y < NY; ++y) {
+    float w[4];
 #pragma unroll
-    for (int v = 0; v < 16; ++v) {
-      const int i = ti * 32 + 8 * (v >> 2) + 4 * h + (v & 3), j = tj * 32 + r;
-      float x = T[v] * root;
-      for (int part = 0; part < 3; ++part) {
-        const bf16_t p = f32_to_bf16(x);
-        x -= bf16_to_f32(p);
-        dst[part * sp * sp + i * sp + j] = p;
-        if (ti != tj) dst[part * sp * sp + j * sp + i] = p;
+    for (int v = 0; v < 4; ++v) w[v] = T[y][v] * root;
+#pragma unroll
+    for (int p = 0; p < 3; ++p) {
+      uint32_t h[4];
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        h[v] = f32_to_bf16(w[v]);
+        w[v] -= __uint_as_float(h[v] << 16);
       }
+      *reinterpret_cast<uint2*>(dst + p * sp * sp + 16 * y) = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
     }
   }
 }
@@ -385,45 +534,47 @@ template <typename T> constexpr int apply_slab() { return sizeof(T) == 2 ? 128 :
 template <typename T, typename TO, bool TALL>
 __global__ __launch_bounds__(256) void blocks_apply_kernel(Runs runs, const char* ws, Epilogue e) {
   constexpr int LS = apply_slab<T>();
-  constexpr bool BF = sizeof(T) == 2;
-  constexpr int NP = BF ? (sizeof(TO) == 2 ? 2 : 3) : 1;
-  constexpr int PITCH = TALL ? 128 * int(sizeof(T)) + 16 : (BF ? kRowPitchTr : 288);   // tall [LS][s], wide [s][LS]
-  constexpr int NF = BF ? 8 : 16;                    // 16-byte fragments of 128 k-values
-  __shared__ __attribute__((aligned(16))) char lds[(TALL ? LS : 128) * PITCH];
+  constexpr int NPT = sizeof(TO) == 2 ? 2 : 3;                 // bf16 parts of T
+  constexpr int NPM = sizeof(T) == 2 ? 1 : NPT;                // and of M
+  constexpr int PITCH = TALL ? row_pitch(256) : tr_pitch(2 * LS);   // tall [LS][s], wide [s][LS]
+  constexpr int PLANE = (TALL ? LS : 128) * PITCH;
+  extern __shared__ __attribute__((aligned(16))) char lds[];   // NPM planes
   int u = blockIdx.x;
   const Run& run = find_run(runs, u, 2);
   const int b = u / run.units, unit = u % run.units;
   const int s = run.s, l = run.l, nt = (s + 31) / 32, sp = nt * 32;
   const T* M = static_cast<const T*>(run.M) + b * run.stride_m;
   TO* out = static_cast<TO*>(run.out) + b * run.stride_out;
+  const int64_t ld = run.ld_m, ld_out = run.ld_out;
+  const bool vec = run.vec_m, vec_out = run.vec_out;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int fr = lane & 31, h = lane >> 5;
   // 4 waves: row tile ti, and every groups-th 32 entries of the long side
   const int groups = 4 / nt, ti = wave % nt, grp = wave / nt;
   const bool busy = grp < groups;
-  u32x4_t tf[NP][NF];
-#pragma unroll
-  for (int p = 0; p < NP; ++p)
-#pragma unroll
-    for (int q = 0; q < NF; ++q) {
-      tf[p][q] = u32x4_t{0, 0, 0, 0};
-      const int kq = BF ? 16 * q + 8 * h : 8 * q + 4 * h;   // first k of this lane's 16 bytes
-      if (kq < sp && busy) {
-        const char* base = ws + run.parts;
-        const int64_t at = int64_t(ti * 32 + fr) * sp + kq;
-        if constexpr (BF)
-          tf[p][q] = *reinterpret_cast<const u32x4_t*>(reinterpret_cast<const bf16_t*>(base) +
-                                                       (int64_t(b) * 3 + p) * sp * sp + at);
-        else
-          tf[p][q] = *reinterpret_cast<const u32x4_t*>(reinterpret_cast<const float*>(base) + int64_t(b) * sp * sp + at);
-      }
-    }
   const int l0 = unit * run.slabs * LS, l1 = min(l, l0 + run.slabs * LS);
+  Region<T, 8> reg;
+  auto fetch = [&](int x) __attribute__((always_inline)) {
+    if (TALL) reg.fetch(M, ld, l, s, x, 0, LS, sp, vec);
+    else reg.fetch(M, ld, s, l, 0, x, sp, LS, vec);
+  };
+  fetch(l0);
+  u32x4_t tf[NPT][8];
+#pragma unroll
+  for (int p = 0; p < NPT; ++p)
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      tf[p][q] = u32x4_t{0, 0, 0, 0};
+      if (16 * q < sp && busy)
+        tf[p][q] = *reinterpret_cast<const u32x4_t*>(reinterpret_cast<const bf16_t*>(ws + run.parts) +
+                                                     (int64_t(b) * 3 + p) * sp * sp + (ti * 32 + fr) * sp + 16 * q + 8 * h);
+    }
   for (int x = l0; x < l1; x += LS) {
     __syncthreads();
-    if (TALL) load_region<T>(M, run.ld_m, l, s, x, 0, LS, sp, lds, PITCH, run.vec_m);
-    else load_region<T>(M, run.ld_m, s, l, 0, x, sp, LS, lds, PITCH, run.vec_m);
+    if (TALL) reg.template store<NPM>(lds, PITCH, PLANE, LS, sp);
+    else reg.template store<NPM>(lds, PITCH, PLANE, sp, LS);
     __syncthreads();
+    if (x + LS < l1) fetch(x + LS);
     if (!busy) continue;
     for (int j = grp; j < LS / 32; j += groups) {
       if (x + 32 * j >= l1) break;
@@ -431,36 +582,15 @@ __global__ __launch_bounds__(256) void blocks_apply_kernel(Runs runs, const char
 #pragma unroll
       for (int v = 0; v < 16; ++v) acc[v] = 0.0f;
 #pragma unroll
-      for (int q = 0; q < NF; ++q) {
-        if ((BF ? 16 : 8) * q < sp) {
-          if constexpr (BF) {
-            u32x4_t fm;
-            if constexpr (TALL) {
-              fm = *reinterpret_cast<const u32x4_t*>(lds + (32 * j + fr) * PITCH + (2 * q + h) * 16);
-            } else {
-              const int gi = lane & 15, G = lane >> 4;
-              const char* base = lds + (q * 16 + 8 * (G >> 1) + (gi >> 2)) * PITCH + (32 * j + 16 * (G & 1) + 4 * (gi & 3)) * 2;
-              fm = gemm::read_tr_pair(base, base + 4 * PITCH);
-            }
+      for (int q = 0; q < 8; ++q) {
+        if (16 * q < sp) {
 #pragma unroll
-            for (int p = 0; p < NP; ++p) {
-              if (TALL) gemm::Mfma<bf16_t>::mma(tf[p][q], fm, acc);
-              else gemm::Mfma<bf16_t>::mma(fm, tf[p][q], acc);
-            }
-          } else {
-            f32x4_t fm;
-            if constexpr (TALL) {
-              fm = *reinterpret_cast<const f32x4_t*>(lds + (32 * j + fr) * PITCH + (2 * q + h) * 16);
-            } else {
+          for (int p = 0; p < NPM; ++p) {
+            const u32x4_t fm = fragment<!TALL>(lds + p * PLANE, PITCH, 32 * j, q, lane);
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                fm[k] = *reinterpret_cast<const float*>(lds + (8 * q + 4 * h + k) * PITCH + (32 * j + fr) * 4);
-            }
-            const f32x4_t t = __builtin_bit_cast(f32x4_t, tf[0][q]);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              if (TALL) acc = __builtin_amdgcn_mfma_f32_32x32x2f32(t[k], fm[k], acc, 0, 0, 0);
-              else acc = __builtin_amdgcn_mfma_f32_32x32x2f32(fm[k], t[k], acc, 0, 0, 0);
+            for (int k = 0; p + k < NPT; ++k) {
+              if (TALL) gemm::Mfma<bf16_t>::mma(tf[k][q], fm, acc);
+              else gemm::Mfma<bf16_t>::mma(fm, tf[k][q], acc);
             }
           }
         }
@@ -472,7 +602,7 @@ __global__ __launch_bounds__(256) void blocks_apply_kernel(Runs runs, const char
         const int first = 8 * q + 4 * h;
         const int row = TALL ? x + 32 * j + fr : ti * 32 + fr;
         const int col = TALL ? ti * 32 + first : x + 32 * j + first;
-        if (row < (TALL ? l : s)) write4<TO>(out + int64_t(row) * run.ld_out + col, v, (TALL ? s : l) - col, run.vec_out, e);
+        if (row < (TALL ? l : s)) write4<TO>(out + int64_t(row) * ld_out + col, v, (TALL ? s : l) - col, vec_out, e);
       }
     }
   }
@@ -482,11 +612,6 @@ __global__ __launch_bounds__(256) void blocks_apply_kernel(Runs runs, const char
 // host
 // ---------------------------------------------------------------------------
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
-struct Plan {
-  size_t bytes = 0;
-  int64_t blocks = 0;
-};
 
 bool valid_shape(const muon_block_problem& p) {
   if (p.rows < 0 || p.cols < 0 || p.count < 0) return false;
@@ -501,7 +626,7 @@ bool empty(const muon_block_problem& p) { return p.rows == 0 || p.cols == 0 || p
 // never shorter than 256 entries: each one writes and reads a whole partial Gram.
 void cut(Run& r, int64_t total_blocks) {
   const int64_t want = std::max<int64_t>(1, ceil_div(1024, std::max<int64_t>(total_blocks, 1)));
-  const int64_t slab = (r.kind & kF32) ? 32 : 64;
+  const int64_t slab = (r.kind & kF32) ? gram_slab<float>() : gram_slab<bf16_t>();
   int64_t chunks = std::min<int64_t>(want, ceil_div(r.l, 256));
   r.chunk = int(ceil_div(ceil_div(r.l, chunks), slab) * slab);
   r.chunks = int(ceil_div(r.l, r.chunk));
@@ -528,7 +653,7 @@ Run make_run(const muon_block_problem& p, int64_t total_blocks, size_t& bytes) {
   r.partials = int64_t(bytes);
   bytes += round_up(size_t(r.count) * r.chunks * tiles_of(int(nt)) * 4096, 256);
   r.parts = int64_t(bytes);
-  bytes += round_up(size_t(r.count) * sp * sp * ((r.kind & kF32) ? 4 : 6), 256);
+  bytes += round_up(size_t(r.count) * sp * sp * 6, 256);
   return r;
 }
 
@@ -543,7 +668,11 @@ template <typename T, typename TO, bool TALL>
 int launch_apply(const Runs& runs, const char* ws, const Epilogue& e, hipStream_t st) {
   int64_t units = 0;
   for (int i = 0; i < runs.n; ++i) units += int64_t(runs.r[i].count) * runs.r[i].units;
-  launch_kernel(blocks_apply_kernel<T, TO, TALL>, dim3(units), dim3(256), 0, st, runs, ws, e);
+  constexpr int LS = apply_slab<T>(), NPM = sizeof(T) == 2 ? 1 : sizeof(TO) == 2 ? 2 : 3;
+  constexpr int LDS = NPM * (TALL ? LS * row_pitch(256) : 128 * tr_pitch(2 * LS));
+  static std::atomic<uint64_t> configured{0};
+  if (gemm::set_lds_limit(blocks_apply_kernel<T, TO, TALL>, LDS, configured) != MUON_OK) return MUON_ELAUNCH;
+  launch_kernel(blocks_apply_kernel<T, TO, TALL>, dim3(units), dim3(256), LDS, st, runs, ws, e);
   return launch_status();
 }
 
@@ -593,14 +722,10 @@ int run_blocks(const muon_block_problem* probs, int nprobs, float a, float b, fl
   if (!aligned16(workspace)) return MUON_EALIGN;
   char* ws = static_cast<char*>(workspace);
   Run all[MUON_BLOCKS_MAX_PROBLEMS];
-  int n = 0, max_tiles = 0;
+  int n = 0;
   size_t bytes = 0;
   for (int i = 0; i < nprobs; ++i)
-    if (!empty(probs[i])) {
-      all[n] = make_run(probs[i], total, bytes);
-      max_tiles = std::max(max_tiles, tiles_of((all[n].s + 31) / 32));
-      ++n;
-    }
+    if (!empty(probs[i])) all[n++] = make_run(probs[i], total, bytes);
   for (int kind = 0; kind < 4; ++kind) {
     const int status = for_runs(all, n, [&](const Run& r) { return r.kind == kind; }, [&](const Runs& runs) {
       switch (kind) {
@@ -612,15 +737,22 @@ int run_blocks(const muon_block_problem* probs, int nprobs, float a, float b, fl
     });
     if (status != MUON_OK) return status;
   }
-  const int lds = 3 * max_tiles * kTileFloats * 4;
-  static std::atomic<uint64_t> configured{0};
-  if (gemm::set_lds_limit(blocks_poly_kernel, 3 * kMaxTiles * kTileFloats * 4, configured) != MUON_OK) return MUON_ELAUNCH;
-  int status = for_runs(all, n, [](const Run&) { return true; }, [&](const Runs& runs) {
-    int64_t blocks = 0;
-    for (int i = 0; i < runs.n; ++i) blocks += runs.r[i].count;
-    launch_kernel(blocks_poly_kernel, dim3(blocks), dim3(64 * max_tiles), lds, st, runs, ws, a, b, c, steps);
-    return launch_status();
-  });
+  const auto poly = [&](auto ny) {
+    constexpr int NY = decltype(ny)::value;
+    return for_runs(all, n, [](const Run& r) { return (r.s + 31) / 32 * 2 == NY; }, [&](const Runs& runs) {
+      int64_t blocks = 0;
+      for (int i = 0; i < runs.n; ++i) blocks += runs.r[i].count;
+      constexpr int LDS = SymLds<NY>::BUFFERS * SymLds<NY>::BYTES;
+      static std::atomic<uint64_t> configured{0};
+      if (gemm::set_lds_limit(blocks_poly_kernel<NY>, LDS, configured) != MUON_OK) return int(MUON_ELAUNCH);
+      launch_kernel(blocks_poly_kernel<NY>, dim3(blocks), dim3(64 * NY), LDS, st, runs, ws, a, b, c, steps);
+      return launch_status();
+    });
+  };
+  int status = poly(std::integral_constant<int, 2>{});
+  if (status == MUON_OK) status = poly(std::integral_constant<int, 4>{});
+  if (status == MUON_OK) status = poly(std::integral_constant<int, 6>{});
+  if (status == MUON_OK) status = poly(std::integral_constant<int, 8>{});
   if (status != MUON_OK) return status;
   for (int kind = 0; kind < 8; ++kind) {
     status = for_runs(all, n, [&](const Run& r) { return r.kind == (kind & 3) && r.out_f32 == (kind >> 2); }, [&](const Runs& runs) {
