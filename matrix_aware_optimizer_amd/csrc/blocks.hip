@@ -43,10 +43,14 @@ struct Run {
   int64_t ld_m, stride_m, ld_out, stride_out;
   int64_t partials, parts;   // byte offsets of its partial Grams and its T in the workspace
   int32_t s, l, count, chunk, chunks, slabs, units;   // chunk: k-values per gram unit; slabs per apply unit
-  int32_t vec_m, vec_out, kind;   // kind: kTall | kF32
+  int32_t vec_m, vec_out, kind;   // kind: kTall | kF32 | kBig
   int32_t out_f32;
 };
-enum { kTall = 1, kF32 = 2 };
+enum { kTall = 1, kF32 = 2, kBig = 4 };   // kBig: a short side over 64
+template <typename T, bool TALL, bool BIG>
+constexpr int kind_of() {
+  return (TALL ? kTall : 0) | (sizeof(T) == 4 ? kF32 : 0) | (BIG ? kBig : 0);
+}
 
 struct Runs {
   Run r[kMaxRuns];
@@ -175,11 +179,12 @@ __device__ __forceinline__ u32x4_t fragment(const char* plane, int pitch, int fi
 // ---------------------------------------------------------------------------
 template <typename T> constexpr int gram_slab() { return 128 / sizeof(T); }   // k-values staged at a time
 
-template <typename T, bool TALL>
+template <typename T, bool TALL, bool BIG>
 __global__ __launch_bounds__(256) void blocks_gram_kernel(Runs runs, char* ws) {
-  constexpr int SLAB = gram_slab<T>(), NP = sizeof(T) == 2 ? 1 : 3;
-  constexpr int PITCH = TALL ? tr_pitch(256) : row_pitch(2 * SLAB);   // tall [SLAB][s], wide [s][SLAB]
-  constexpr int PLANE = (TALL ? SLAB : 128) * PITCH;
+  constexpr int SLAB = gram_slab<T>(), NP = sizeof(T) == 2 ? 1 : 3, SIDE = BIG ? 128 : 64;
+  constexpr int PITCH = TALL ? tr_pitch(2 * SIDE) : row_pitch(2 * SLAB);   // tall [SLAB][s], wide [s][SLAB]
+  constexpr int PLANE = (TALL ? SLAB : SIDE) * PITCH;
+  constexpr int NA = BIG ? 3 : 1;   // lower tiles of a wave
   __shared__ __attribute__((aligned(16))) char lds[NP * PLANE];
   int u = blockIdx.x;
   const Run& run = find_run(runs, u, 0);
@@ -191,12 +196,12 @@ __global__ __launch_bounds__(256) void blocks_gram_kernel(Runs runs, char* ws) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int nlow = tiles_of(nt);
   const int k0 = chunk * run.chunk, k1 = min(l, k0 + run.chunk);
-  f32x16_t acc[3];
+  f32x16_t acc[NA];
 #pragma unroll
-  for (int q = 0; q < 3; ++q)
+  for (int q = 0; q < NA; ++q)
 #pragma unroll
     for (int v = 0; v < 16; ++v) acc[q][v] = 0.0f;
-  Region<T, 4> reg;
+  Region<T, BIG ? 4 : 2> reg;
   auto fetch = [&](int k) __attribute__((always_inline)) {
     if (TALL) reg.fetch(M, ld, k1, s, k, 0, SLAB, sp, vec);
     else reg.fetch(M, ld, s, k1, 0, k, sp, SLAB, vec);
@@ -209,7 +214,7 @@ __global__ __launch_bounds__(256) void blocks_gram_kernel(Runs runs, char* ws) {
     __syncthreads();
     if (k + SLAB < k1) fetch(k + SLAB);
 #pragma unroll
-    for (int q = 0; q < 3; ++q) {
+    for (int q = 0; q < NA; ++q) {
       const int t = wave + 4 * q;
       if (t < nlow) {
         int ti, tj;
@@ -232,7 +237,7 @@ __global__ __launch_bounds__(256) void blocks_gram_kernel(Runs runs, char* ws) {
   }
   float* dst = reinterpret_cast<float*>(ws + run.partials) + int64_t(u) * nlow * 1024;
 #pragma unroll
-  for (int q = 0; q < 3; ++q) {
+  for (int q = 0; q < NA; ++q) {
     const int t = wave + 4 * q;
     if (t < nlow)
 #pragma unroll
@@ -258,21 +263,27 @@ struct SymOperand {
   bf16x8_t p[kParts][NY / 2];
 };
 
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+typedef float f32x2_t __attribute__((ext_vector_type(2)));
+
 template <int NY>
 __device__ __forceinline__ void split_strip(const f32x4_t (&v)[NY], SymOperand<NY>& o) {
 #pragma unroll
   for (int t = 0; t < NY / 2; ++t) {
-    float x[8];
+    uint32_t w[kParts][4];
 #pragma unroll
-    for (int q = 0; q < 8; ++q) x[q] = v[2 * t + (q >> 2)][q & 3];
+    for (int q = 0; q < 4; ++q) {
+      f32x2_t x = {v[2 * t + (q >> 1)][2 * (q & 1)], v[2 * t + (q >> 1)][2 * (q & 1) + 1]};
+#pragma unroll
+      for (int p = 0; p < kParts; ++p) {
+        w[p][q] = __builtin_bit_cast(uint32_t, __builtin_convertvector(x, bf16x2_t));
+        x[0] -= __uint_as_float(w[p][q] << 16);
+        x[1] -= __uint_as_float(w[p][q] & 0xffff0000u);
+      }
+    }
 #pragma unroll
     for (int p = 0; p < kParts; ++p)
-#pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        const __bf16 h = static_cast<__bf16>(x[q]);
-        o.p[p][t][q] = h;
-        x[q] -= static_cast<float>(h);
-      }
+      o.p[p][t] = __builtin_bit_cast(bf16x8_t, make_uint4(w[p][0], w[p][1], w[p][2], w[p][3]));
   }
 }
 
@@ -313,45 +324,59 @@ __device__ __forceinline__ void get_transposed(const char* buf, int wave, int la
   }
 }
 
-// out = S o, S in LDS.  The parts of the next 16 x 32 piece of S are read while the
-// current one is multiplied.
-template <int NY>
-__device__ __forceinline__ void sym_product(const char* buf, int lane, const SymOperand<NY>& o, f32x4_t (&out)[NY]) {
-  constexpr int NT = NY / 2;
+// out = S o for the wave's strips, S in LDS.  The parts of the pieces of S are read DEPTH
+// pieces (16 x 32) ahead of their products.
+template <int NY, int NS>
+__device__ __forceinline__ void sym_product(const char* buf, int lane, const SymOperand<NY> (&o)[NS],
+                                            f32x4_t (&out)[NS][NY]) {
+  constexpr int NT = NY / 2, PIECES = NY * NT, DEPTH = PIECES < 4 ? 1 : 3;
   const char* row = buf + (lane & 15) * SymLds<NY>::PITCH + 16 * (lane >> 4);
-  bf16x8_t f[2][kParts];
+  bf16x8_t f[DEPTH + 1][kParts];
   auto read = [&](int k) __attribute__((always_inline)) {
 #pragma unroll
     for (int p = 0; p < kParts; ++p)
-      f[k & 1][p] = *reinterpret_cast<const bf16x8_t*>(row + (k / NT) * 16 * SymLds<NY>::PITCH + (k % NT) * 64 +
-                                                       p * SymLds<NY>::PLANE);
+      f[k % (DEPTH + 1)][p] = *reinterpret_cast<const bf16x8_t*>(row + (k / NT) * 16 * SymLds<NY>::PITCH + (k % NT) * 64 +
+                                                                 p * SymLds<NY>::PLANE);
   };
-  read(0);
+#pragma unroll
+  for (int k = 0; k < DEPTH; ++k) read(k);
 #pragma unroll
   for (int y = 0; y < NY; ++y) {
-    f32x4_t acc = {0.0f, 0.0f, 0.0f, 0.0f}, low = {0.0f, 0.0f, 0.0f, 0.0f};
+    f32x4_t acc[NS], low[NS];
+#pragma unroll
+    for (int i = 0; i < NS; ++i) acc[i] = low[i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       const int k = y * NT + t;
-      if (k + 1 < NY * NT) read(k + 1);
-      const bf16x8_t(&s)[kParts] = f[k & 1];
+      if (k + DEPTH < PIECES) read(k + DEPTH);
+      const bf16x8_t(&s)[kParts] = f[k % (DEPTH + 1)];
 #pragma unroll
       for (int p = 0; p < kParts; ++p)
 #pragma unroll
-        for (int r = 0; p + r < kParts; ++r) {
-          f32x4_t& to = (p + r) == 2 ? low : acc;   // two chains of three
-          to = __builtin_amdgcn_mfma_f32_16x16x32_bf16(s[p], o.p[r][t], to, 0, 0, 0);
-        }
+        for (int r = 0; p + r < kParts; ++r)
+#pragma unroll
+          for (int i = 0; i < NS; ++i) {
+            f32x4_t& to = (p + r) == 2 ? low[i] : acc[i];   // two chains of three
+            to = __builtin_amdgcn_mfma_f32_16x16x32_bf16(s[p], o[i].p[r][t], to, 0, 0, 0);
+          }
       __builtin_amdgcn_sched_barrier(0);
     }
-    out[y] = acc + low;
+#pragma unroll
+    for (int i = 0; i < NS; ++i) out[i][y] = acc[i] + low[i];
   }
 }
 
+// Strips of a wave.  One gives the most waves; at s > 96 eight waves would each read all
+// of S for every product, as long as their matrix instructions take, so four waves take
+// two strips each.
+template <int NY> constexpr int strips() { return NY == 8 ? 2 : 1; }
+
 template <int NY>
-__global__ __launch_bounds__(64 * NY) void blocks_poly_kernel(Runs runs, char* ws, float a, float b, float c, int steps) {
+__global__ __launch_bounds__(64 * NY / strips<NY>()) void blocks_poly_kernel(Runs runs, char* ws, float a, float b, float c,
+                                                                             int steps) {
   extern __shared__ __attribute__((aligned(16))) char sm[];
-  __shared__ double trace[NY];
+  constexpr int NS = strips<NY>(), W = NY / NS;
+  __shared__ double trace[W];
   constexpr bool SHARED = SymLds<NY>::BUFFERS == 1;
   char* buf = sm;                                        // what is written next
   char* other = SHARED ? sm : sm + SymLds<NY>::BYTES;
@@ -360,63 +385,80 @@ __global__ __launch_bounds__(64 * NY) void blocks_poly_kernel(Runs runs, char* w
   constexpr int nlow = tiles_of(NY / 2), sp = 16 * NY;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
-  const int x = 16 * wave + r;                       // this lane's column
-  f32x4_t A[NY], T[NY];
+  f32x4_t A[NS][NY], T[NS][NY];
+  // f(i, y): the wave's strip i (strip NS wave + i of the matrix, column 16 strip + r of this
+  // lane), rows 16 y + 4 g .. + 3
+  auto each = [&](auto&& f) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < NS; ++i)
+#pragma unroll
+      for (int y = 0; y < NY; ++y) f(i, y);
+  };
+  auto column = [&](int i) { return 16 * (NS * wave + i) + r; };
+  // the entry v of (i, y) lies on the diagonal
+  auto diag = [&](int i, int y, int v) { return 16 * y + 4 * g + v == column(i); };
   {
     // the partial Grams are lower 32 x 32 tiles as they lay in the accumulators: entry
     // (row i, column j) of a tile is value 4 (i / 8) + i % 4 of lane j + 32 (i / 4 % 2)
     const int chunks = run.chunks;
     const float* src = reinterpret_cast<const float*>(ws + run.partials) + int64_t(u) * chunks * nlow * 1024;
+    auto load = [&](const float* at, int i, int y) __attribute__((always_inline)) {
+      const int X = (NS * wave + i) >> 1, j = column(i) & 31, Y = y >> 1, i0 = 16 * (y & 1) + 4 * g;
+      f32x4_t w;
+      if (Y >= X) {
+        at += (Y * (Y + 1) / 2 + X) * 1024 + 4 * (i0 >> 3) * 64 + j + 32 * ((i0 >> 2) & 1);
 #pragma unroll
-    for (int y = 0; y < NY; ++y) A[y] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-    const int X = wave >> 1, j = x & 31;
-    for (int k = 0; k < chunks; ++k) {
-#pragma unroll
-      for (int y = 0; y < NY; ++y) {
-        const int Y = y >> 1, i0 = 16 * (y & 1) + 4 * g;   // rows i0 .. i0 + 3 of tile row Y
-        f32x4_t w;
-        if (Y >= X) {
-          const float* at = src + (Y * (Y + 1) / 2 + X) * 1024 + 4 * (i0 >> 3) * 64 + j + 32 * ((i0 >> 2) & 1);
-#pragma unroll
-          for (int v = 0; v < 4; ++v) w[v] = at[64 * v];
-        } else {
-          // above the diagonal: the mirrored entry, row j of tile (X, Y), columns i0 ..
-          w = *reinterpret_cast<const f32x4_t*>(src + (X * (X + 1) / 2 + Y) * 1024 + (4 * (j >> 3) + (j & 3)) * 64 + i0 +
-                                                32 * ((j >> 2) & 1));
-        }
-        A[y] += w;
+        for (int v = 0; v < 4; ++v) w[v] = at[64 * v];
+      } else {
+        // above the diagonal: the mirrored entry, row j of tile (X, Y), columns i0 ..
+        w = *reinterpret_cast<const f32x4_t*>(at + (X * (X + 1) / 2 + Y) * 1024 + (4 * (j >> 3) + (j & 3)) * 64 + i0 +
+                                              32 * ((j >> 2) & 1));
       }
-      src += nlow * 1024;
+      return w;
+    };
+    each([&](int i, int y) __attribute__((always_inline)) { A[i][y] = load(src, i, y); });
+    // in order, the loads of chunk k + 1 under way while chunk k is added
+    if (chunks > 1) {
+      f32x4_t next[NS][NY];
+      each([&](int i, int y) __attribute__((always_inline)) { next[i][y] = load(src + nlow * 1024, i, y); });
+      for (int k = 1; k < chunks; ++k) {
+        f32x4_t cur[NS][NY];
+        each([&](int i, int y) __attribute__((always_inline)) { cur[i][y] = next[i][y]; });
+        const float* at = src + int64_t(min(k + 1, chunks - 1)) * nlow * 1024;
+        each([&](int i, int y) __attribute__((always_inline)) { next[i][y] = load(at, i, y); });
+        each([&](int i, int y) __attribute__((always_inline)) { A[i][y] += cur[i][y]; });
+      }
     }
   }
-  // this lane's entry y, v lies on the diagonal
-  auto diag = [&](int y, int v) { return 16 * y + 4 * g + v == x; };
   double mine = 0.0;
+  each([&](int i, int y) __attribute__((always_inline)) {
 #pragma unroll
-  for (int y = 0; y < NY; ++y)
-#pragma unroll
-    for (int v = 0; v < 4; ++v) mine += diag(y, v) ? double(A[y][v]) : 0.0;
+    for (int v = 0; v < 4; ++v) mine += diag(i, y, v) ? double(A[i][y][v]) : 0.0;
+  });
   mine = wave_sum(mine);
   if (lane == 0) trace[wave] = mine;
   __syncthreads();
   double total = 0.0;
 #pragma unroll
-  for (int i = 0; i < NY; ++i) total += trace[i];
+  for (int i = 0; i < W; ++i) total += trace[i];
   // a block of zeros gives U = 0
   const float inv = total == 0.0 ? 0.0f : float(1.0 / total);
   const float root = total == 0.0 ? 0.0f : float(1.0 / sqrt(total));
+  each([&](int i, int y) __attribute__((always_inline)) {
+    A[i][y] *= inv;
 #pragma unroll
-  for (int y = 0; y < NY; ++y)
+    for (int v = 0; v < 4; ++v) T[i][y][v] = diag(i, y, v) ? 1.0f : 0.0f;
+  });
+  auto split = [&](const f32x4_t (&v)[NS][NY], SymOperand<NY> (&o)[NS]) __attribute__((always_inline)) {
 #pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      A[y][v] *= inv;
-      T[y][v] = diag(y, v) ? 1.0f : 0.0f;
-    }
+    for (int i = 0; i < NS; ++i) split_strip<NY>(v[i], o[i]);
+  };
   // one buffer: everybody is done reading before it is written; two: the one written now
   // was read before the last barrier
-  auto put = [&](const SymOperand<NY>& o) __attribute__((always_inline)) {
+  auto put = [&](const SymOperand<NY> (&o)[NS]) __attribute__((always_inline)) {
     if (SHARED) __syncthreads();
-    put_strip<NY>(buf, wave, lane, o);
+#pragma unroll
+    for (int i = 0; i < NS; ++i) put_strip<NY>(buf, NS * wave + i, lane, o[i]);
     __syncthreads();
     char* const w = buf;
     buf = other;
@@ -424,62 +466,58 @@ __global__ __launch_bounds__(64 * NY) void blocks_poly_kernel(Runs runs, char* w
   };
   for (int it = 0; it < steps; ++it) {
     const bool last = it == steps - 1;
-    SymOperand<NY> oA;
-    f32x4_t P[NY];
-    split_strip<NY>(A, oA);
+    SymOperand<NY> oA[NS];
+    f32x4_t P[NS][NY];
+    split(A, oA);
     if (it > 0) {
       put(oA);
-      get_transposed<NY>(other, wave, lane, P);
 #pragma unroll
-      for (int y = 0; y < NY; ++y) A[y] = 0.5f * (A[y] + P[y]);
-      split_strip<NY>(A, oA);
+      for (int i = 0; i < NS; ++i) get_transposed<NY>(other, NS * wave + i, lane, P[i]);
+      each([&](int i, int y) __attribute__((always_inline)) { A[i][y] = 0.5f * (A[i][y] + P[i][y]); });
+      split(A, oA);
     }
     if (c != 0.0f) {
       put(oA);
-      sym_product<NY>(other, lane, oA, P);               // A A
+      sym_product<NY, NS>(other, lane, oA, P);               // A A
     } else {
-#pragma unroll
-      for (int y = 0; y < NY; ++y) P[y] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+      each([&](int i, int y) __attribute__((always_inline)) { P[i][y] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f}; });
     }
+    each([&](int i, int y) __attribute__((always_inline)) {
 #pragma unroll
-    for (int y = 0; y < NY; ++y)
-#pragma unroll
-      for (int v = 0; v < 4; ++v) P[y][v] = fmaf(c, P[y][v], fmaf(b, A[y][v], diag(y, v) ? a : 0.0f));
-    SymOperand<NY> o;
-    split_strip<NY>(P, o);
+      for (int v = 0; v < 4; ++v) P[i][y][v] = fmaf(c, P[i][y][v], fmaf(b, A[i][y][v], diag(i, y, v) ? a : 0.0f));
+    });
+    SymOperand<NY> o[NS];
+    split(P, o);
     if (it == 0) {
-#pragma unroll
-      for (int y = 0; y < NY; ++y) T[y] = P[y];
+      each([&](int i, int y) __attribute__((always_inline)) { T[i][y] = P[i][y]; });
       if (last) break;
       put(o);
     } else {
       put(o);
-      split_strip<NY>(T, o);
-      sym_product<NY>(other, lane, o, T);                // T' = P T
+      split(T, o);
+      sym_product<NY, NS>(other, lane, o, T);                // T' = P T
       if (last) break;
     }
-    sym_product<NY>(other, lane, oA, P);                 // P A
-    split_strip<NY>(P, o);
-    sym_product<NY>(other, lane, o, A);                  // A' = P (P A)
+    sym_product<NY, NS>(other, lane, oA, P);                 // P A
+    split(P, o);
+    sym_product<NY, NS>(other, lane, o, A);                  // A' = P (P A)
   }
   // T / |M|_F in three bf16 parts, rows of [part][sp][sp]
-  bf16_t* dst = reinterpret_cast<bf16_t*>(ws + run.parts) + int64_t(u) * 3 * sp * sp + x * sp + 4 * g;
+  bf16_t* dst = reinterpret_cast<bf16_t*>(ws + run.parts) + int64_t(u) * 3 * sp * sp + 4 * g;
+  each([&](int i, int y) __attribute__((always_inline)) {
+    f32x2_t lo = {T[i][y][0] * root, T[i][y][1] * root}, hi = {T[i][y][2] * root, T[i][y][3] * root};
 #pragma unroll
-  for (int y = 0; y < NY; ++y) {
-    float w[4];
-#pragma unroll
-    for (int v = 0; v < 4; ++v) w[v] = T[y][v] * root;
-#pragma unroll
-    for (int p = 0; p < 3; ++p) {
-      uint32_t h[4];
-#pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        h[v] = f32_to_bf16(w[v]);
-        w[v] -= __uint_as_float(h[v] << 16);
-      }
-      *reinterpret_cast<uint2*>(dst + p * sp * sp + 16 * y) = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+    for (int p = 0; p < kParts; ++p) {
+      uint2 w;
+      w.x = __builtin_bit_cast(uint32_t, __builtin_convertvector(lo, bf16x2_t));
+      w.y = __builtin_bit_cast(uint32_t, __builtin_convertvector(hi, bf16x2_t));
+      lo[0] -= __uint_as_float(w.x << 16);
+      lo[1] -= __uint_as_float(w.x & 0xffff0000u);
+      hi[0] -= __uint_as_float(w.y << 16);
+      hi[1] -= __uint_as_float(w.y & 0xffff0000u);
+      *reinterpret_cast<uint2*>(dst + p * sp * sp + column(i) * sp + 16 * y) = w;
     }
-  }
+  });
 }
 
 // ---------------------------------------------------------------------------
@@ -531,13 +569,13 @@ __device__ __forceinline__ void write4(TO* dst, const float v[4], int valid, boo
 
 template <typename T> constexpr int apply_slab() { return sizeof(T) == 2 ? 128 : 64; }   // long-side entries at a time
 
-template <typename T, typename TO, bool TALL>
+template <typename T, typename TO, bool TALL, bool BIG>
 __global__ __launch_bounds__(256) void blocks_apply_kernel(Runs runs, const char* ws, Epilogue e) {
-  constexpr int LS = apply_slab<T>();
+  constexpr int LS = apply_slab<T>(), SIDE = BIG ? 128 : 64, NQ = SIDE / 16;
   constexpr int NPT = sizeof(TO) == 2 ? 2 : 3;                 // bf16 parts of T
   constexpr int NPM = sizeof(T) == 2 ? 1 : NPT;                // and of M
-  constexpr int PITCH = TALL ? row_pitch(256) : tr_pitch(2 * LS);   // tall [LS][s], wide [s][LS]
-  constexpr int PLANE = (TALL ? LS : 128) * PITCH;
+  constexpr int PITCH = TALL ? row_pitch(2 * SIDE) : tr_pitch(2 * LS);   // tall [LS][s], wide [s][LS]
+  constexpr int PLANE = (TALL ? LS : SIDE) * PITCH;
   extern __shared__ __attribute__((aligned(16))) char lds[];   // NPM planes
   int u = blockIdx.x;
   const Run& run = find_run(runs, u, 2);
@@ -553,17 +591,17 @@ __global__ __launch_bounds__(256) void blocks_apply_kernel(Runs runs, const char
   const int groups = 4 / nt, ti = wave % nt, grp = wave / nt;
   const bool busy = grp < groups;
   const int l0 = unit * run.slabs * LS, l1 = min(l, l0 + run.slabs * LS);
-  Region<T, 8> reg;
+  Region<T, BIG ? 8 : 4> reg;
   auto fetch = [&](int x) __attribute__((always_inline)) {
     if (TALL) reg.fetch(M, ld, l, s, x, 0, LS, sp, vec);
     else reg.fetch(M, ld, s, l, 0, x, sp, LS, vec);
   };
   fetch(l0);
-  u32x4_t tf[NPT][8];
+  u32x4_t tf[NPT][NQ];
 #pragma unroll
   for (int p = 0; p < NPT; ++p)
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
+    for (int q = 0; q < NQ; ++q) {
       tf[p][q] = u32x4_t{0, 0, 0, 0};
       if (16 * q < sp && busy)
         tf[p][q] = *reinterpret_cast<const u32x4_t*>(reinterpret_cast<const bf16_t*>(ws + run.parts) +
@@ -582,7 +620,7 @@ __global__ __launch_bounds__(256) void blocks_apply_kernel(Runs runs, const char
 #pragma unroll
       for (int v = 0; v < 16; ++v) acc[v] = 0.0f;
 #pragma unroll
-      for (int q = 0; q < 8; ++q) {
+      for (int q = 0; q < NQ; ++q) {
         if (16 * q < sp) {
 #pragma unroll
           for (int p = 0; p < NPM; ++p) {
@@ -643,7 +681,7 @@ Run make_run(const muon_block_problem& p, int64_t total_blocks, size_t& bytes) {
   r.M = p.M; r.out = p.out;
   r.ld_m = p.ld_m; r.stride_m = p.stride_m; r.ld_out = p.ld_out; r.stride_out = p.stride_out;
   r.s = int(std::min(p.rows, p.cols)); r.l = int(std::max(p.rows, p.cols)); r.count = int(p.count);
-  r.kind = (tall ? kTall : 0) | (p.m_dtype == MUON_F32 ? kF32 : 0);
+  r.kind = (tall ? kTall : 0) | (p.m_dtype == MUON_F32 ? kF32 : 0) | (r.s > 64 ? kBig : 0);
   r.out_f32 = p.out_dtype == MUON_F32;
   const int64_t em = p.m_dtype == MUON_F32 ? 4 : 8;
   r.vec_m = p.ld_m % em == 0 && (p.count <= 1 || p.stride_m % em == 0);
@@ -664,23 +702,24 @@ int64_t count_blocks(const muon_block_problem* probs, int n) {
   return total;
 }
 
-template <typename T, typename TO, bool TALL>
+template <typename T, typename TO, bool TALL, bool BIG>
 int launch_apply(const Runs& runs, const char* ws, const Epilogue& e, hipStream_t st) {
   int64_t units = 0;
   for (int i = 0; i < runs.n; ++i) units += int64_t(runs.r[i].count) * runs.r[i].units;
   constexpr int LS = apply_slab<T>(), NPM = sizeof(T) == 2 ? 1 : sizeof(TO) == 2 ? 2 : 3;
-  constexpr int LDS = NPM * (TALL ? LS * row_pitch(256) : 128 * tr_pitch(2 * LS));
+  constexpr int SIDE = BIG ? 128 : 64;
+  constexpr int LDS = NPM * (TALL ? LS * row_pitch(2 * SIDE) : SIDE * tr_pitch(2 * LS));
   static std::atomic<uint64_t> configured{0};
-  if (gemm::set_lds_limit(blocks_apply_kernel<T, TO, TALL>, LDS, configured) != MUON_OK) return MUON_ELAUNCH;
-  launch_kernel(blocks_apply_kernel<T, TO, TALL>, dim3(units), dim3(256), LDS, st, runs, ws, e);
+  if (gemm::set_lds_limit(blocks_apply_kernel<T, TO, TALL, BIG>, LDS, configured) != MUON_OK) return MUON_ELAUNCH;
+  launch_kernel(blocks_apply_kernel<T, TO, TALL, BIG>, dim3(units), dim3(256), LDS, st, runs, ws, e);
   return launch_status();
 }
 
-template <typename T, bool TALL>
+template <typename T, bool TALL, bool BIG>
 int launch_gram(const Runs& runs, char* ws, hipStream_t st) {
   int64_t units = 0;
   for (int i = 0; i < runs.n; ++i) units += int64_t(runs.r[i].count) * runs.r[i].chunks;
-  launch_kernel(blocks_gram_kernel<T, TALL>, dim3(units), dim3(256), 0, st, runs, ws);
+  launch_kernel(blocks_gram_kernel<T, TALL, BIG>, dim3(units), dim3(256), 0, st, runs, ws);
   return launch_status();
 }
 
@@ -726,17 +765,37 @@ int run_blocks(const muon_block_problem* probs, int nprobs, float a, float b, fl
   size_t bytes = 0;
   for (int i = 0; i < nprobs; ++i)
     if (!empty(probs[i])) all[n++] = make_run(probs[i], total, bytes);
-  for (int kind = 0; kind < 4; ++kind) {
-    const int status = for_runs(all, n, [&](const Run& r) { return r.kind == kind; }, [&](const Runs& runs) {
-      switch (kind) {
-        case 0: return launch_gram<bf16_t, false>(runs, ws, st);
-        case kTall: return launch_gram<bf16_t, true>(runs, ws, st);
-        case kF32: return launch_gram<float, false>(runs, ws, st);
-        default: return launch_gram<float, true>(runs, ws, st);
-      }
-    });
+  // gram and apply: one launch per type, orientation and half of the range of short sides
+  const auto gram = [&](auto t_c, auto tall_c, auto big_c) {
+    using T = decltype(t_c);
+    constexpr bool TALL = decltype(tall_c)::value, BIG = decltype(big_c)::value;
+    return for_runs(all, n, [](const Run& r) { return r.kind == kind_of<T, TALL, BIG>(); },
+                    [&](const Runs& runs) { return launch_gram<T, TALL, BIG>(runs, ws, st); });
+  };
+  const auto apply = [&](auto t_c, auto tall_c, auto big_c) {
+    using T = decltype(t_c);
+    constexpr bool TALL = decltype(tall_c)::value, BIG = decltype(big_c)::value;
+    const int status = for_runs(all, n, [](const Run& r) { return r.kind == kind_of<T, TALL, BIG>() && !r.out_f32; },
+                                [&](const Runs& runs) { return launch_apply<T, bf16_t, TALL, BIG>(runs, ws, e, st); });
     if (status != MUON_OK) return status;
-  }
+    return for_runs(all, n, [](const Run& r) { return r.kind == kind_of<T, TALL, BIG>() && r.out_f32; },
+                    [&](const Runs& runs) { return launch_apply<T, float, TALL, BIG>(runs, ws, e, st); });
+  };
+  const auto every_kind = [&](const auto& f) {
+    using Yes = std::true_type;
+    using No = std::false_type;
+    int status = f(bf16_t{}, No{}, No{});
+    if (status == MUON_OK) status = f(bf16_t{}, No{}, Yes{});
+    if (status == MUON_OK) status = f(bf16_t{}, Yes{}, No{});
+    if (status == MUON_OK) status = f(bf16_t{}, Yes{}, Yes{});
+    if (status == MUON_OK) status = f(float{}, No{}, No{});
+    if (status == MUON_OK) status = f(float{}, No{}, Yes{});
+    if (status == MUON_OK) status = f(float{}, Yes{}, No{});
+    if (status == MUON_OK) status = f(float{}, Yes{}, Yes{});
+    return status;
+  };
+  int status = every_kind(gram);
+  if (status != MUON_OK) return status;
   const auto poly = [&](auto ny) {
     constexpr int NY = decltype(ny)::value;
     return for_runs(all, n, [](const Run& r) { return (r.s + 31) / 32 * 2 == NY; }, [&](const Runs& runs) {
@@ -745,31 +804,16 @@ int run_blocks(const muon_block_problem* probs, int nprobs, float a, float b, fl
       constexpr int LDS = SymLds<NY>::BUFFERS * SymLds<NY>::BYTES;
       static std::atomic<uint64_t> configured{0};
       if (gemm::set_lds_limit(blocks_poly_kernel<NY>, LDS, configured) != MUON_OK) return int(MUON_ELAUNCH);
-      launch_kernel(blocks_poly_kernel<NY>, dim3(blocks), dim3(64 * NY), LDS, st, runs, ws, a, b, c, steps);
+      launch_kernel(blocks_poly_kernel<NY>, dim3(blocks), dim3(64 * NY / strips<NY>()), LDS, st, runs, ws, a, b, c, steps);
       return launch_status();
     });
   };
-  int status = poly(std::integral_constant<int, 2>{});
+  status = poly(std::integral_constant<int, 2>{});
   if (status == MUON_OK) status = poly(std::integral_constant<int, 4>{});
   if (status == MUON_OK) status = poly(std::integral_constant<int, 6>{});
   if (status == MUON_OK) status = poly(std::integral_constant<int, 8>{});
   if (status != MUON_OK) return status;
-  for (int kind = 0; kind < 8; ++kind) {
-    status = for_runs(all, n, [&](const Run& r) { return r.kind == (kind & 3) && r.out_f32 == (kind >> 2); }, [&](const Runs& runs) {
-      switch (kind) {
-        case 0: return launch_apply<bf16_t, bf16_t, false>(runs, ws, e, st);
-        case 1: return launch_apply<bf16_t, bf16_t, true>(runs, ws, e, st);
-        case 2: return launch_apply<float, bf16_t, false>(runs, ws, e, st);
-        case 3: return launch_apply<float, bf16_t, true>(runs, ws, e, st);
-        case 4: return launch_apply<bf16_t, float, false>(runs, ws, e, st);
-        case 5: return launch_apply<bf16_t, float, true>(runs, ws, e, st);
-        case 6: return launch_apply<float, float, false>(runs, ws, e, st);
-        default: return launch_apply<float, float, true>(runs, ws, e, st);
-      }
-    });
-    if (status != MUON_OK) return status;
-  }
-  return MUON_OK;
+  return every_kind(apply);
 }
 
 }  // namespace
