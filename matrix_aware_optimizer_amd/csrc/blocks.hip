@@ -82,6 +82,17 @@ __device__ __forceinline__ const Run& find_run(const Runs& runs, int& u, int uni
   return runs.r[k];
 }
 
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+typedef float f32x2_t __attribute__((ext_vector_type(2)));
+
+// the bf16 values nearest to x, packed; x becomes what they leave (exact)
+__device__ __forceinline__ uint32_t leading_part(f32x2_t& x) {
+  const uint32_t w = __builtin_bit_cast(uint32_t, __builtin_convertvector(x, bf16x2_t));
+  x[0] -= __uint_as_float(w << 16);
+  x[1] -= __uint_as_float(w & 0xffff0000u);
+  return w;
+}
+
 // A region of a row-major matrix on its way from memory to LDS: rows [r0, r0 + NR),
 // columns [c0, c0 + NC), entries outside rows x cols as zeros.  fetch() leaves it in
 // registers (LD 16-byte pieces per thread, 256 threads), so that it is under way while
@@ -137,16 +148,12 @@ struct Region {
         if constexpr (sizeof(T) == 2) {
           *reinterpret_cast<uint4*>(dst) = w[q];
         } else {
-          float x[4] = {__uint_as_float(w[q].x), __uint_as_float(w[q].y), __uint_as_float(w[q].z), __uint_as_float(w[q].w)};
+          f32x2_t lo = {__uint_as_float(w[q].x), __uint_as_float(w[q].y)};
+          f32x2_t hi = {__uint_as_float(w[q].z), __uint_as_float(w[q].w)};
 #pragma unroll
           for (int p = 0; p < NP; ++p) {
-            uint32_t b[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              b[k] = f32_to_bf16(x[k]);
-              x[k] -= __uint_as_float(b[k] << 16);
-            }
-            *reinterpret_cast<uint2*>(dst + p * plane) = make_uint2(b[0] | (b[1] << 16), b[2] | (b[3] << 16));
+            const uint32_t a = leading_part(lo), b = leading_part(hi);
+            *reinterpret_cast<uint2*>(dst + p * plane) = make_uint2(a, b);
           }
         }
       }
@@ -263,9 +270,6 @@ struct SymOperand {
   bf16x8_t p[kParts][NY / 2];
 };
 
-typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
-typedef float f32x2_t __attribute__((ext_vector_type(2)));
-
 template <int NY>
 __device__ __forceinline__ void split_strip(const f32x4_t (&v)[NY], SymOperand<NY>& o) {
 #pragma unroll
@@ -275,11 +279,7 @@ __device__ __forceinline__ void split_strip(const f32x4_t (&v)[NY], SymOperand<N
     for (int q = 0; q < 4; ++q) {
       f32x2_t x = {v[2 * t + (q >> 1)][2 * (q & 1)], v[2 * t + (q >> 1)][2 * (q & 1) + 1]};
 #pragma unroll
-      for (int p = 0; p < kParts; ++p) {
-        w[p][q] = __builtin_bit_cast(uint32_t, __builtin_convertvector(x, bf16x2_t));
-        x[0] -= __uint_as_float(w[p][q] << 16);
-        x[1] -= __uint_as_float(w[p][q] & 0xffff0000u);
-      }
+      for (int p = 0; p < kParts; ++p) w[p][q] = leading_part(x);
     }
 #pragma unroll
     for (int p = 0; p < kParts; ++p)
@@ -376,7 +376,6 @@ __global__ __launch_bounds__(64 * NY / strips<NY>()) void blocks_poly_kernel(Run
                                                                              int steps) {
   extern __shared__ __attribute__((aligned(16))) char sm[];
   constexpr int NS = strips<NY>(), W = NY / NS;
-  __shared__ double trace[W];
   constexpr bool SHARED = SymLds<NY>::BUFFERS == 1;
   char* buf = sm;                                        // what is written next
   char* other = SHARED ? sm : sm + SymLds<NY>::BYTES;
@@ -386,6 +385,7 @@ __global__ __launch_bounds__(64 * NY / strips<NY>()) void blocks_poly_kernel(Run
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
   f32x4_t A[NS][NY], T[NS][NY];
+  double total = 0.0;                                    // |M|_F^2
   // f(i, y): the wave's strip i (strip NS wave + i of the matrix, column 16 strip + r of this
   // lane), rows 16 y + 4 g .. + 3
   auto each = [&](auto&& f) __attribute__((always_inline)) {
@@ -398,49 +398,56 @@ __global__ __launch_bounds__(64 * NY / strips<NY>()) void blocks_poly_kernel(Run
   // the entry v of (i, y) lies on the diagonal
   auto diag = [&](int i, int y, int v) { return 16 * y + 4 * g + v == column(i); };
   {
-    // the partial Grams are lower 32 x 32 tiles as they lay in the accumulators: entry
-    // (row i, column j) of a tile is value 4 (i / 8) + i % 4 of lane j + 32 (i / 4 % 2)
+    // The partial Grams are lower 32 x 32 tiles as they lay in the accumulators: float4 q of
+    // a tile is value v = q / 16 of lanes 4 (q % 16) .., row 8 (v / 4) + 4 (lane / 32) + v % 4,
+    // columns lane % 32 ... All threads add them up, chunk after chunk (four in flight), and
+    // lay the whole matrix out in LDS.
+    constexpr int THREADS = 64 * W, Q = nlow * 256 / THREADS;   // float4 per thread
+    static_assert(nlow * 256 % THREADS == 0, "whole float4 per thread");
     const int chunks = run.chunks;
-    const float* src = reinterpret_cast<const float*>(ws + run.partials) + int64_t(u) * chunks * nlow * 1024;
-    auto load = [&](const float* at, int i, int y) __attribute__((always_inline)) {
-      const int X = (NS * wave + i) >> 1, j = column(i) & 31, Y = y >> 1, i0 = 16 * (y & 1) + 4 * g;
-      f32x4_t w;
-      if (Y >= X) {
-        at += (Y * (Y + 1) / 2 + X) * 1024 + 4 * (i0 >> 3) * 64 + j + 32 * ((i0 >> 2) & 1);
+    const f32x4_t* src = reinterpret_cast<const f32x4_t*>(ws + run.partials) + int64_t(u) * chunks * nlow * 256 + threadIdx.x;
+    f32x4_t sum[Q];
 #pragma unroll
-        for (int v = 0; v < 4; ++v) w[v] = at[64 * v];
-      } else {
-        // above the diagonal: the mirrored entry, row j of tile (X, Y), columns i0 ..
-        w = *reinterpret_cast<const f32x4_t*>(at + (X * (X + 1) / 2 + Y) * 1024 + (4 * (j >> 3) + (j & 3)) * 64 + i0 +
-                                              32 * ((j >> 2) & 1));
-      }
-      return w;
-    };
-    each([&](int i, int y) __attribute__((always_inline)) { A[i][y] = load(src, i, y); });
-    // in order, the loads of chunk k + 1 under way while chunk k is added
-    if (chunks > 1) {
-      f32x4_t next[NS][NY];
-      each([&](int i, int y) __attribute__((always_inline)) { next[i][y] = load(src + nlow * 1024, i, y); });
-      for (int k = 1; k < chunks; ++k) {
-        f32x4_t cur[NS][NY];
-        each([&](int i, int y) __attribute__((always_inline)) { cur[i][y] = next[i][y]; });
-        const float* at = src + int64_t(min(k + 1, chunks - 1)) * nlow * 1024;
-        each([&](int i, int y) __attribute__((always_inline)) { next[i][y] = load(at, i, y); });
-        each([&](int i, int y) __attribute__((always_inline)) { A[i][y] += cur[i][y]; });
-      }
+    for (int q = 0; q < Q; ++q) sum[q] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    int k = 0;
+    for (; k + 4 <= chunks; k += 4, src += 4 * nlow * 256) {
+      f32x4_t w[4][Q];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+#pragma unroll
+        for (int q = 0; q < Q; ++q) w[e][q] = src[e * nlow * 256 + q * THREADS];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+#pragma unroll
+        for (int q = 0; q < Q; ++q) sum[q] += w[e][q];
     }
+    for (; k < chunks; ++k, src += nlow * 256)
+#pragma unroll
+      for (int q = 0; q < Q; ++q) sum[q] += src[q * THREADS];
+    float* full = reinterpret_cast<float*>(sm);
+    constexpr int LD = sp + 4;
+    static_assert(sp * LD * 4 <= SymLds<NY>::BYTES, "the matrix fits a buffer");
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      const int at = threadIdx.x + q * THREADS, tile = at >> 8, v = (at & 255) >> 4, l4 = 4 * (at & 15);
+      int ti, tj;
+      tile_rc(tile, ti, tj);
+      const int row = 32 * ti + 8 * (v >> 2) + 4 * (l4 >> 5) + (v & 3), col = 32 * tj + (l4 & 31);
+      *reinterpret_cast<f32x4_t*>(full + row * LD + col) = sum[q];
+      if (ti != tj)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) full[(col + e) * LD + row] = sum[q][e];
+    }
+    __syncthreads();
+    each([&](int i, int y) __attribute__((always_inline)) {
+      A[i][y] = *reinterpret_cast<const f32x4_t*>(full + column(i) * LD + 16 * y + 4 * g);
+    });
+#pragma unroll
+    for (int d = 0; d < sp; d += 64)
+      if (d + lane < sp) total += double(full[(d + lane) * LD + d + lane]);
+    total = wave_sum(total);          // every wave adds the same entries in the same order
+    __syncthreads();
   }
-  double mine = 0.0;
-  each([&](int i, int y) __attribute__((always_inline)) {
-#pragma unroll
-    for (int v = 0; v < 4; ++v) mine += diag(i, y, v) ? double(A[i][y][v]) : 0.0;
-  });
-  mine = wave_sum(mine);
-  if (lane == 0) trace[wave] = mine;
-  __syncthreads();
-  double total = 0.0;
-#pragma unroll
-  for (int i = 0; i < W; ++i) total += trace[i];
   // a block of zeros gives U = 0
   const float inv = total == 0.0 ? 0.0f : float(1.0 / total);
   const float root = total == 0.0 ? 0.0f : float(1.0 / sqrt(total));
@@ -509,12 +516,8 @@ __global__ __launch_bounds__(64 * NY / strips<NY>()) void blocks_poly_kernel(Run
 #pragma unroll
     for (int p = 0; p < kParts; ++p) {
       uint2 w;
-      w.x = __builtin_bit_cast(uint32_t, __builtin_convertvector(lo, bf16x2_t));
-      w.y = __builtin_bit_cast(uint32_t, __builtin_convertvector(hi, bf16x2_t));
-      lo[0] -= __uint_as_float(w.x << 16);
-      lo[1] -= __uint_as_float(w.x & 0xffff0000u);
-      hi[0] -= __uint_as_float(w.y << 16);
-      hi[1] -= __uint_as_float(w.y & 0xffff0000u);
+      w.x = leading_part(lo);
+      w.y = leading_part(hi);
       *reinterpret_cast<uint2*>(dst + p * sp * sp + column(i) * sp + 16 * y) = w;
     }
   });
@@ -660,10 +663,11 @@ bool empty(const muon_block_problem& p) { return p.rows == 0 || p.cols == 0 || p
 
 // How a problem is cut: chunks of the long side for the Gram, slabs per unit of the
 // last product, chosen so that all blocks of the call together give the 256 CUs
-// about four workgroups each (two or three fit one by their LDS), but a chunk is
-// never shorter than 256 entries: each one writes and reads a whole partial Gram.
+// about four workgroups each (two over a short side of 64, which need twice the
+// registers), but a chunk is never shorter than 256 entries: each one writes a whole
+// partial Gram, and the one CU that iterates reads them all.
 void cut(Run& r, int64_t total_blocks) {
-  const int64_t want = std::max<int64_t>(1, ceil_div(1024, std::max<int64_t>(total_blocks, 1)));
+  const int64_t want = std::max<int64_t>(1, ceil_div((r.kind & kBig) ? 512 : 1024, std::max<int64_t>(total_blocks, 1)));
   const int64_t slab = (r.kind & kF32) ? gram_slab<float>() : gram_slab<bf16_t>();
   int64_t chunks = std::min<int64_t>(want, ceil_div(r.l, 256));
   r.chunk = int(ceil_div(ceil_div(r.l, chunks), slab) * slab);
