@@ -136,6 +136,55 @@ struct Region {
     }
   }
 
+  // tile holds U for the region: dst = U, or c1 (what fetch() got) - c2 U
+  __device__ __forceinline__ void finish(const float* tile, int tile_ld, T* dst, int64_t ld, int rows, int cols, int r0,
+                                         int c0, int NR, int NC, bool vec, const Epilogue& e) const {
+    const int per = NC / E, n = NR * per;
+#pragma unroll
+    for (int q = 0; q < LD; ++q) {
+      const int t = threadIdx.x + 256 * q;
+      if (t < n) {
+        const int r = t / per, c = (t % per) * E;
+        if (r0 + r >= rows || c0 + c >= cols) continue;
+        float v[E];
+#pragma unroll
+        for (int k = 0; k < E; k += 4) {
+          const f32x4_t x = *reinterpret_cast<const f32x4_t*>(tile + r * tile_ld + c + k);
+#pragma unroll
+          for (int m = 0; m < 4; ++m) v[k + m] = x[m];
+        }
+        const uint32_t was[4] = {w[q].x, w[q].y, w[q].z, w[q].w};
+        if (e.update) {
+#pragma unroll
+          for (int k = 0; k < E; ++k) {
+            float o;
+            if constexpr (sizeof(T) == 2) o = __uint_as_float((k & 1) ? was[k >> 1] & 0xffff0000u : was[k >> 1] << 16);
+            else o = __uint_as_float(was[k]);
+            v[k] = fmaf(e.c1, o, -e.c2 * v[k]);
+          }
+        }
+        T* p = dst + int64_t(r0 + r) * ld + c0 + c;
+        if (vec && c0 + c + E <= cols) {
+          uint4 o;
+          if constexpr (sizeof(T) == 2) {
+            f32x2_t a = {v[0], v[1]}, b = {v[2], v[3]}, g = {v[4], v[5]}, h = {v[6], v[7]};
+            o = make_uint4(__builtin_bit_cast(uint32_t, __builtin_convertvector(a, bf16x2_t)),
+                           __builtin_bit_cast(uint32_t, __builtin_convertvector(b, bf16x2_t)),
+                           __builtin_bit_cast(uint32_t, __builtin_convertvector(g, bf16x2_t)),
+                           __builtin_bit_cast(uint32_t, __builtin_convertvector(h, bf16x2_t)));
+          } else {
+            o = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+          }
+          *reinterpret_cast<uint4*>(p) = o;
+        } else {
+#pragma unroll
+          for (int k = 0; k < E; ++k)
+            if (c0 + c + k < cols) p[k] = from_f32<T>(v[k]);
+        }
+      }
+    }
+  }
+
   template <int NP>
   __device__ __forceinline__ void store(char* lds, int pitch, int plane, int NR, int NC) const {
     const int per = NC / E, n = NR * per;
@@ -304,26 +353,6 @@ __device__ __forceinline__ void put_strip(char* buf, int wave, int lane, const S
     for (int t = 0; t < NY / 2; ++t) *reinterpret_cast<bf16x8_t*>(row + 64 * t + p * SymLds<NY>::PLANE) = o.p[p][t];
 }
 
-// the strip's transpose, from what put_strip left: four consecutive rows of one column per
-// transposing read
-template <int NY>
-__device__ __forceinline__ void get_transposed(const char* buf, int wave, int lane, f32x4_t (&out)[NY]) {
-  // lane 4 j + q of a group of 16 points at row j, columns 4 q .. + 3 of the strip
-  const char* at = buf + (4 * (lane >> 4) + ((lane & 15) >> 2)) * SymLds<NY>::PITCH + 64 * (wave >> 1) + 8 * (wave & 1) +
-                   16 * (lane & 3);
-#pragma unroll
-  for (int y = 0; y < NY; ++y) {
-    out[y] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-    for (int p = kParts - 1; p >= 0; --p) {
-      const gemm::lds_bf16x4_t w = __builtin_amdgcn_ds_read_tr16_b64_v4bf16(
-          (__attribute__((address_space(3))) gemm::lds_bf16x4_t*)(at + 16 * y * SymLds<NY>::PITCH + p * SymLds<NY>::PLANE));
-#pragma unroll
-      for (int v = 0; v < 4; ++v) out[y][v] += static_cast<float>(w[v]);
-    }
-  }
-}
-
 // out = S o for the wave's strips, S in LDS.  The parts of the pieces of S are read DEPTH
 // pieces (16 x 32) ahead of their products.
 template <int NY, int NS>
@@ -382,6 +411,8 @@ __global__ __launch_bounds__(64 * NY / strips<NY>()) void blocks_poly_kernel(Run
   int u = blockIdx.x;
   const Run& run = find_run(runs, u, 1);
   constexpr int nlow = tiles_of(NY / 2), sp = 16 * NY;
+  constexpr int LD = sp + 4;   // floats per row of a whole fp32 matrix in LDS: rows four apart start a quarter of the banks apart
+  static_assert(sp * LD * 4 <= SymLds<NY>::BYTES, "the matrix fits a buffer");
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
   f32x4_t A[NS][NY], T[NS][NY];
@@ -425,8 +456,6 @@ __global__ __launch_bounds__(64 * NY / strips<NY>()) void blocks_poly_kernel(Run
 #pragma unroll
       for (int q = 0; q < Q; ++q) sum[q] += src[q * THREADS];
     float* full = reinterpret_cast<float*>(sm);
-    constexpr int LD = sp + 4;
-    static_assert(sp * LD * 4 <= SymLds<NY>::BYTES, "the matrix fits a buffer");
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
       const int at = threadIdx.x + q * THREADS, tile = at >> 8, v = (at & 255) >> 4, l4 = 4 * (at & 15);
@@ -475,14 +504,23 @@ __global__ __launch_bounds__(64 * NY / strips<NY>()) void blocks_poly_kernel(Run
     const bool last = it == steps - 1;
     SymOperand<NY> oA[NS];
     f32x4_t P[NS][NY];
-    split(A, oA);
     if (it > 0) {
-      put(oA);
+      // (A + A^T) / 2: strips as rows in, their rows out
+      if (SHARED) __syncthreads();
+      float* full = reinterpret_cast<float*>(buf);
+      each([&](int i, int y) __attribute__((always_inline)) {
+        *reinterpret_cast<f32x4_t*>(full + column(i) * LD + 16 * y + 4 * g) = A[i][y];
+      });
+      __syncthreads();
+      each([&](int i, int y) __attribute__((always_inline)) {
 #pragma unroll
-      for (int i = 0; i < NS; ++i) get_transposed<NY>(other, NS * wave + i, lane, P[i]);
-      each([&](int i, int y) __attribute__((always_inline)) { A[i][y] = 0.5f * (A[i][y] + P[i][y]); });
-      split(A, oA);
+        for (int v = 0; v < 4; ++v) A[i][y][v] = 0.5f * (A[i][y][v] + full[(16 * y + 4 * g + v) * LD + column(i)]);
+      });
+      char* const w = buf;
+      buf = other;
+      other = w;
     }
+    split(A, oA);
     if (c != 0.0f) {
       put(oA);
       sym_product<NY, NS>(other, lane, oA, P);               // A A
@@ -524,62 +562,33 @@ __global__ __launch_bounds__(64 * NY / strips<NY>()) void blocks_poly_kernel(Run
 }
 
 // ---------------------------------------------------------------------------
-// apply: U = T M.  A wave keeps 32 rows of T in registers and runs over the long
-// side; the operand whose index is contiguous in the output comes first, so a lane
-// holds four consecutive entries of an output row.
+// apply: U = T M.  A wave keeps 32 rows of T in registers and multiplies them with its
+// share of a slab of the long side.  The results meet in LDS in the output's own layout
+// (over the slab's operand planes, which are done with), so that the output is read (for
+// an update; fetched while the slab is multiplied) and written in whole rows, 16 bytes
+// per lane.
 // ---------------------------------------------------------------------------
-template <typename TO>
-__device__ __forceinline__ void write4(TO* dst, const float v[4], int valid, bool vec, const Epilogue& e) {
-  if (vec && valid >= 4) {
-    float o[4];
-    if constexpr (sizeof(TO) == 2) {
-      if (e.update) {
-        const uint2 w = *reinterpret_cast<const uint2*>(dst);
-        o[0] = fmaf(e.c1, __uint_as_float(w.x << 16), -e.c2 * v[0]);
-        o[1] = fmaf(e.c1, __uint_as_float(w.x & 0xffff0000u), -e.c2 * v[1]);
-        o[2] = fmaf(e.c1, __uint_as_float(w.y << 16), -e.c2 * v[2]);
-        o[3] = fmaf(e.c1, __uint_as_float(w.y & 0xffff0000u), -e.c2 * v[3]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] = v[i];
-      }
-      *reinterpret_cast<uint2*>(dst) =
-          make_uint2(uint32_t(f32_to_bf16(o[0])) | (uint32_t(f32_to_bf16(o[1])) << 16),
-                     uint32_t(f32_to_bf16(o[2])) | (uint32_t(f32_to_bf16(o[3])) << 16));
-    } else {
-      if (e.update) {
-        const float4 w = *reinterpret_cast<const float4*>(dst);
-        o[0] = fmaf(e.c1, w.x, -e.c2 * v[0]);
-        o[1] = fmaf(e.c1, w.y, -e.c2 * v[1]);
-        o[2] = fmaf(e.c1, w.z, -e.c2 * v[2]);
-        o[3] = fmaf(e.c1, w.w, -e.c2 * v[3]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] = v[i];
-      }
-      *reinterpret_cast<float4*>(dst) = make_float4(o[0], o[1], o[2], o[3]);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (i < valid) {
-        float o = v[i];
-        if (e.update) o = fmaf(e.c1, to_f32(dst[i]), -e.c2 * v[i]);
-        dst[i] = from_f32<TO>(o);
-      }
-  }
-}
-
-template <typename T> constexpr int apply_slab() { return sizeof(T) == 2 ? 128 : 64; }   // long-side entries at a time
+// entries of the long side at a time: 64 keep two waves per SIMD in registers
+constexpr int apply_slab(bool all_bf16, bool big) { return all_bf16 && !big ? 128 : 64; }
+template <typename T, typename TO, bool TALL, bool BIG>
+struct ApplyTile {
+  static constexpr int LS = apply_slab(sizeof(T) == 2 && sizeof(TO) == 2, BIG), SIDE = BIG ? 128 : 64, NQ = SIDE / 16;
+  static constexpr int NPT = sizeof(TO) == 2 ? 2 : 3;                 // bf16 parts of T
+  static constexpr int NPM = sizeof(T) == 2 ? 1 : NPT;                // and of M
+  static constexpr int PITCH = TALL ? row_pitch(2 * SIDE) : tr_pitch(2 * LS);   // tall [LS][s], wide [s][LS]
+  static constexpr int PLANE = (TALL ? LS : SIDE) * PITCH;
+  static constexpr int ROWS = TALL ? LS : SIDE, COLS = TALL ? SIDE : LS;        // of the output's tile
+  static constexpr int OUT_LD = COLS + 4;
+  static constexpr int LDS_BYTES = NPM * PLANE > ROWS * OUT_LD * 4 ? NPM * PLANE : ROWS * OUT_LD * 4;
+  static constexpr int M_LOADS = SIDE * LS * int(sizeof(T)) / 16 / 256, OUT_LOADS = SIDE * LS * int(sizeof(TO)) / 16 / 256;
+};
 
 template <typename T, typename TO, bool TALL, bool BIG>
-__global__ __launch_bounds__(256) void blocks_apply_kernel(Runs runs, const char* ws, Epilogue e) {
-  constexpr int LS = apply_slab<T>(), SIDE = BIG ? 128 : 64, NQ = SIDE / 16;
-  constexpr int NPT = sizeof(TO) == 2 ? 2 : 3;                 // bf16 parts of T
-  constexpr int NPM = sizeof(T) == 2 ? 1 : NPT;                // and of M
-  constexpr int PITCH = TALL ? row_pitch(2 * SIDE) : tr_pitch(2 * LS);   // tall [LS][s], wide [s][LS]
-  constexpr int PLANE = (TALL ? LS : SIDE) * PITCH;
-  extern __shared__ __attribute__((aligned(16))) char lds[];   // NPM planes
+__global__ __launch_bounds__(256, 2) void blocks_apply_kernel(Runs runs, const char* ws, Epilogue e) {
+  using C_ = ApplyTile<T, TO, TALL, BIG>;
+  constexpr int LS = C_::LS, NQ = C_::NQ, NPT = C_::NPT, NPM = C_::NPM, PITCH = C_::PITCH, PLANE = C_::PLANE;
+  constexpr int TILES = BIG ? LS / 32 : LS / 64;               // 32 x 32 tiles of a wave and slab (a short side over 32)
+  extern __shared__ __attribute__((aligned(16))) char lds[];
   int u = blockIdx.x;
   const Run& run = find_run(runs, u, 2);
   const int b = u / run.units, unit = u % run.units;
@@ -594,7 +603,8 @@ __global__ __launch_bounds__(256) void blocks_apply_kernel(Runs runs, const char
   const int groups = 4 / nt, ti = wave % nt, grp = wave / nt;
   const bool busy = grp < groups;
   const int l0 = unit * run.slabs * LS, l1 = min(l, l0 + run.slabs * LS);
-  Region<T, BIG ? 8 : 4> reg;
+  Region<T, C_::M_LOADS> reg;
+  Region<TO, C_::OUT_LOADS> old;
   auto fetch = [&](int x) __attribute__((always_inline)) {
     if (TALL) reg.fetch(M, ld, l, s, x, 0, LS, sp, vec);
     else reg.fetch(M, ld, s, l, 0, x, sp, LS, vec);
@@ -615,37 +625,52 @@ __global__ __launch_bounds__(256) void blocks_apply_kernel(Runs runs, const char
     if (TALL) reg.template store<NPM>(lds, PITCH, PLANE, LS, sp);
     else reg.template store<NPM>(lds, PITCH, PLANE, sp, LS);
     __syncthreads();
+    if (e.update) {
+      if (TALL) old.fetch(out, ld_out, l, s, x, 0, LS, sp, vec_out);
+      else old.fetch(out, ld_out, s, l, 0, x, sp, LS, vec_out);
+    }
     if (x + LS < l1) fetch(x + LS);
-    if (!busy) continue;
-    for (int j = grp; j < LS / 32; j += groups) {
-      if (x + 32 * j >= l1) break;
-      f32x16_t acc;
+    f32x16_t acc[TILES];
 #pragma unroll
-      for (int v = 0; v < 16; ++v) acc[v] = 0.0f;
+    for (int k = 0; k < TILES; ++k) {
+      const int j = grp + k * groups;   // this tile's 32 entries of the slab
 #pragma unroll
-      for (int q = 0; q < NQ; ++q) {
-        if (16 * q < sp) {
+      for (int v = 0; v < 16; ++v) acc[k][v] = 0.0f;
+      if (busy && 32 * j < LS) {
 #pragma unroll
-          for (int p = 0; p < NPM; ++p) {
-            const u32x4_t fm = fragment<!TALL>(lds + p * PLANE, PITCH, 32 * j, q, lane);
+        for (int q = 0; q < NQ; ++q) {
+          if (16 * q < sp) {
 #pragma unroll
-            for (int k = 0; p + k < NPT; ++k) {
-              if (TALL) gemm::Mfma<bf16_t>::mma(tf[k][q], fm, acc);
-              else gemm::Mfma<bf16_t>::mma(fm, tf[k][q], acc);
+            for (int p = 0; p < NPM; ++p) {
+              const u32x4_t fm = fragment<!TALL>(lds + p * PLANE, PITCH, 32 * j, q, lane);
+#pragma unroll
+              for (int r = 0; p + r < NPT; ++r) {
+                // the index that is contiguous in the output first: four of its entries per lane
+                if (TALL) gemm::Mfma<bf16_t>::mma(tf[r][q], fm, acc[k]);
+                else gemm::Mfma<bf16_t>::mma(fm, tf[r][q], acc[k]);
+              }
             }
           }
         }
       }
-      // accumulator v of this lane: first operand's row 8 (v / 4) + 4 h + v % 4, second's row fr
+    }
+    __syncthreads();
+    float* tile = reinterpret_cast<float*>(lds);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const float v[4] = {acc[4 * q], acc[4 * q + 1], acc[4 * q + 2], acc[4 * q + 3]};
-        const int first = 8 * q + 4 * h;
-        const int row = TALL ? x + 32 * j + fr : ti * 32 + fr;
-        const int col = TALL ? ti * 32 + first : x + 32 * j + first;
-        if (row < (TALL ? l : s)) write4<TO>(out + int64_t(row) * ld_out + col, v, (TALL ? s : l) - col, vec_out, e);
+    for (int k = 0; k < TILES; ++k) {
+      const int j = grp + k * groups;
+      if (busy && 32 * j < LS) {
+        // accumulator v of this lane: first operand's row 8 (v / 4) + 4 h + v % 4, second's row fr
+        const int row = (TALL ? 32 * j : 32 * ti) + fr, col = (TALL ? 32 * ti : 32 * j) + 4 * h;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          *reinterpret_cast<f32x4_t*>(tile + row * C_::OUT_LD + col + 8 * q) =
+              f32x4_t{acc[k][4 * q], acc[k][4 * q + 1], acc[k][4 * q + 2], acc[k][4 * q + 3]};
       }
     }
+    __syncthreads();
+    if (TALL) old.finish(tile, C_::OUT_LD, out, ld_out, l, s, x, 0, LS, sp, vec_out, e);
+    else old.finish(tile, C_::OUT_LD, out, ld_out, s, l, 0, x, sp, LS, vec_out, e);
   }
 }
 
@@ -672,7 +697,7 @@ void cut(Run& r, int64_t total_blocks) {
   int64_t chunks = std::min<int64_t>(want, ceil_div(r.l, 256));
   r.chunk = int(ceil_div(ceil_div(r.l, chunks), slab) * slab);
   r.chunks = int(ceil_div(r.l, r.chunk));
-  const int64_t ls = (r.kind & kF32) ? apply_slab<float>() : apply_slab<bf16_t>();
+  const int64_t ls = apply_slab(!(r.kind & kF32) && !r.out_f32, (r.kind & kBig) != 0);
   const int64_t slabs = ceil_div(r.l, ls);
   r.slabs = int(ceil_div(slabs, std::min<int64_t>(slabs, want)));
   r.units = int(ceil_div(slabs, r.slabs));
@@ -689,7 +714,8 @@ Run make_run(const muon_block_problem& p, int64_t total_blocks, size_t& bytes) {
   r.out_f32 = p.out_dtype == MUON_F32;
   const int64_t em = p.m_dtype == MUON_F32 ? 4 : 8;
   r.vec_m = p.ld_m % em == 0 && (p.count <= 1 || p.stride_m % em == 0);
-  r.vec_out = p.ld_out % 4 == 0 && (p.count <= 1 || p.stride_out % 4 == 0);
+  const int64_t eo = p.out_dtype == MUON_F32 ? 4 : 8;
+  r.vec_out = p.ld_out % eo == 0 && (p.count <= 1 || p.stride_out % eo == 0);
   cut(r, total_blocks);
   const int64_t nt = ceil_div(r.s, 32), sp = nt * 32;
   r.partials = int64_t(bytes);
@@ -710,9 +736,7 @@ template <typename T, typename TO, bool TALL, bool BIG>
 int launch_apply(const Runs& runs, const char* ws, const Epilogue& e, hipStream_t st) {
   int64_t units = 0;
   for (int i = 0; i < runs.n; ++i) units += int64_t(runs.r[i].count) * runs.r[i].units;
-  constexpr int LS = apply_slab<T>(), NPM = sizeof(T) == 2 ? 1 : sizeof(TO) == 2 ? 2 : 3;
-  constexpr int SIDE = BIG ? 128 : 64;
-  constexpr int LDS = NPM * (TALL ? LS * row_pitch(2 * SIDE) : SIDE * tr_pitch(2 * LS));
+  constexpr int LDS = ApplyTile<T, TO, TALL, BIG>::LDS_BYTES;
   static std::atomic<uint64_t> configured{0};
   if (gemm::set_lds_limit(blocks_apply_kernel<T, TO, TALL, BIG>, LDS, configured) != MUON_OK) return MUON_ELAUNCH;
   launch_kernel(blocks_apply_kernel<T, TO, TALL, BIG>, dim3(units), dim3(256), LDS, st, runs, ws, e);
