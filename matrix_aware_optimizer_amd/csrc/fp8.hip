@@ -17,6 +17,7 @@ namespace muon {
 namespace {
 
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
+typedef float f32x2_t __attribute__((ext_vector_type(2)));
 
 // 32 bytes of a matrix operand from two 16-byte reads
 __device__ __forceinline__ i32x8_t join(const u32x4_t (&v)[2]) {
@@ -212,6 +213,9 @@ struct Fp8GemmArgs {
   int64_t ra4, rb4;         // rows of the scale arrays
   float alpha, beta;
   int vec;                  // rows of C can be written 4 entries at a time
+  int splits;               // parts of a split contraction (tile kernels): > 1 writes fp32 partial products
+  float* partials;          // [splits][m][ldp]
+  int64_t ldp;
 };
 
 // C[row][col .. col + 3] <- beta C + alpha acc, one rounding to the stored type
@@ -303,39 +307,60 @@ __global__ __launch_bounds__(1024) void fp8_gemm_direct_kernel(Fp8GemmArgs g) {
   const int r = lane & 15, kq = lane >> 4;
   const int64_t n0 = int64_t(blockIdx.x) * 16, m0 = int64_t(blockIdx.y) * (16 * MT);
   const int64_t brow = min(n0 + r, g.n - 1);
-  const uint8_t* pb = g.B + brow * g.ldb + 32 * kq;
+  // 16 bytes at 16 kq and at 64 + 16 kq of the group: whole 64-byte runs of a row per
+  // load, the same k-values for both operands
+  const uint8_t* pb = g.B + brow * g.ldb + 16 * kq;
   const uint8_t* psb = g.sb + brow * 4;
   const uint8_t* pa[MT];
   const uint8_t* psa[MT];
 #pragma unroll
   for (int i = 0; i < MT; ++i) {
     const int64_t arow = min(m0 + 16 * i + r, g.m - 1);
-    pa[i] = g.A + arow * g.lda + 32 * kq;
+    pa[i] = g.A + arow * g.lda + 16 * kq;
     psa[i] = g.sa + arow * 4;
   }
   f32x4_t acc[MT];
 #pragma unroll
   for (int i = 0; i < MT; ++i) acc[i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
   const int64_t groups = g.K / kGroup;
-  for (int64_t kb = wave; kb < groups; kb += waves) {
-    const i32x8_t fb = *reinterpret_cast<const i32x8_t*>(pb + kb * kGroup);
-    const int sb = psb[(kb >> 2) * g.rb4 * 4 + (kb & 3)];
-    bf16x8_t wb[4];
-    if constexpr (EXACT) {
+  constexpr int U = MT == 1 ? 4 : 2;   // groups whose loads are in flight together
+  for (int64_t kb0 = wave; kb0 < groups; kb0 += U * waves) {
+    u32x4_t fb[U][2], fa[U][MT][2];
+    int sb[U], sa[U][MT];
 #pragma unroll
-      for (int h = 0; h < 4; ++h) wb[h] = widen8<MUON_FP8_E4M3>(fb[2 * h], fb[2 * h + 1], scale_value(sb));
+    for (int u = 0; u < U; ++u) {
+      const int64_t kb = min(kb0 + u * waves, groups - 1);   // past the end: read again, not used
+      sb[u] = psb[(kb >> 2) * g.rb4 * 4 + (kb & 3)];
+#pragma unroll
+      for (int c = 0; c < 2; ++c) fb[u][c] = *reinterpret_cast<const u32x4_t*>(pb + kb * kGroup + 64 * c);
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        sa[u][i] = psa[i][(kb >> 2) * g.ra4 * 4 + (kb & 3)];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) fa[u][i][c] = *reinterpret_cast<const u32x4_t*>(pa[i] + kb * kGroup + 64 * c);
+      }
     }
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
-      const i32x8_t fa = *reinterpret_cast<const i32x8_t*>(pa[i] + kb * kGroup);
-      const int sa = psa[i][(kb >> 2) * g.ra4 * 4 + (kb & 3)];
+    for (int u = 0; u < U; ++u) {
+      if (kb0 + u * waves >= groups) break;
+      bf16x8_t wb[4];
       if constexpr (EXACT) {
 #pragma unroll
-        for (int h = 0; h < 4; ++h)
-          acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-              wb[h], widen8<FA>(fa[2 * h], fa[2 * h + 1], scale_value(sa)), acc[i], 0, 0, 0);
-      } else {
-        acc[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fb, fa, acc[i], 0, FA, 0, sb, 0, sa);
+        for (int p = 0; p < 4; ++p)
+          wb[p] = widen8<MUON_FP8_E4M3>(fb[u][p >> 1][2 * (p & 1)], fb[u][p >> 1][2 * (p & 1) + 1], scale_value(sb[u]));
+      }
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        if constexpr (EXACT) {
+#pragma unroll
+          for (int p = 0; p < 4; ++p)
+            acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                wb[p], widen8<FA>(fa[u][i][p >> 1][2 * (p & 1)], fa[u][i][p >> 1][2 * (p & 1) + 1], scale_value(sa[u][i])),
+                acc[i], 0, 0, 0);
+        } else {
+          acc[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(join(fb[u]), join(fa[u][i]), acc[i], 0, FA, 0, sb[u], 0,
+                                                                    sa[u][i]);
+        }
       }
     }
   }
@@ -393,9 +418,10 @@ struct Fp8Tile {
   static constexpr int A_BYTES = BM * 64, B_BYTES = BN * 64;
   static constexpr int STAGE = A_BYTES + B_BYTES + (BM + BN) * 4;
   static constexpr int LDS_BYTES = S * STAGE;
-  static constexpr int A_DMA = A_BYTES / 1024 / W, B_DMA = B_BYTES / 1024 / W, S_DMA = (BM + BN) / 64 / W;
+  static constexpr int A_DMA = A_BYTES / 1024 / W, B_DMA = B_BYTES / 1024 / W, S_ALL = (BM + BN) / 64;
+  static constexpr int S_DMA = (S_ALL + W - 1) / W;   // past the last, a wave copies the last rows again
   static constexpr int D = A_DMA + B_DMA + S_DMA;   // DMA instructions per wave and stage
-  static_assert(A_BYTES % (1024 * W) == 0 && B_BYTES % (1024 * W) == 0 && (BM + BN) % (64 * W) == 0, "DMA split");
+  static_assert(A_BYTES % (1024 * W) == 0 && B_BYTES % (1024 * W) == 0, "DMA split");
   static_assert(BM % 64 == 0, "one DMA of scale words lies in one operand");
   static_assert(S >= 3 && D * (S - 2) <= 63 && LDS_BYTES <= 160 * 1024, "ring");
 };
@@ -425,26 +451,25 @@ __device__ __forceinline__ void ring_barrier() {
 
 constexpr int kGroupRows = 8;   // tile rows walked together, column by column
 
-template <int FA, typename TC, int BM, int BN, int WM, int WN, int S>
-__global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void fp8_gemm_tile_kernel(Fp8GemmArgs g) {
+// Where a unit's result goes: C <- beta C + alpha acc for an m x width matrix of row pitch ld
+template <typename TS>
+struct TileOut {
+  TS* C;
+  int64_t ld, width;
+  float alpha, beta;
+  bool vec;   // rows can be written 16 bytes at a time
+};
+
+// One BM x BN tile at rows m0, columns n0 over 64-value steps [kt0, kt0 + nk) (both even)
+template <int FA, bool EXACT, typename TS, int BM, int BN, int WM, int WN, int S>
+__device__ __forceinline__ void fp8_tile_unit(const Fp8GemmArgs& g, int64_t m0, int64_t n0, int kt0, int nk,
+                                              const TileOut<TS>& out, char* lds) {
   using C_ = Fp8Tile<BM, BN, WM, WN, S>;
-  constexpr bool EXACT = sizeof(TC) == 4;
   constexpr int FM = C_::FM, FN = C_::FN;
-  extern __shared__ __attribute__((aligned(1024))) char lds[];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int fr = lane & 31, h = lane >> 5;
   const int wm0 = (wave / (BN / WN)) * WM, wn0 = (wave % (BN / WN)) * WN;
-  const int64_t TM = (g.m + BM - 1) / BM, TN = (g.n + BN - 1) / BN;
-  int64_t tm, tn;
-  {
-    const int64_t t = gemm::xcd_remap(blockIdx.x, gridDim.x);
-    const int64_t per = int64_t(kGroupRows) * TN, first = (t / per) * kGroupRows;
-    const int64_t size = min(TM - first, int64_t(kGroupRows)), r = t % per;
-    tm = __builtin_amdgcn_readfirstlane(int(first + r % size));
-    tn = __builtin_amdgcn_readfirstlane(int(r / size));
-  }
-  const int64_t m0 = tm * BM, n0 = tn * BN;
   // rows past the matrix read its last row; what they compute is not stored
   const int mlast = int(min(g.m - 1 - m0, int64_t(BM - 1))), nlast = int(min(g.n - 1 - n0, int64_t(BN - 1)));
   const uint8_t* At = g.A + m0 * g.lda;
@@ -466,7 +491,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void fp8_gemm_tile_kern
   uint32_t s_off[C_::S_DMA];
 #pragma unroll
   for (int i = 0; i < C_::S_DMA; ++i) {
-    const int r = 64 * (wave * C_::S_DMA + i);
+    const int r = 64 * min(wave * C_::S_DMA + i, C_::S_ALL - 1);
     const bool of_a = r < BM;
     s_off[i] = uint32_t(of_a ? min(r + lane, mlast) : min(r - BM + lane, nlast)) * 4;
     s_src[i] = of_a ? g.sa + m0 * 4 : g.sb + n0 * 4;
@@ -484,7 +509,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void fp8_gemm_tile_kern
       dma16_at(Bt + int64_t(kt) * 64, b_off[b], st + C_::A_BYTES + (wave * C_::B_DMA + b) * 1024);
     } else {
       const int s = q - C_::A_DMA - C_::B_DMA;
-      dma4_at(s_src[s] + (kt >> 3) * s_step[s], s_off[s], st + C_::A_BYTES + C_::B_BYTES + (wave * C_::S_DMA + s) * 256);
+      dma4_at(s_src[s] + (kt >> 3) * s_step[s], s_off[s], st + C_::A_BYTES + C_::B_BYTES + min(wave * C_::S_DMA + s, C_::S_ALL - 1) * 256);
     }
   };
   auto ring_next = [](uint32_t o) {
@@ -547,7 +572,10 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void fp8_gemm_tile_kern
         for (int t = 0; t < FM * FN; ++t) {
           const int i = t / FN, j = t % FN;
           acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(w[p & 1][FM + j], w[p & 1][i], acc[i][j], 0, 0, 0);
-          if (p < 3 && t < FM + FN) widen(p + 1, t);
+          if (p < 3) {
+#pragma unroll
+            for (int k = t; k < FM + FN; k += FM * FN) widen(p + 1, k);
+          }
           between(p * FM * FN + t);
           __builtin_amdgcn_sched_barrier(0);
         }
@@ -567,13 +595,11 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void fp8_gemm_tile_kern
       }
     }
   };
-  // 64-value steps: an even number, at least two
-  const int nk = __builtin_amdgcn_readfirstlane(int(g.K / 64));
 #pragma unroll
   for (int s = 0; s < S - 1; ++s)
     if (s < nk)
 #pragma unroll
-      for (int q = 0; q < C_::D; ++q) issue_one(q, s, uint32_t(s) * C_::STAGE);
+      for (int q = 0; q < C_::D; ++q) issue_one(q, kt0 + s, uint32_t(s) * C_::STAGE);
   if (nk >= S - 1) ring_barrier<C_::D * (S - 2)>();
   else ring_barrier<0>();
   Frags f0, f1;
@@ -585,13 +611,13 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void fp8_gemm_tile_kern
   auto steady = [&](Frags& cur, Frags& nxt) __attribute__((always_inline)) {
     const char* st = lds + ring_next(o_cur);
     ring_barrier<C_::D * (S - 3)>();
-    mma(it, cur, [&](int n) __attribute__((always_inline)) {
+    mma(kt0 + it, cur, [&](int n) __attribute__((always_inline)) {
 #pragma unroll
       for (int r = 0; r < RPM; ++r)
         if (RPM * n + r < READS) read_one(RPM * n + r, st, nxt);
 #pragma unroll
       for (int q = 0; q < C_::D; ++q)
-        if (q * N / C_::D == n) issue_one(q, it + S - 1, o_iss);
+        if (q * N / C_::D == n) issue_one(q, kt0 + it + S - 1, o_iss);
     });
     o_cur = ring_next(o_cur);
     o_iss = ring_next(o_iss);
@@ -605,7 +631,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void fp8_gemm_tile_kern
 #pragma unroll
       for (int q = 0; q < READS; ++q) read_one(q, st, nxt);
     }
-    mma(it, cur, [](int) {});
+    mma(kt0 + it, cur, [](int) {});
     o_cur = ring_next(o_cur);
     ++it;
   };
@@ -622,45 +648,224 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void fp8_gemm_tile_kern
     drain(f0, f1);
     drain(f1, f0);
   }
-  // accumulator v of a lane: column 8 (v / 4) + 4 h + v % 4 of B's block, row fr of A's
+  // The tile leaves through LDS, 32 rows at a time and each wave through its own part of
+  // the ring, so that rows are read (beta) and written 16 bytes per lane and whole lines
+  // at a time.  Accumulator v of a lane: column 8 (v / 4) + 4 h + v % 4 of B's block, row
+  // fr of A's.
+  ring_barrier<0>();
+  constexpr int LDW = WN + 4, E = 16 / int(sizeof(TS)), LPR = WN / E, RPP = 64 / LPR, PASSES = 32 / RPP;
+  static_assert(C_::W * 32 * LDW * 4 <= C_::LDS_BYTES, "the slabs fit the ring");
+  float* slab = reinterpret_cast<float*>(lds) + wave * 32 * LDW;
+  const int pr = lane / LPR, pc = (lane % LPR) * E;
+  const int64_t col = n0 + wn0 + pc;
 #pragma unroll
   for (int i = 0; i < FM; ++i) {
-    const int64_t row = m0 + wm0 + 32 * i + fr;
-    if (row >= g.m) continue;
 #pragma unroll
     for (int j = 0; j < FN; ++j)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int64_t col = n0 + wn0 + 32 * j + 8 * q + 4 * h;
-        const float v[4] = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
-        if (col < g.n) store4<TC>(g, row, col, v);
+      for (int q = 0; q < 4; ++q)
+        *reinterpret_cast<f32x4_t*>(slab + fr * LDW + 32 * j + 8 * q + 4 * h) =
+            f32x4_t{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+    const int64_t row0 = m0 + wm0 + 32 * i + pr;
+    if (out.vec && col + E <= out.width) {
+      uint4 was[PASSES];
+      if (out.beta != 0.0f) {
+#pragma unroll
+        for (int p = 0; p < PASSES; ++p) {
+          was[p] = make_uint4(0, 0, 0, 0);
+          if (row0 + RPP * p < g.m) was[p] = *reinterpret_cast<const uint4*>(out.C + (row0 + RPP * p) * out.ld + col);
+        }
       }
+#pragma unroll
+      for (int p = 0; p < PASSES; ++p) {
+        float o[E];
+#pragma unroll
+        for (int k = 0; k < E; k += 4) {
+          const f32x4_t x = *reinterpret_cast<const f32x4_t*>(slab + (pr + RPP * p) * LDW + pc + k);
+#pragma unroll
+          for (int v = 0; v < 4; ++v) o[k + v] = out.alpha * x[v];
+        }
+        if (out.beta != 0.0f) {
+          const uint32_t w[4] = {was[p].x, was[p].y, was[p].z, was[p].w};
+#pragma unroll
+          for (int k = 0; k < E; ++k) {
+            float c;
+            if constexpr (sizeof(TS) == 2) c = __uint_as_float((k & 1) ? w[k >> 1] & 0xffff0000u : w[k >> 1] << 16);
+            else c = __uint_as_float(w[k]);
+            o[k] = fmaf(out.beta, c, o[k]);
+          }
+        }
+        if (row0 + RPP * p < g.m) {
+          TS* dst = out.C + (row0 + RPP * p) * out.ld + col;
+          if constexpr (sizeof(TS) == 2) {
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const f32x2_t x = {o[2 * k], o[2 * k + 1]};
+              w[k] = __builtin_bit_cast(uint32_t, __builtin_convertvector(x, bf16x2_t));
+            }
+            *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+          } else {
+            *reinterpret_cast<float4*>(dst) = make_float4(o[0], o[1], o[2], o[3]);
+          }
+        }
+      }
+    } else {
+      for (int p = 0; p < PASSES; ++p)
+        if (row0 + RPP * p < g.m)
+          for (int k = 0; k < E; ++k)
+            if (col + k < out.width) {
+              TS* dst = out.C + (row0 + RPP * p) * out.ld + col + k;
+              float o = out.alpha * slab[(pr + RPP * p) * LDW + pc + k];
+              if (out.beta != 0.0f) o = fmaf(out.beta, to_f32(*dst), o);
+              *dst = from_f32<TS>(o);
+            }
+    }
   }
 }
 
-template <int FA, typename TC, int BM, int BN, int WM, int WN, int S>
+// tile t of the grid of TM x TN tiles: groups of kGroupRows tile rows, column by column
+__device__ __forceinline__ void tile_at(int64_t t, int64_t TM, int64_t TN, int64_t& tm, int64_t& tn) {
+  const int64_t per = int64_t(kGroupRows) * TN, first = (t / per) * kGroupRows;
+  const int64_t size = min(TM - first, int64_t(kGroupRows)), r = t % per;
+  tm = __builtin_amdgcn_readfirstlane(int(first + r % size));
+  tn = __builtin_amdgcn_readfirstlane(int(r / size));
+}
+
+template <typename TC>
+__device__ __forceinline__ TileOut<TC> whole_out(const Fp8GemmArgs& g) {
+  return TileOut<TC>{static_cast<TC*>(g.C), g.ldc, g.n, g.alpha, g.beta, g.ldc % (16 / int64_t(sizeof(TC))) == 0};
+}
+
+// All tiles of one size; with SPLIT each is g.splits units along the contraction, whose
+// fp32 results lie one after another in g.partials.
+template <int FA, typename TC, int BM, int BN, int WM, int WN, int S, bool SPLIT>
+__global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void fp8_gemm_tile_kernel(Fp8GemmArgs g) {
+  extern __shared__ __attribute__((aligned(1024))) char lds[];
+  constexpr bool EXACT = sizeof(TC) == 4;
+  const int64_t TM = (g.m + BM - 1) / BM, TN = (g.n + BN - 1) / BN;
+  int64_t u = gemm::xcd_remap(blockIdx.x, gridDim.x), tm, tn;
+  if constexpr (SPLIT) {
+    // a split's tiles are neighbours, and the splits of 128-value groups as even as they come
+    const int64_t tiles = TM * TN, part = u / tiles, groups = g.K / kGroup;
+    tile_at(u % tiles, TM, TN, tm, tn);
+    const int g0 = __builtin_amdgcn_readfirstlane(int(part * groups / g.splits));
+    const int g1 = __builtin_amdgcn_readfirstlane(int((part + 1) * groups / g.splits));
+    const TileOut<float> out{g.partials + part * g.m * g.ldp, g.ldp, g.ldp, 1.0f, 0.0f, true};
+    fp8_tile_unit<FA, EXACT, float, BM, BN, WM, WN, S>(g, tm * BM, tn * BN, 2 * g0, 2 * (g1 - g0), out, lds);
+  } else {
+    tile_at(u, TM, TN, tm, tn);
+    fp8_tile_unit<FA, EXACT, TC, BM, BN, WM, WN, S>(g, tm * BM, tn * BN, 0, __builtin_amdgcn_readfirstlane(int(g.K / 64)),
+                                                    whole_out<TC>(g), lds);
+  }
+}
+
+// 256 x 256 tiles in rounds of one per CU; those of the last, partial round come in
+// `parts` (2: 128 x 256, 4: 128 x 128) so that they fill the CUs.  Workgroups [0, whole)
+// take whole tiles.
+template <int FA, typename TC>
+__global__ __launch_bounds__(256) void fp8_gemm_mixed_kernel(Fp8GemmArgs g, int64_t whole, int parts) {
+  extern __shared__ __attribute__((aligned(1024))) char lds[];
+  constexpr bool EXACT = sizeof(TC) == 4;
+  const int64_t TM = (g.m + 255) / 256, TN = (g.n + 255) / 256;
+  const int nk = __builtin_amdgcn_readfirstlane(int(g.K / 64));
+  const int64_t b = blockIdx.x;
+  int64_t tm, tn;
+  if (b < whole) {
+    tile_at(gemm::xcd_remap(b, whole), TM, TN, tm, tn);
+    fp8_tile_unit<FA, EXACT, TC, 256, 256, 128, 128, 4>(g, tm * 256, tn * 256, 0, nk, whole_out<TC>(g), lds);
+    return;
+  }
+  const int64_t u = gemm::xcd_remap(b - whole, int64_t(gridDim.x) - whole), part = u % parts;
+  tile_at(whole + u / parts, TM, TN, tm, tn);
+  const int64_t m0 = tm * 256 + 128 * (part & 1), n0 = tn * 256 + 128 * (part >> 1);
+  if (m0 >= g.m || n0 >= g.n) return;
+  if (parts == 2) fp8_tile_unit<FA, EXACT, TC, 128, 256, 64, 128, 4>(g, m0, n0, 0, nk, whole_out<TC>(g), lds);
+  else fp8_tile_unit<FA, EXACT, TC, 128, 128, 64, 64, 4>(g, m0, n0, 0, nk, whole_out<TC>(g), lds);
+}
+
+// C <- beta C + alpha sum of the splits' partial products, added in their order
+template <typename TC>
+__global__ __launch_bounds__(256) void fp8_gemm_join_kernel(Fp8GemmArgs g) {
+  const int64_t per = g.ldp / 4, t = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  if (t >= g.m * per) return;
+  const int64_t row = t / per, col = (t % per) * 4;
+  const float* src = g.partials + row * g.ldp + col;
+  f32x4_t sum = *reinterpret_cast<const f32x4_t*>(src);
+  for (int p = 1; p < g.splits; ++p) sum += *reinterpret_cast<const f32x4_t*>(src + p * g.m * g.ldp);
+  const float v[4] = {sum[0], sum[1], sum[2], sum[3]};
+  store4<TC>(g, row, col, v);
+}
+
+template <int FA, typename TC, int BM, int BN, int WM, int WN, int S, bool SPLIT>
 int launch_tile(const Fp8GemmArgs& g, hipStream_t st) {
   using C_ = Fp8Tile<BM, BN, WM, WN, S>;
-  auto kern = fp8_gemm_tile_kernel<FA, TC, BM, BN, WM, WN, S>;
+  auto kern = fp8_gemm_tile_kernel<FA, TC, BM, BN, WM, WN, S, SPLIT>;
   static std::atomic<uint64_t> configured{0};   // devices with the LDS limit set
   if (gemm::set_lds_limit(kern, C_::LDS_BYTES, configured) != MUON_OK) return MUON_ELAUNCH;
-  const int64_t tiles = ceil_div(g.m, BM) * ceil_div(g.n, BN);
+  const int64_t tiles = ceil_div(g.m, BM) * ceil_div(g.n, BN) * (SPLIT ? g.splits : 1);
   if (tiles > INT32_MAX) return MUON_EINVAL;
   launch_kernel(kern, dim3(tiles), dim3(C_::NT), C_::LDS_BYTES, st, g);
   return launch_status();
 }
 
 template <int FA, typename TC>
-int launch_product(const Fp8GemmArgs& g, hipStream_t st) {
-  if (g.K > 0 && g.m > 64) {
-    // 256 x 256 tiles where they fill at least half of the CUs, else 128 x 128
-    const int64_t big = ceil_div(g.m, 256) * ceil_div(g.n, 256);
-    if (2 * big >= gemm::device_cus()) return launch_tile<FA, TC, 256, 256, 128, 128, 4>(g, st);
-    return launch_tile<FA, TC, 128, 128, 64, 64, 4>(g, st);
+int launch_mixed(const Fp8GemmArgs& g, int64_t whole, int64_t rest, int parts, hipStream_t st) {
+  auto kern = fp8_gemm_mixed_kernel<FA, TC>;
+  constexpr int LDS = Fp8Tile<256, 256, 128, 128, 4>::LDS_BYTES;
+  static std::atomic<uint64_t> configured{0};
+  if (gemm::set_lds_limit(kern, LDS, configured) != MUON_OK) return MUON_ELAUNCH;
+  if (whole + rest * parts > INT32_MAX) return MUON_EINVAL;
+  launch_kernel(kern, dim3(whole + rest * parts), dim3(256), LDS, st, g, whole, parts);
+  return launch_status();
+}
+
+// How a product is cut, by its sizes alone (kCus: one 256 x 256 tile each).
+//  direct  up to 16 rows: bound by reading B once, straight from memory
+//  split   fewer 128-wide tiles than half the CUs: along the contraction into units of at
+//          least 512 k-values, about two per CU, joined by a second kernel; up to 64 rows
+//          on 64 x 128 tiles
+//  small   128 x 128 tiles where 256 x 256 ones would leave more than half the CUs idle
+//  mixed   256 x 256 tiles, the last round in halves or quarters
+constexpr int64_t kCus = 256;
+enum ProductKind { kDirect, kSplit, kSmall, kMixed };
+struct ProductPlan {
+  ProductKind kind;
+  int splits;
+};
+inline ProductPlan plan_product(int64_t m, int64_t n, int64_t K) {
+  if (m <= 16 || K == 0) return {kDirect, 1};
+  const int64_t tiles = ceil_div(m, m <= 64 ? 64 : 128) * ceil_div(n, 128);
+  const int64_t splits = std::min<int64_t>(std::min<int64_t>(16, K / 512), ceil_div(2 * kCus, tiles));
+  if (2 * tiles <= kCus && splits > 1) return {kSplit, int(splits)};
+  if (m <= 64) return {kDirect, 1};
+  if (2 * ceil_div(m, 256) * ceil_div(n, 256) < kCus) return {kSmall, 1};
+  return {kMixed, 1};
+}
+
+template <int FA, typename TC>
+int launch_product(const Fp8GemmArgs& g, const ProductPlan& plan, hipStream_t st) {
+  switch (plan.kind) {
+    case kDirect:
+      if (g.m <= 16) return launch_direct<FA, TC, 1>(g, st);
+      if (g.m <= 32) return launch_direct<FA, TC, 2>(g, st);
+      return launch_direct<FA, TC, 4>(g, st);
+    case kSplit: {
+      const int status = g.m <= 64 ? launch_tile<FA, TC, 64, 128, 32, 64, 4, true>(g, st)
+                                   : launch_tile<FA, TC, 128, 128, 64, 64, 4, true>(g, st);
+      if (status != MUON_OK) return status;
+      launch_kernel(fp8_gemm_join_kernel<TC>, dim3(ceil_div(g.m * (g.ldp / 4), 256)), dim3(256), 0, st, g);
+      return launch_status();
+    }
+    case kSmall:
+      return launch_tile<FA, TC, 128, 128, 64, 64, 4, false>(g, st);
+    default: {
+      const int64_t tiles = ceil_div(g.m, 256) * ceil_div(g.n, 256), rest = tiles % kCus;
+      const int parts = rest * 4 <= kCus ? 4 : rest * 2 <= kCus ? 2 : 1;
+      if (rest == 0 || parts == 1) return launch_mixed<FA, TC>(g, tiles, 0, 1, st);
+      return launch_mixed<FA, TC>(g, tiles - rest, rest, parts, st);
+    }
   }
-  if (g.m <= 16) return launch_direct<FA, TC, 1>(g, st);
-  if (g.m <= 32) return launch_direct<FA, TC, 2>(g, st);
-  return launch_direct<FA, TC, 4>(g, st);
 }
 
 // the tiles address their 256 rows with 32-bit offsets
@@ -713,8 +918,9 @@ int fp8_quantize(const void* x, int x_dtype, int64_t rows, int64_t cols, int64_t
 }
 
 size_t fp8_gemm_workspace_bytes(int64_t m, int64_t n, int64_t K) {
-  (void)m; (void)n; (void)K;
-  return 0;
+  if (m <= 0 || n <= 0 || K <= 0 || m > MUON_FP8_MAX_SIDE || n > MUON_FP8_MAX_SIDE || K > MUON_FP8_MAX_SIDE) return 0;
+  const ProductPlan p = plan_product(m, n, K);
+  return p.kind == kSplit ? size_t(p.splits) * size_t(m) * size_t(ceil_div(n, 4) * 4) * 4 : 0;
 }
 
 int fp8_gemm(const void* A, int a_fmt, int64_t lda, const void* sa, const void* B, int b_fmt, int64_t ldb,
@@ -739,10 +945,14 @@ int fp8_gemm(const void* A, int a_fmt, int64_t lda, const void* sa, const void* 
   g.ra4 = scale_rows(m); g.rb4 = scale_rows(n);
   g.alpha = alpha; g.beta = beta;
   g.vec = ldc % 4 == 0;
-  hipStream_t st = static_cast<hipStream_t>(stream);
+  const ProductPlan plan = plan_product(m, n, K);
+  g.splits = plan.splits;
+  g.partials = static_cast<float*>(workspace);
+  g.ldp = ceil_div(n, 4) * 4;
+  hipStream_t hs = static_cast<hipStream_t>(stream);
   if (a_fmt == MUON_FP8_E4M3)
-    return c_dtype == MUON_F32 ? launch_product<0, float>(g, st) : launch_product<0, bf16_t>(g, st);
-  return c_dtype == MUON_F32 ? launch_product<1, float>(g, st) : launch_product<1, bf16_t>(g, st);
+    return c_dtype == MUON_F32 ? launch_product<0, float>(g, plan, hs) : launch_product<0, bf16_t>(g, plan, hs);
+  return c_dtype == MUON_F32 ? launch_product<1, float>(g, plan, hs) : launch_product<1, bf16_t>(g, plan, hs);
 }
 
 }  // extern "C"
