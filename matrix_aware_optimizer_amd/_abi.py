@@ -9,6 +9,7 @@ missing the first call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional, Sequence, Tuple, Union
 
@@ -152,8 +153,14 @@ def _dev(t: Optional[torch.Tensor], name: str) -> Optional[int]:
     return t.data_ptr()
 
 
+# the current stream's handle without building a Stream object (2 us of a call's host time)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> int:
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
@@ -588,6 +595,7 @@ def _ceil_to(n: int, m: int) -> int:
     return -(-n // m) * m
 
 
+@functools.lru_cache(maxsize=1024)
 def fp8_scale_shape(rows: int, cols: int) -> Tuple[int, int, int]:
     """Shape of the scale bytes of a rows x cols matrix: [words of four groups][rows][4]."""
     return _ceil_to(cols, 4 * MUON_FP8_GROUP) // (4 * MUON_FP8_GROUP), _ceil_to(rows, 4), 4
@@ -603,25 +611,33 @@ def _rows2(t: torch.Tensor, name: str) -> Tuple[int, int]:
     """(pointer, row pitch) of a 2-D device tensor whose rows are contiguous."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+    if t.dim() != 2:
         raise ValueError(f"{name} must be 2-D with contiguous rows")
-    if t.shape[0] > 1 and t.shape[1] > 0 and t.stride(0) < t.shape[1]:
+    rows, cols = t.shape
+    pitch, step = t.stride()
+    if cols > 1 and step != 1:
+        raise ValueError(f"{name} must be 2-D with contiguous rows")
+    if rows <= 1 or cols == 0:
+        return t.data_ptr(), max(cols, 1)
+    if pitch < cols:
         raise ValueError(f"{name} must not overlap itself")
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+    return t.data_ptr(), pitch
 
 
 def _fp8_operand(q: torch.Tensor, s: torch.Tensor, rows: int, cols: int, name: str):
-    """(codes, pitch, scales) of an fp8 matrix that holds rows x cols."""
-    if q.dtype not in _FP8:
+    """(codes, pitch, scales, format code) of an fp8 matrix that holds rows x cols."""
+    fmt = _FP8.get(q.dtype)
+    if fmt is None:
         raise TypeError(f"{name} must be float8_e4m3fn or float8_e5m2")
     ptr, ld = _rows2(q, name)
-    if q.shape[0] != rows or q.shape[1] < _ceil_to(cols, MUON_FP8_GROUP):
+    held, width = q.shape
+    if held != rows or width < _ceil_to(cols, MUON_FP8_GROUP):
         raise ValueError(f"{name} must hold {rows} rows of at least {_ceil_to(cols, MUON_FP8_GROUP)} codes")
-    if s.dtype != torch.uint8 or tuple(s.shape) != fp8_scale_shape(rows, cols):
+    if s.dtype != torch.uint8 or s.shape != fp8_scale_shape(rows, cols):
         raise ValueError(f"the scales of {name} must be uint8 of shape {fp8_scale_shape(rows, cols)}")
     if rows <= 1 or cols == 0:      # no second row: the pitch is not used, the library wants a multiple of 16
-        ld = _ceil_to(q.shape[1], 16)
-    return ptr, ld, _dev(s, f"scales of {name}")
+        ld = _ceil_to(width, 16)
+    return ptr, ld, _dev(s, name), fmt
 
 
 def fp8_quantize(x: torch.Tensor, q: Optional[torch.Tensor], s: Optional[torch.Tensor],
@@ -636,13 +652,14 @@ def fp8_quantize(x: torch.Tensor, q: Optional[torch.Tensor], s: Optional[torch.T
     rows, cols = x.shape
     if q is not None and qt is not None and q.dtype != qt.dtype:
         raise TypeError("q and qt must have one format")
-    qp = _fp8_operand(q, s, rows, cols, "q") if q is not None else (None, 0, None)
-    tp = _fp8_operand(qt, st, cols, rows, "qt") if qt is not None else (None, 0, None)
-    fmt = _FP8[(q if q is not None else qt).dtype]
+    qp = _fp8_operand(q, s, rows, cols, "q") if q is not None else (None, 0, None, 0)
+    tp = _fp8_operand(qt, st, cols, rows, "qt") if qt is not None else (None, 0, None, 0)
+    fmt = qp[3] if q is not None else tp[3]
     _check("fp8_quantize", lib().fp8_quantize(xp, dtype_code(x), rows, cols, max(ldx, cols), fmt, int(block_rows),
                                               qp[0], qp[1], qp[2], tp[0], tp[1], tp[2], _stream(stream)))
 
 
+@functools.lru_cache(maxsize=1024)
 def fp8_gemm_workspace_bytes(m: int, n: int, K: int) -> int:
     return int(lib().fp8_gemm_workspace_bytes(m, n, K))
 
@@ -651,19 +668,21 @@ def fp8_gemm(A: torch.Tensor, sa: torch.Tensor, B: torch.Tensor, sb: torch.Tenso
              alpha: float = 1.0, beta: float = 0.0, workspace: Optional[torch.Tensor] = None, stream=None) -> None:
     """``C <- beta C + alpha A B^T`` for fp8 operands (codes, scales) with K = ``A.shape[1]`` columns."""
     m, K = A.shape
-    n = B.shape[0]
-    if B.shape[1] != K or tuple(C.shape) != (m, n):
+    n, kb = B.shape
+    if kb != K or C.shape != (m, n):
         raise ValueError("A is m x K, B n x K and C m x n")
-    ap, lda, sap = _fp8_operand(A, sa, m, K, "A")
-    bp, ldb, sbp = _fp8_operand(B, sb, n, K, "B")
+    ap, lda, sap, fa = _fp8_operand(A, sa, m, K, "A")
+    bp, ldb, sbp, fb = _fp8_operand(B, sb, n, K, "B")
     cp, ldc = _rows2(C, "C")
     need = fp8_gemm_workspace_bytes(m, n, K)
     ws, nbytes = None, 0
     if need > 0:
         workspace = _workspace(need, C, workspace)
         ws, nbytes = _dev(workspace, "workspace"), workspace.numel() * workspace.element_size()
-    _check("fp8_gemm", lib().fp8_gemm(ap, _FP8[A.dtype], lda, sap, bp, _FP8[B.dtype], ldb, sbp, cp, dtype_code(C),
-                                      max(ldc, n), m, n, K, float(alpha), float(beta), ws, nbytes, _stream(stream)))
+    status = lib().fp8_gemm(ap, fa, lda, sap, bp, fb, ldb, sbp, cp, dtype_code(C), ldc if ldc > n else n, m, n, K,
+                            alpha, beta, ws, nbytes, _stream(stream))
+    if status:
+        _check("fp8_gemm", status)
 
 
 # ---------------------------------------------------------------------------

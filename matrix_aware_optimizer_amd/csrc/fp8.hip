@@ -394,7 +394,7 @@ __global__ __launch_bounds__(1024) void fp8_gemm_direct_kernel(Fp8GemmArgs g) {
 template <int FA, typename TC, int MT>
 int launch_direct(const Fp8GemmArgs& g, hipStream_t st) {
   const int64_t groups = g.K / kGroup;
-  const int waves = int(std::max<int64_t>(1, std::min<int64_t>(groups, 8)));
+  const int waves = int(std::max<int64_t>(1, std::min<int64_t>(groups / 8, 8)));   // eight groups each, up to eight waves
   const uint32_t lds = waves > 1 ? uint32_t(waves) * MT * 4 * 64 * 4 : 0;
   const dim3 grid(ceil_div(g.n, 16), ceil_div(g.m, 16 * MT));
   launch_kernel(fp8_gemm_direct_kernel<FA, TC, MT>, grid, dim3(64 * waves), lds, st, g);
