@@ -21,3 +21,4 @@ from ._abi import MUON_FP8_GROUP, MUON_FP8_MAX_SIDE, fp8_buffers, fp8_gemm, fp8_
 from ._abi import fp8_quantize, fp8_scale_shape  # noqa: F401
 from ._abi import MUON_BLOCKS_MAX_SHORT, PreparedNSBlocks, ns_blocks, ns_blocks_update  # noqa: F401
 from ._abi import ns_blocks_workspace_bytes  # noqa: F401
+from .blocklinear import BlockLinear  # noqa: F401

@@ -359,6 +359,7 @@ template <int NY, int NS>
 __device__ __forceinline__ void sym_product(const char* buf, int lane, const SymOperand<NY> (&o)[NS],
                                             f32x4_t (&out)[NS][NY]) {
   constexpr int NT = NY / 2, PIECES = NY * NT, DEPTH = PIECES < 4 ? 1 : 3;
+  constexpr int CHAINS = 2;   // sums per strip: two independent ones follow each other either way
   const char* row = buf + (lane & 15) * SymLds<NY>::PITCH + 16 * (lane >> 4);
   bf16x8_t f[DEPTH + 1][kParts];
   auto read = [&](int k) __attribute__((always_inline)) {
@@ -371,9 +372,11 @@ __device__ __forceinline__ void sym_product(const char* buf, int lane, const Sym
   for (int k = 0; k < DEPTH; ++k) read(k);
 #pragma unroll
   for (int y = 0; y < NY; ++y) {
-    f32x4_t acc[NS], low[NS];
+    f32x4_t acc[CHAINS][NS];
 #pragma unroll
-    for (int i = 0; i < NS; ++i) acc[i] = low[i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int h = 0; h < CHAINS; ++h)
+#pragma unroll
+      for (int i = 0; i < NS; ++i) acc[h][i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       const int k = y * NT + t;
@@ -385,13 +388,16 @@ __device__ __forceinline__ void sym_product(const char* buf, int lane, const Sym
         for (int r = 0; p + r < kParts; ++r)
 #pragma unroll
           for (int i = 0; i < NS; ++i) {
-            f32x4_t& to = (p + r) == 2 ? low[i] : acc[i];   // two chains of three
+            f32x4_t& to = acc[(p + r) == 2 ? CHAINS - 1 : 0][i];
             to = __builtin_amdgcn_mfma_f32_16x16x32_bf16(s[p], o[i].p[r][t], to, 0, 0, 0);
           }
       __builtin_amdgcn_sched_barrier(0);
     }
 #pragma unroll
-    for (int i = 0; i < NS; ++i) out[i][y] = acc[i] + low[i];
+    for (int i = 0; i < NS; ++i) {
+      if constexpr (CHAINS == 2) out[i][y] = acc[0][i] + acc[1][i];
+      else out[i][y] = acc[0][i];
+    }
   }
 }
 
@@ -426,8 +432,10 @@ __global__ __launch_bounds__(64 * NY / strips<NY>()) void blocks_poly_kernel(Run
       for (int y = 0; y < NY; ++y) f(i, y);
   };
   auto column = [&](int i) { return 16 * (NS * wave + i) + r; };
-  // the entry v of (i, y) lies on the diagonal
-  auto diag = [&](int i, int y, int v) { return 16 * y + 4 * g + v == column(i); };
+  // the identity's entries in a tile on the diagonal (y == strip)
+  float unit[4];
+#pragma unroll
+  for (int v = 0; v < 4; ++v) unit[v] = 4 * g + v == r ? 1.0f : 0.0f;
   {
     // The partial Grams are lower 32 x 32 tiles as they lay in the accumulators: float4 q of
     // a tile is value v = q / 16 of lanes 4 (q % 16) .., row 8 (v / 4) + 4 (lane / 32) + v % 4,
@@ -483,7 +491,7 @@ __global__ __launch_bounds__(64 * NY / strips<NY>()) void blocks_poly_kernel(Run
   each([&](int i, int y) __attribute__((always_inline)) {
     A[i][y] *= inv;
 #pragma unroll
-    for (int v = 0; v < 4; ++v) T[i][y][v] = diag(i, y, v) ? 1.0f : 0.0f;
+    for (int v = 0; v < 4; ++v) T[i][y][v] = y == NS * wave + i ? unit[v] : 0.0f;
   });
   auto split = [&](const f32x4_t (&v)[NS][NY], SymOperand<NY> (&o)[NS]) __attribute__((always_inline)) {
 #pragma unroll
@@ -528,8 +536,9 @@ __global__ __launch_bounds__(64 * NY / strips<NY>()) void blocks_poly_kernel(Run
       each([&](int i, int y) __attribute__((always_inline)) { P[i][y] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f}; });
     }
     each([&](int i, int y) __attribute__((always_inline)) {
+      const float on = y == NS * wave + i ? a : 0.0f;        // this tile lies on the diagonal
 #pragma unroll
-      for (int v = 0; v < 4; ++v) P[i][y][v] = fmaf(c, P[i][y][v], fmaf(b, A[i][y][v], diag(i, y, v) ? a : 0.0f));
+      for (int v = 0; v < 4; ++v) P[i][y][v] = fmaf(c, P[i][y][v], fmaf(b, A[i][y][v], on * unit[v]));
     });
     SymOperand<NY> o[NS];
     split(P, o);
