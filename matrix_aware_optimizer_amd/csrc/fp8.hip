@@ -17,7 +17,6 @@ namespace muon {
 namespace {
 
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
-typedef float f32x2_t __attribute__((ext_vector_type(2)));
 
 // 32 bytes of a matrix operand from two 16-byte reads
 __device__ __forceinline__ i32x8_t join(const u32x4_t (&v)[2]) {
@@ -41,7 +40,7 @@ inline int64_t scale_rows(int64_t rows) { return ceil_div(rows, 4) * 4; }
 // amax = m 2^E (1 <= m < 2): the smallest e with amax <= MAX 2^e, MAX = 1.75 2^8
 // (e4m3) or 1.75 2^15 (e5m2), is E - 8 (or 15), plus one when m > 1.75.  In bits:
 // the biased exponent field less that, plus one when the fraction is over 0x600000.
-// The byte is held to 1 .. 254 so that its inverse 2^-e is a normal fp32.
+// The byte is at least 1, so that 2^e is a normal fp32.
 template <int FMT>
 __device__ __forceinline__ uint32_t scale_byte(uint32_t amax_bits) {
   constexpr int drop = FMT == MUON_FP8_E4M3 ? 8 : 15;
@@ -49,15 +48,15 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t amax_bits) {
   const int b = int(amax_bits >> 23) - drop + ((amax_bits & 0x7fffffu) > 0x600000u ? 1 : 0);
   return uint32_t(b < 1 ? 1 : b);
 }
-__device__ __forceinline__ float inverse_scale(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }
-
-// |x| as bits, 0 for infinities and NaN: they take no part in a group's scale
-__device__ __forceinline__ uint32_t finite_abs_bits(float x) {
-  const uint32_t u = __float_as_uint(x) & 0x7fffffffu;
-  return u < 0x7f800000u ? u : 0u;
-}
+// 2^e as the scaled conversions take it
+__device__ __forceinline__ float scale_float(uint32_t byte) { return __uint_as_float(byte << 23); }
 
 __device__ __forceinline__ uint32_t max_u32(uint32_t a, uint32_t b) { return a > b ? a : b; }
+
+typedef unsigned short u16x2_t __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2_t, a), __builtin_bit_cast(u16x2_t, b)));
+}
 
 // maximum over the 16 lanes of a DPP row, in every lane (rotations by 8, 4, 2, 1)
 __device__ __forceinline__ uint32_t row16_max(uint32_t v) {
@@ -68,19 +67,129 @@ __device__ __forceinline__ uint32_t row16_max(uint32_t v) {
   return v;
 }
 
-// Four codes of x 2^-e in one word.  The product with a power of two is exact (or
-// far below the format's smallest step), so each entry is rounded once, to
-// nearest even, by the conversion.  e4m3 has no infinity: an infinite entry
-// becomes NaN there, as NaN does.
-template <int FMT>
-__device__ __forceinline__ uint32_t pack4(float a, float b, float c, float d) {
-  if (FMT == MUON_FP8_E4M3) {
-    const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
-    return uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(c, d, lo, true));
+// A thread's 8 x 8 entries.  Maxima are of |x| as bits (of the fp32 value); with FINITE
+// infinities and NaN count as 0, without it they show as 0x7f800000 or more.  The codes
+// come from the scaled conversions, x 2^-e rounded once to nearest even; e4m3 has no
+// infinity: an infinite entry becomes NaN there, as NaN does.
+typedef short s16x2_t __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+typedef float f32x2_t __attribute__((ext_vector_type(2)));
+
+template <typename T> struct Cells;
+
+// bf16 stays packed: two columns per register
+template <> struct Cells<bf16_t> {
+  uint32_t w[8][4];
+  static constexpr int COLS = 4;   // registers of column maxima
+
+  __device__ __forceinline__ void load(int p, const bf16_t* src, int64_t left, bool vec) {
+    if (vec && left >= 8) {
+      const uint4 r = *reinterpret_cast<const uint4*>(src);
+      w[p][0] = r.x; w[p][1] = r.y; w[p][2] = r.z; w[p][3] = r.w;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t lo = 2 * j < left ? src[2 * j] : 0u, hi = 2 * j + 1 < left ? src[2 * j + 1] : 0u;
+        w[p][j] = lo | (hi << 16);
+      }
+    }
   }
-  const int lo = __builtin_amdgcn_cvt_pk_bf8_f32(a, b, 0, false);
-  return uint32_t(__builtin_amdgcn_cvt_pk_bf8_f32(c, d, lo, true));
-}
+  template <bool FINITE> __device__ __forceinline__ uint32_t abs2(int p, int j) const {
+    uint32_t a = w[p][j] & 0x7fff7fffu;
+    if (FINITE) {
+      if ((a & 0xffffu) >= 0x7f80u) a &= 0xffff0000u;
+      if (a >= 0x7f800000u) a &= 0xffffu;
+    }
+    return a;
+  }
+  template <bool FINITE> __device__ __forceinline__ uint32_t row(int p) const {
+    const uint32_t m = max_u16x2(max_u16x2(abs2<FINITE>(p, 0), abs2<FINITE>(p, 1)),
+                                 max_u16x2(abs2<FINITE>(p, 2), abs2<FINITE>(p, 3)));
+    return max_u32(m << 16, m & 0xffff0000u);
+  }
+  template <bool FINITE> __device__ __forceinline__ uint32_t col(int c) const {
+    uint32_t m = abs2<FINITE>(0, c);
+#pragma unroll
+    for (int p = 1; p < 8; ++p) m = max_u16x2(m, abs2<FINITE>(p, c));
+    return m;
+  }
+  __device__ __forceinline__ static uint32_t join(uint32_t a, uint32_t b) { return max_u16x2(a, b); }
+  // maximum of column j from the registers of column maxima
+  __device__ __forceinline__ static uint32_t of_column(const uint32_t (&m)[4], int j) {
+    return (j & 1) ? m[j >> 1] & 0xffff0000u : m[j >> 1] << 16;
+  }
+  template <int FMT> __device__ __forceinline__ static uint32_t codes(uint32_t a, uint32_t b, float scale) {
+    s16x2_t r = {0, 0};
+    if constexpr (FMT == MUON_FP8_E4M3) {
+      r = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(r, __builtin_bit_cast(bf16x2_t, a), scale, false);
+      r = __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(r, __builtin_bit_cast(bf16x2_t, b), scale, true);
+    } else {
+      r = __builtin_amdgcn_cvt_scalef32_pk_bf8_bf16(r, __builtin_bit_cast(bf16x2_t, a), scale, false);
+      r = __builtin_amdgcn_cvt_scalef32_pk_bf8_bf16(r, __builtin_bit_cast(bf16x2_t, b), scale, true);
+    }
+    return __builtin_bit_cast(uint32_t, r);
+  }
+  template <int FMT> __device__ __forceinline__ uint2 row_codes(int p, float s) const {
+    return make_uint2(codes<FMT>(w[p][0], w[p][1], s), codes<FMT>(w[p][2], w[p][3], s));
+  }
+  template <int FMT> __device__ __forceinline__ uint2 col_codes(int j, float s) const {
+    uint32_t v[4];   // rows 2 q, 2 q + 1 of column j
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      v[q] = (j & 1) ? __builtin_amdgcn_perm(w[2 * q + 1][j >> 1], w[2 * q][j >> 1], 0x07060302u)
+                     : __builtin_amdgcn_perm(w[2 * q + 1][j >> 1], w[2 * q][j >> 1], 0x05040100u);
+    return make_uint2(codes<FMT>(v[0], v[1], s), codes<FMT>(v[2], v[3], s));
+  }
+};
+
+template <> struct Cells<float> {
+  float v[8][8];
+  static constexpr int COLS = 8;
+
+  __device__ __forceinline__ void load(int p, const float* src, int64_t left, bool vec) {
+    if (vec && left >= 8) {
+      Vec8<float>::load(src, v[p]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[p][j] = j < left ? src[j] : 0.0f;
+    }
+  }
+  template <bool FINITE> __device__ __forceinline__ uint32_t abs1(int p, int j) const {
+    const uint32_t a = __float_as_uint(v[p][j]) & 0x7fffffffu;
+    return FINITE && a >= 0x7f800000u ? 0u : a;
+  }
+  template <bool FINITE> __device__ __forceinline__ uint32_t row(int p) const {
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = max_u32(m, abs1<FINITE>(p, j));
+    return m;
+  }
+  template <bool FINITE> __device__ __forceinline__ uint32_t col(int j) const {
+    uint32_t m = 0;
+#pragma unroll
+    for (int p = 0; p < 8; ++p) m = max_u32(m, abs1<FINITE>(p, j));
+    return m;
+  }
+  __device__ __forceinline__ static uint32_t join(uint32_t a, uint32_t b) { return max_u32(a, b); }
+  __device__ __forceinline__ static uint32_t of_column(const uint32_t (&m)[8], int j) { return m[j]; }
+  template <int FMT> __device__ __forceinline__ static uint32_t codes(float a, float b, float c, float d, float scale) {
+    s16x2_t r = {0, 0};
+    if constexpr (FMT == MUON_FP8_E4M3) {
+      r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, a, b, scale, false);
+      r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, c, d, scale, true);
+    } else {
+      r = __builtin_amdgcn_cvt_scalef32_pk_bf8_f32(r, a, b, scale, false);
+      r = __builtin_amdgcn_cvt_scalef32_pk_bf8_f32(r, c, d, scale, true);
+    }
+    return __builtin_bit_cast(uint32_t, r);
+  }
+  template <int FMT> __device__ __forceinline__ uint2 row_codes(int p, float s) const {
+    return make_uint2(codes<FMT>(v[p][0], v[p][1], v[p][2], v[p][3], s), codes<FMT>(v[p][4], v[p][5], v[p][6], v[p][7], s));
+  }
+  template <int FMT> __device__ __forceinline__ uint2 col_codes(int j, float s) const {
+    return make_uint2(codes<FMT>(v[0][j], v[1][j], v[2][j], v[3][j], s), codes<FMT>(v[4][j], v[5][j], v[6][j], v[7][j], s));
+  }
+};
 
 struct QuantArgs {
   const void* x;
@@ -98,29 +207,34 @@ struct QuantArgs {
 // or 4 bytes read and 1 or 2 written per entry.
 template <typename T, int FMT, bool BLOCK>
 __global__ __launch_bounds__(256) void fp8_quantize_kernel(QuantArgs g) {
+  using C_ = Cells<T>;
+  constexpr int NC = C_::COLS;
   __shared__ __attribute__((aligned(16))) char tile[128 * 128];
-  __shared__ uint32_t colmax[4][128];
+  __shared__ uint32_t colmax[4][16 * NC];
   const int t = threadIdx.x, cg = t & 15, rg = t >> 4, wave = t >> 6;
   const int64_t kb = blockIdx.x, rb = blockIdx.y;
   const int64_t c0 = kb * 128 + 8 * cg, r0 = rb * 128 + 8 * rg;
-  float v[8][8];
+  C_ x;
 #pragma unroll
-  for (int p = 0; p < 8; ++p) {
-    const T* src = static_cast<const T*>(g.x) + (r0 + p) * g.ldx + c0;
-    if (r0 + p < g.rows && c0 + 8 <= g.cols && g.vec) {
-      Vec8<T>::load(src, v[p]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[p][j] = (r0 + p < g.rows && c0 + j < g.cols) ? to_f32(src[j]) : 0.0f;
-    }
-  }
+  for (int p = 0; p < 8; ++p)
+    x.load(p, static_cast<const T*>(g.x) + (r0 + p) * g.ldx + c0, r0 + p < g.rows ? g.cols - c0 : 0, g.vec);
   const bool rows_out = g.q != nullptr, cols_out = g.qt != nullptr;
-  uint32_t all = 0;
+  uint32_t rm[8], cm[NC], all = 0;
+  auto maxima = [&](auto finite) __attribute__((always_inline)) {
+    constexpr bool FINITE = decltype(finite)::value;
+    all = 0;
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+      rm[p] = x.template row<FINITE>(p);
+      all = max_u32(all, rm[p]);
+    }
+    if (!BLOCK && cols_out)
+#pragma unroll
+      for (int c = 0; c < NC; ++c) cm[c] = x.template col<FINITE>(c);
+  };
+  maxima(std::false_type{});
+  if (__any(all >= 0x7f800000u)) maxima(std::true_type{});   // infinities or NaN: leave them out
   if (BLOCK) {
-#pragma unroll
-    for (int p = 0; p < 8; ++p)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) all = max_u32(all, finite_abs_bits(v[p][j]));
     all = row16_max(all);
     all = max_u32(all, uint32_t(__shfl_xor(int(all), 16, kWave)));
     all = max_u32(all, uint32_t(__shfl_xor(int(all), 32, kWave)));
@@ -133,21 +247,9 @@ __global__ __launch_bounds__(256) void fp8_quantize_kernel(QuantArgs g) {
     const int64_t R4 = (g.rows + 3) / 4 * 4;
 #pragma unroll
     for (int p = 0; p < 8; ++p) {
-      uint32_t m = all;
-      if (!BLOCK) {
-        m = 0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) m = max_u32(m, finite_abs_bits(v[p][j]));
-        m = row16_max(m);
-      }
-      const uint32_t byte = scale_byte<FMT>(m);
-      const float inv = inverse_scale(byte);
+      const uint32_t byte = scale_byte<FMT>(BLOCK ? all : row16_max(rm[p]));
       const int64_t r = r0 + p;
-      if (r < g.rows) {
-        const uint2 w = make_uint2(pack4<FMT>(v[p][0] * inv, v[p][1] * inv, v[p][2] * inv, v[p][3] * inv),
-                                   pack4<FMT>(v[p][4] * inv, v[p][5] * inv, v[p][6] * inv, v[p][7] * inv));
-        *reinterpret_cast<uint2*>(g.q + r * g.ldq + c0) = w;
-      }
+      if (r < g.rows) *reinterpret_cast<uint2*>(g.q + r * g.ldq + c0) = x.template row_codes<FMT>(p, scale_float(byte));
       if (cg == 0 && r < R4) {
         uint8_t* dst = g.s + ((kb >> 2) * R4 + r) * 4;
         dst[kb & 3] = r < g.rows ? byte : 127;
@@ -157,31 +259,24 @@ __global__ __launch_bounds__(256) void fp8_quantize_kernel(QuantArgs g) {
     }
   }
   if (!cols_out) return;
-  uint32_t m[8];
   if (!BLOCK) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      uint32_t c = 0;
-#pragma unroll
-      for (int p = 0; p < 8; ++p) c = max_u32(c, finite_abs_bits(v[p][j]));
-      c = max_u32(c, uint32_t(__shfl_xor(int(c), 16, kWave)));
-      c = max_u32(c, uint32_t(__shfl_xor(int(c), 32, kWave)));
-      if ((t & 63) < 16) colmax[wave][8 * cg + j] = c;
+    for (int c = 0; c < NC; ++c) {
+      cm[c] = C_::join(cm[c], uint32_t(__shfl_xor(int(cm[c]), 16, kWave)));
+      cm[c] = C_::join(cm[c], uint32_t(__shfl_xor(int(cm[c]), 32, kWave)));
+      if ((t & 63) < 16) colmax[wave][NC * cg + c] = cm[c];
     }
     __syncthreads();
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      m[j] = max_u32(max_u32(colmax[0][8 * cg + j], colmax[1][8 * cg + j]),
-                     max_u32(colmax[2][8 * cg + j], colmax[3][8 * cg + j]));
+    for (int c = 0; c < NC; ++c)
+      cm[c] = C_::join(C_::join(colmax[0][NC * cg + c], colmax[1][NC * cg + c]),
+                       C_::join(colmax[2][NC * cg + c], colmax[3][NC * cg + c]));
   }
   const int64_t C4 = (g.cols + 3) / 4 * 4;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const uint32_t byte = scale_byte<FMT>(BLOCK ? all : m[j]);
-    const float inv = inverse_scale(byte);
-    const uint2 w = make_uint2(pack4<FMT>(v[0][j] * inv, v[1][j] * inv, v[2][j] * inv, v[3][j] * inv),
-                               pack4<FMT>(v[4][j] * inv, v[5][j] * inv, v[6][j] * inv, v[7][j] * inv));
-    *reinterpret_cast<uint2*>(tile + (8 * cg + j) * 128 + ((rg ^ cg) << 3)) = w;
+    const uint32_t byte = scale_byte<FMT>(BLOCK ? all : C_::of_column(cm, j));
+    *reinterpret_cast<uint2*>(tile + (8 * cg + j) * 128 + ((rg ^ cg) << 3)) = x.template col_codes<FMT>(j, scale_float(byte));
     const int64_t c = c0 + j;
     if (rg == 0 && c < C4) {
       uint8_t* dst = g.st + ((rb >> 2) * C4 + c) * 4;
@@ -271,7 +366,6 @@ __device__ __forceinline__ void store4(const Fp8GemmArgs& g, int64_t row, int64_
 // fp32 C (a momentum that gradients are summed into) keeps what fp32 holds: its
 // codes are widened to bf16 with their scale (v_cvt_scalef32_pk_bf16_*, exact) and
 // multiplied on the bf16 instructions.
-typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 
 // eight codes times their scale, as bf16 (exact: at most four significant bits)
 template <int FMT>
