@@ -583,9 +583,8 @@ int fp8_gemm(const void* A, int a_fmt, int64_t lda, const void* sa, const void* 
  * At most MUON_BLOCKS_MAX_PROBLEMS problems, MUON_BLOCKS_MAX_COUNT blocks each,
  * long sides up to MUON_BLOCKS_MAX_LONG, strides positive where count > 1, ld
  * at least cols, and under 2^31 units of 64 long-side entries over all blocks
- * (MUON_EINVAL).  M and out 16-byte aligned; blocks whose pitch or stride is
- * not a multiple of 16 bytes are read entry by entry.  Empty problems (count,
- * rows or cols 0) are skipped.
+ * (MUON_EINVAL).  M and out 16-byte aligned; pitches and strides may be any
+ * number of entries.  Empty problems (count, rows or cols 0) are skipped.
  * ------------------------------------------------------------------------- */
 #define MUON_BLOCKS_MAX_SHORT 128
 #define MUON_BLOCKS_MAX_LONG (1 << 24)

@@ -43,7 +43,7 @@ struct Run {
   int64_t ld_m, stride_m, ld_out, stride_out;
   int64_t partials, parts;   // byte offsets of its partial Grams and its T in the workspace
   int32_t s, l, count, chunk, chunks, slabs, units;   // chunk: k-values per gram unit; slabs per apply unit
-  int32_t vec_m, vec_out, kind;   // kind: kTall | kF32 | kBig
+  int32_t kind;   // kTall | kF32 | kBig
   int32_t out_f32;
 };
 enum { kTall = 1, kF32 = 2, kBig = 4 };   // kBig: a short side over 64
@@ -103,8 +103,7 @@ struct Region {
   static constexpr int E = 16 / sizeof(T);
   uint4 w[LD];
 
-  __device__ __forceinline__ void fetch(const T* src, int64_t ld, int rows, int cols, int r0, int c0, int NR, int NC,
-                                        bool vec) {
+  __device__ __forceinline__ void fetch(const T* src, int64_t ld, int rows, int cols, int r0, int c0, int NR, int NC) {
     const int per = NC / E, n = NR * per;
 #pragma unroll
     for (int q = 0; q < LD; ++q) {
@@ -114,8 +113,8 @@ struct Region {
         const int r = t / per, c = (t % per) * E;
         const T* p = src + int64_t(r0 + r) * ld + c0 + c;
         if (r0 + r < rows) {
-          if (vec && c0 + c + E <= cols) {
-            w[q] = *reinterpret_cast<const uint4*>(p);
+          if (c0 + c + E <= cols) {
+            w[q] = load16(p);
           } else {
             uint32_t e[E];
 #pragma unroll
@@ -138,7 +137,7 @@ struct Region {
 
   // tile holds U for the region: dst = U, or c1 (what fetch() got) - c2 U
   __device__ __forceinline__ void finish(const float* tile, int tile_ld, T* dst, int64_t ld, int rows, int cols, int r0,
-                                         int c0, int NR, int NC, bool vec, const Epilogue& e) const {
+                                         int c0, int NR, int NC, const Epilogue& e) const {
     const int per = NC / E, n = NR * per;
 #pragma unroll
     for (int q = 0; q < LD; ++q) {
@@ -164,7 +163,7 @@ struct Region {
           }
         }
         T* p = dst + int64_t(r0 + r) * ld + c0 + c;
-        if (vec && c0 + c + E <= cols) {
+        if (c0 + c + E <= cols) {
           uint4 o;
           if constexpr (sizeof(T) == 2) {
             f32x2_t a = {v[0], v[1]}, b = {v[2], v[3]}, g = {v[4], v[5]}, h = {v[6], v[7]};
@@ -175,7 +174,7 @@ struct Region {
           } else {
             o = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
           }
-          *reinterpret_cast<uint4*>(p) = o;
+          store16(p, o);
         } else {
 #pragma unroll
           for (int k = 0; k < E; ++k)
@@ -248,7 +247,6 @@ __global__ __launch_bounds__(256) void blocks_gram_kernel(Runs runs, char* ws) {
   const int s = run.s, l = run.l, nt = (s + 31) / 32, sp = nt * 32;
   const T* M = static_cast<const T*>(run.M) + b * run.stride_m;
   const int64_t ld = run.ld_m;
-  const bool vec = run.vec_m;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int nlow = tiles_of(nt);
   const int k0 = chunk * run.chunk, k1 = min(l, k0 + run.chunk);
@@ -259,8 +257,8 @@ __global__ __launch_bounds__(256) void blocks_gram_kernel(Runs runs, char* ws) {
     for (int v = 0; v < 16; ++v) acc[q][v] = 0.0f;
   Region<T, BIG ? 4 : 2> reg;
   auto fetch = [&](int k) __attribute__((always_inline)) {
-    if (TALL) reg.fetch(M, ld, k1, s, k, 0, SLAB, sp, vec);
-    else reg.fetch(M, ld, s, k1, 0, k, sp, SLAB, vec);
+    if (TALL) reg.fetch(M, ld, k1, s, k, 0, SLAB, sp);
+    else reg.fetch(M, ld, s, k1, 0, k, sp, SLAB);
   };
   fetch(k0);
   for (int k = k0; k < k1; k += SLAB) {
@@ -605,7 +603,6 @@ __global__ __launch_bounds__(256, 2) void blocks_apply_kernel(Runs runs, const c
   const T* M = static_cast<const T*>(run.M) + b * run.stride_m;
   TO* out = static_cast<TO*>(run.out) + b * run.stride_out;
   const int64_t ld = run.ld_m, ld_out = run.ld_out;
-  const bool vec = run.vec_m, vec_out = run.vec_out;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int fr = lane & 31, h = lane >> 5;
   // 4 waves: row tile ti, and every groups-th 32 entries of the long side
@@ -615,8 +612,8 @@ __global__ __launch_bounds__(256, 2) void blocks_apply_kernel(Runs runs, const c
   Region<T, C_::M_LOADS> reg;
   Region<TO, C_::OUT_LOADS> old;
   auto fetch = [&](int x) __attribute__((always_inline)) {
-    if (TALL) reg.fetch(M, ld, l, s, x, 0, LS, sp, vec);
-    else reg.fetch(M, ld, s, l, 0, x, sp, LS, vec);
+    if (TALL) reg.fetch(M, ld, l, s, x, 0, LS, sp);
+    else reg.fetch(M, ld, s, l, 0, x, sp, LS);
   };
   fetch(l0);
   u32x4_t tf[NPT][NQ];
@@ -635,8 +632,8 @@ __global__ __launch_bounds__(256, 2) void blocks_apply_kernel(Runs runs, const c
     else reg.template store<NPM>(lds, PITCH, PLANE, sp, LS);
     __syncthreads();
     if (e.update) {
-      if (TALL) old.fetch(out, ld_out, l, s, x, 0, LS, sp, vec_out);
-      else old.fetch(out, ld_out, s, l, 0, x, sp, LS, vec_out);
+      if (TALL) old.fetch(out, ld_out, l, s, x, 0, LS, sp);
+      else old.fetch(out, ld_out, s, l, 0, x, sp, LS);
     }
     if (x + LS < l1) fetch(x + LS);
     f32x16_t acc[TILES];
@@ -678,8 +675,8 @@ __global__ __launch_bounds__(256, 2) void blocks_apply_kernel(Runs runs, const c
       }
     }
     __syncthreads();
-    if (TALL) old.finish(tile, C_::OUT_LD, out, ld_out, l, s, x, 0, LS, sp, vec_out, e);
-    else old.finish(tile, C_::OUT_LD, out, ld_out, s, l, 0, x, sp, LS, vec_out, e);
+    if (TALL) old.finish(tile, C_::OUT_LD, out, ld_out, l, s, x, 0, LS, sp, e);
+    else old.finish(tile, C_::OUT_LD, out, ld_out, s, l, 0, x, sp, LS, e);
   }
 }
 
@@ -721,10 +718,6 @@ Run make_run(const muon_block_problem& p, int64_t total_blocks, size_t& bytes) {
   r.s = int(std::min(p.rows, p.cols)); r.l = int(std::max(p.rows, p.cols)); r.count = int(p.count);
   r.kind = (tall ? kTall : 0) | (p.m_dtype == MUON_F32 ? kF32 : 0) | (r.s > 64 ? kBig : 0);
   r.out_f32 = p.out_dtype == MUON_F32;
-  const int64_t em = p.m_dtype == MUON_F32 ? 4 : 8;
-  r.vec_m = p.ld_m % em == 0 && (p.count <= 1 || p.stride_m % em == 0);
-  const int64_t eo = p.out_dtype == MUON_F32 ? 4 : 8;
-  r.vec_out = p.ld_out % eo == 0 && (p.count <= 1 || p.stride_out % eo == 0);
   cut(r, total_blocks);
   const int64_t nt = ceil_div(r.s, 32), sp = nt * 32;
   r.partials = int64_t(bytes);

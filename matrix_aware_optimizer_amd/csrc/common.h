@@ -19,6 +19,36 @@ typedef float f32x16_t __attribute__((ext_vector_type(16)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 typedef unsigned int u32x4_t __attribute__((ext_vector_type(4)));
 
+// 16 (or 8) bytes of global memory at any entry of type T: the device loads and stores
+// them in one access whatever the address, so rows need no alignment of their own.
+template <typename T> struct Unaligned;
+template <> struct Unaligned<float> {
+  typedef unsigned int x4 __attribute__((ext_vector_type(4), aligned(4)));
+  typedef unsigned int x2 __attribute__((ext_vector_type(2), aligned(4)));
+};
+template <> struct Unaligned<bf16_t> {
+  typedef unsigned int x4 __attribute__((ext_vector_type(4), aligned(2)));
+  typedef unsigned int x2 __attribute__((ext_vector_type(2), aligned(2)));
+};
+template <typename T> __device__ __forceinline__ uint4 load16(const T* p) {
+  const typename Unaligned<T>::x4 v = *reinterpret_cast<const typename Unaligned<T>::x4*>(p);
+  return make_uint4(v[0], v[1], v[2], v[3]);
+}
+template <typename T> __device__ __forceinline__ void store16(T* p, const uint4& v) {
+  typename Unaligned<T>::x4 w;
+  w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+  *reinterpret_cast<typename Unaligned<T>::x4*>(p) = w;
+}
+template <typename T> __device__ __forceinline__ uint2 load8(const T* p) {
+  const typename Unaligned<T>::x2 v = *reinterpret_cast<const typename Unaligned<T>::x2*>(p);
+  return make_uint2(v[0], v[1]);
+}
+template <typename T> __device__ __forceinline__ void store8(T* p, const uint2& v) {
+  typename Unaligned<T>::x2 w;
+  w[0] = v.x; w[1] = v.y;
+  *reinterpret_cast<typename Unaligned<T>::x2*>(p) = w;
+}
+
 constexpr int kWave = 64;
 
 // Host-side one-time set-up is tracked per device (ordinals 0..63) with

@@ -82,9 +82,9 @@ template <> struct Cells<bf16_t> {
   uint32_t w[8][4];
   static constexpr int COLS = 4;   // registers of column maxima
 
-  __device__ __forceinline__ void load(int p, const bf16_t* src, int64_t left, bool vec) {
-    if (vec && left >= 8) {
-      const uint4 r = *reinterpret_cast<const uint4*>(src);
+  __device__ __forceinline__ void load(int p, const bf16_t* src, int64_t left) {
+    if (left >= 8) {
+      const uint4 r = load16(src);
       w[p][0] = r.x; w[p][1] = r.y; w[p][2] = r.z; w[p][3] = r.w;
     } else {
 #pragma unroll
@@ -146,9 +146,11 @@ template <> struct Cells<float> {
   float v[8][8];
   static constexpr int COLS = 8;
 
-  __device__ __forceinline__ void load(int p, const float* src, int64_t left, bool vec) {
-    if (vec && left >= 8) {
-      Vec8<float>::load(src, v[p]);
+  __device__ __forceinline__ void load(int p, const float* src, int64_t left) {
+    if (left >= 8) {
+      const uint4 a = load16(src), b = load16(src + 4);
+      v[p][0] = __uint_as_float(a.x); v[p][1] = __uint_as_float(a.y); v[p][2] = __uint_as_float(a.z); v[p][3] = __uint_as_float(a.w);
+      v[p][4] = __uint_as_float(b.x); v[p][5] = __uint_as_float(b.y); v[p][6] = __uint_as_float(b.z); v[p][7] = __uint_as_float(b.w);
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[p][j] = j < left ? src[j] : 0.0f;
@@ -196,7 +198,6 @@ struct QuantArgs {
   int64_t rows, cols, ldx;
   uint8_t *q, *s, *qt, *st;   // q/s or qt/st may be null
   int64_t ldq, ldqt;
-  int vec;                    // rows of x can be read 8 entries at a time
 };
 
 // One workgroup per 128 x 128 tile, read once: each thread holds an 8 x 8 block
@@ -217,7 +218,7 @@ __global__ __launch_bounds__(256) void fp8_quantize_kernel(QuantArgs g) {
   C_ x;
 #pragma unroll
   for (int p = 0; p < 8; ++p)
-    x.load(p, static_cast<const T*>(g.x) + (r0 + p) * g.ldx + c0, r0 + p < g.rows ? g.cols - c0 : 0, g.vec);
+    x.load(p, static_cast<const T*>(g.x) + (r0 + p) * g.ldx + c0, r0 + p < g.rows ? g.cols - c0 : 0);
   const bool rows_out = g.q != nullptr, cols_out = g.qt != nullptr;
   uint32_t rm[8], cm[NC], all = 0;
   auto maxima = [&](auto finite) __attribute__((always_inline)) {
@@ -307,7 +308,6 @@ struct Fp8GemmArgs {
   int64_t m, n, K, lda, ldb, ldc;
   int64_t ra4, rb4;         // rows of the scale arrays
   float alpha, beta;
-  int vec;                  // rows of C can be written 4 entries at a time
   int splits;               // parts of a split contraction (tile kernels): > 1 writes fp32 partial products
   float* partials;          // [splits][m][ldp]
   int64_t ldp;
@@ -317,11 +317,11 @@ struct Fp8GemmArgs {
 template <typename TC>
 __device__ __forceinline__ void store4(const Fp8GemmArgs& g, int64_t row, int64_t col, const float acc[4]) {
   TC* dst = static_cast<TC*>(g.C) + row * g.ldc + col;
-  if (g.vec && col + 4 <= g.n) {
+  if (col + 4 <= g.n) {
     float o[4];
     if constexpr (sizeof(TC) == 2) {
       if (g.beta != 0.0f) {
-        const uint2 z = *reinterpret_cast<const uint2*>(dst);
+        const uint2 z = load8(dst);
         o[0] = fmaf(g.beta, __uint_as_float(z.x << 16), g.alpha * acc[0]);
         o[1] = fmaf(g.beta, __uint_as_float(z.x & 0xffff0000u), g.alpha * acc[1]);
         o[2] = fmaf(g.beta, __uint_as_float(z.y << 16), g.alpha * acc[2]);
@@ -330,21 +330,20 @@ __device__ __forceinline__ void store4(const Fp8GemmArgs& g, int64_t row, int64_
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[i] = g.alpha * acc[i];
       }
-      *reinterpret_cast<uint2*>(dst) =
-          make_uint2(uint32_t(f32_to_bf16(o[0])) | (uint32_t(f32_to_bf16(o[1])) << 16),
-                     uint32_t(f32_to_bf16(o[2])) | (uint32_t(f32_to_bf16(o[3])) << 16));
+      store8(dst, make_uint2(uint32_t(f32_to_bf16(o[0])) | (uint32_t(f32_to_bf16(o[1])) << 16),
+                             uint32_t(f32_to_bf16(o[2])) | (uint32_t(f32_to_bf16(o[3])) << 16)));
     } else {
       if (g.beta != 0.0f) {
-        const float4 z = *reinterpret_cast<const float4*>(dst);
-        o[0] = fmaf(g.beta, z.x, g.alpha * acc[0]);
-        o[1] = fmaf(g.beta, z.y, g.alpha * acc[1]);
-        o[2] = fmaf(g.beta, z.z, g.alpha * acc[2]);
-        o[3] = fmaf(g.beta, z.w, g.alpha * acc[3]);
+        const uint4 z = load16(dst);
+        o[0] = fmaf(g.beta, __uint_as_float(z.x), g.alpha * acc[0]);
+        o[1] = fmaf(g.beta, __uint_as_float(z.y), g.alpha * acc[1]);
+        o[2] = fmaf(g.beta, __uint_as_float(z.z), g.alpha * acc[2]);
+        o[3] = fmaf(g.beta, __uint_as_float(z.w), g.alpha * acc[3]);
       } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[i] = g.alpha * acc[i];
       }
-      *reinterpret_cast<float4*>(dst) = make_float4(o[0], o[1], o[2], o[3]);
+      store16(dst, make_uint4(__float_as_uint(o[0]), __float_as_uint(o[1]), __float_as_uint(o[2]), __float_as_uint(o[3])));
     }
   } else {
 #pragma unroll
@@ -551,7 +550,6 @@ struct TileOut {
   TS* C;
   int64_t ld, width;
   float alpha, beta;
-  bool vec;   // rows can be written 16 bytes at a time
 };
 
 // One BM x BN tile at rows m0, columns n0 over 64-value steps [kt0, kt0 + nk) (both even)
@@ -761,13 +759,13 @@ __device__ __forceinline__ void fp8_tile_unit(const Fp8GemmArgs& g, int64_t m0, 
         *reinterpret_cast<f32x4_t*>(slab + fr * LDW + 32 * j + 8 * q + 4 * h) =
             f32x4_t{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
     const int64_t row0 = m0 + wm0 + 32 * i + pr;
-    if (out.vec && col + E <= out.width) {
+    if (col + E <= out.width) {
       uint4 was[PASSES];
       if (out.beta != 0.0f) {
 #pragma unroll
         for (int p = 0; p < PASSES; ++p) {
           was[p] = make_uint4(0, 0, 0, 0);
-          if (row0 + RPP * p < g.m) was[p] = *reinterpret_cast<const uint4*>(out.C + (row0 + RPP * p) * out.ld + col);
+          if (row0 + RPP * p < g.m) was[p] = load16(out.C + (row0 + RPP * p) * out.ld + col);
         }
       }
 #pragma unroll
@@ -798,9 +796,9 @@ __device__ __forceinline__ void fp8_tile_unit(const Fp8GemmArgs& g, int64_t m0, 
               const f32x2_t x = {o[2 * k], o[2 * k + 1]};
               w[k] = __builtin_bit_cast(uint32_t, __builtin_convertvector(x, bf16x2_t));
             }
-            *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+            store16(dst, make_uint4(w[0], w[1], w[2], w[3]));
           } else {
-            *reinterpret_cast<float4*>(dst) = make_float4(o[0], o[1], o[2], o[3]);
+            store16(dst, make_uint4(__float_as_uint(o[0]), __float_as_uint(o[1]), __float_as_uint(o[2]), __float_as_uint(o[3])));
           }
         }
       }
@@ -828,7 +826,7 @@ __device__ __forceinline__ void tile_at(int64_t t, int64_t TM, int64_t TN, int64
 
 template <typename TC>
 __device__ __forceinline__ TileOut<TC> whole_out(const Fp8GemmArgs& g) {
-  return TileOut<TC>{static_cast<TC*>(g.C), g.ldc, g.n, g.alpha, g.beta, g.ldc % (16 / int64_t(sizeof(TC))) == 0};
+  return TileOut<TC>{static_cast<TC*>(g.C), g.ldc, g.n, g.alpha, g.beta};
 }
 
 // All tiles of one size; with SPLIT each is g.splits units along the contraction, whose
@@ -845,7 +843,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void fp8_gemm_tile_kern
     tile_at(u % tiles, TM, TN, tm, tn);
     const int g0 = __builtin_amdgcn_readfirstlane(int(part * groups / g.splits));
     const int g1 = __builtin_amdgcn_readfirstlane(int((part + 1) * groups / g.splits));
-    const TileOut<float> out{g.partials + part * g.m * g.ldp, g.ldp, g.ldp, 1.0f, 0.0f, true};
+    const TileOut<float> out{g.partials + part * g.m * g.ldp, g.ldp, g.ldp, 1.0f, 0.0f};
     fp8_tile_unit<FA, EXACT, float, BM, BN, WM, WN, S>(g, tm * BM, tn * BN, 2 * g0, 2 * (g1 - g0), out, lds);
   } else {
     tile_at(u, TM, TN, tm, tn);
@@ -995,7 +993,6 @@ int fp8_quantize(const void* x, int x_dtype, int64_t rows, int64_t cols, int64_t
   g.q = static_cast<uint8_t*>(q); g.s = static_cast<uint8_t*>(s);
   g.qt = static_cast<uint8_t*>(qt); g.st = static_cast<uint8_t*>(st);
   g.ldq = ldq; g.ldqt = ldqt;
-  g.vec = ldx % 8 == 0;
   const dim3 grid(ceil_div(cols, 128), ceil_div(rows, 128));
   hipStream_t hs = static_cast<hipStream_t>(stream);
   auto go = [&](auto t_c, auto f_c) {
@@ -1038,7 +1035,6 @@ int fp8_gemm(const void* A, int a_fmt, int64_t lda, const void* sa, const void* 
   g.C = C; g.m = m; g.n = n; g.K = K; g.lda = lda; g.ldb = ldb; g.ldc = ldc;
   g.ra4 = scale_rows(m); g.rb4 = scale_rows(n);
   g.alpha = alpha; g.beta = beta;
-  g.vec = ldc % 4 == 0;
   const ProductPlan plan = plan_product(m, n, K);
   g.splits = plan.splits;
   g.partials = static_cast<float*>(workspace);
