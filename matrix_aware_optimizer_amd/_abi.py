@@ -173,6 +173,17 @@ def _workspace(nbytes: int, like: torch.Tensor, workspace: Optional[torch.Tensor
     return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=like.device)
 
 
+def _workspace_on(nbytes: int, like: torch.Tensor, workspace: Optional[torch.Tensor], stream) -> torch.Tensor:
+    """As _workspace, for a call that goes to ``stream``: memory of that stream's own pool, so that it is free
+    when the call begins there and is not given to another stream's work while the call runs."""
+    if workspace is not None or stream is None:
+        return _workspace(nbytes, like, workspace)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=like.device)
+    with torch.cuda.stream(stream):
+        return _workspace(nbytes, like, None)
+
+
 # ---------------------------------------------------------------------------
 # a1
 # ---------------------------------------------------------------------------
@@ -677,7 +688,7 @@ def fp8_gemm(A: torch.Tensor, sa: torch.Tensor, B: torch.Tensor, sb: torch.Tenso
     need = fp8_gemm_workspace_bytes(m, n, K)
     ws, nbytes = None, 0
     if need > 0:
-        workspace = _workspace(need, C, workspace)
+        workspace = _workspace_on(need, C, workspace, stream)
         ws, nbytes = _dev(workspace, "workspace"), workspace.numel() * workspace.element_size()
     status = lib().fp8_gemm(ap, fa, lda, sap, bp, fb, ldb, sbp, cp, dtype_code(C), ldc if ldc > n else n, m, n, K,
                             alpha, beta, ws, nbytes, _stream(stream))
@@ -758,6 +769,7 @@ def ns_blocks(problems, a: float, b: float, c: float, steps: int, workspace: Opt
               stream=None) -> None:
     """Newton-Schulz directions of every block of every (M, U) problem, each block by itself."""
     if len(problems) > 0:
+        workspace = _workspace_on(ns_blocks_workspace_bytes(problems), problems[0][0], workspace, stream)
         PreparedNSBlocks(problems, a, b, c, steps, workspace=workspace)(stream)
 
 
@@ -765,4 +777,5 @@ def ns_blocks_update(problems, a: float, b: float, c: float, steps: int, eta: fl
                      scale: float = 1.0, workspace: Optional[torch.Tensor] = None, stream=None) -> None:
     """``W <- (1 - eta decay) W - eta scale U`` for every block of every (M, W) problem, U as in ns_blocks."""
     if len(problems) > 0:
+        workspace = _workspace_on(ns_blocks_workspace_bytes(problems), problems[0][0], workspace, stream)
         PreparedNSBlocks(problems, a, b, c, steps, eta, decay, scale, workspace)(stream)

@@ -273,3 +273,23 @@ def test_agrees_with_ns_orthogonalize():
     mao.ns_blocks([(Mv, U)], *QUINTIC, 5)
     mao.ns_orthogonalize([(Mv[0].contiguous(), V, None)], *QUINTIC, 5)
     assert torch.linalg.vector_norm(U[0] - V) <= 2e-2 * torch.linalg.vector_norm(U)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("tall", [False, True])
+def test_offsets_past_32_bits(tall):
+    """Blocks more than 2^31 entries apart, and rows whose pitch takes them there."""
+    rows, cols = (300, 64) if tall else (64, 300)
+    far = torch.empty(2 ** 31 + 2 ** 20, dtype=torch.bfloat16, device="cuda")
+    small = torch.empty(2, rows, cols, device="cuda")
+    views = [far.as_strided((2, rows, cols), (2 ** 31 + 8, cols, 1)),
+             far.as_strided((1, rows, cols), (1, (2 ** 31 + 2 ** 20 - cols) // (rows - 1), 1))]
+    for k, view in enumerate(views):
+        M = (0.02 * torch.randn(view.shape, generator=torch.Generator().manual_seed(k))).to(torch.bfloat16)
+        view.copy_(M)
+        mao.ns_blocks([(view, small[:view.shape[0]])], *QUINTIC, 5)
+        check(M, None, small[:view.shape[0]])
+        view.copy_(M)
+        W = view.clone()
+        mao.ns_blocks_update([(M.cuda(), view)], *QUINTIC, 5, eta=0.1, decay=0.5, scale=2.0)
+        check(M, W.cpu(), view, update=(0.1, 0.5, 2.0))

@@ -392,3 +392,74 @@ def test_gemm_on_another_stream_and_in_a_graph(m):
         g.replay()
         torch.cuda.synchronize()
         np.testing.assert_array_equal(C.double().cpu().numpy(), x.double().cpu().numpy() @ b.T)
+
+
+@pytest.mark.gpu
+def test_offsets_past_32_bits():
+    """More than 2^31 entries: the last rows of a long matrix, quantised both ways and multiplied, against the reference."""
+    rows, cols = 131072 + 130, 16384
+    x = torch.zeros((rows, cols), dtype=torch.bfloat16, device="cuda")
+    tail = spread(200, cols, 71, "bf16")
+    x[-200:] = tail.cuda()
+    q, s = mao.fp8_buffers(rows, cols)
+    qt, st = mao.fp8_buffers(cols, rows)
+    mao.fp8_quantize(x, q, s, qt, st)
+    ref, ex = F.quantize(tail.double().numpy(), "e4m3")
+    np.testing.assert_array_equal(F.decode(q[-200:].view(torch.uint8).cpu().numpy(), "e4m3"), ref)
+    np.testing.assert_array_equal(s[:, rows - 200:rows].cpu().numpy(), F.pack_scales(ex)[:, :200])
+    # a column group of the transpose starts at a multiple of 128 rows: take the rows of its last two groups
+    first = (rows // 128 - 1) * 128
+    part = x[first:].double().cpu().numpy()[:, :300].T
+    ref, ex = F.quantize(part, "e4m3")
+    np.testing.assert_array_equal(F.decode(qt[:300, first:first + ref.shape[1]].view(torch.uint8).cpu().numpy(), "e4m3"), ref)
+    del x, qt, st
+    w = ints_operand(48, cols)
+    C = torch.empty((rows, 48), device="cuda")
+    mao.fp8_gemm(q, s, w[0], w[1], C)
+    a = F.values(q[-200:].view(torch.uint8).cpu().numpy(), F.pack_scales(F.quantize(tail.double().numpy(), "e4m3")[1]), "e4m3")
+    want = a @ w[2].T
+    mag = np.abs(a) @ np.abs(w[2]).T
+    assert (np.abs(C[-200:].double().cpu().numpy() - want) <= (cols + 4) * 2.0 ** -23 * mag + 2.0 ** -24 * np.abs(want)).all()
+    assert (C[:rows - 200] == 0).all()
+
+
+def ints_operand(rows, cols):
+    return operand(rows, cols, "e4m3", 72, small_ints=True)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+def test_output_offsets_past_32_bits(out):
+    """A C of more than 2^31 entries: ones and minus ones, so every entry is exact."""
+    m, n, K = 262144 + 70, 8200, 128
+    rng = np.random.default_rng(73)
+    a, b = (rng.integers(-1, 2, (r, K)).astype(np.float32) for r in (256, n))
+    A = torch.zeros((m, K), device="cuda")
+    A[-256:] = torch.from_numpy(a).cuda()
+    A, B = A.to(torch.float8_e4m3fn), torch.from_numpy(b).cuda().to(torch.float8_e4m3fn)
+    sa, sb = (torch.full(mao.fp8_scale_shape(r, K), 127, dtype=torch.uint8, device="cuda") for r in (m, n))
+    C = torch.full((m, n), 5.0, dtype=torch.float32 if out == "f32" else torch.bfloat16, device="cuda")
+    mao.fp8_gemm(A, sa, B, sb, C)
+    np.testing.assert_array_equal(C[-256:].float().cpu().numpy(), a @ b.T)
+    assert not C[:-256].any()
+
+
+@pytest.mark.gpu
+def test_temporary_workspace_belongs_to_the_stream_of_the_call():
+    """A split product on a side stream with a workspace of its own, while the current stream allocates and fills."""
+    m, n, K = 100, 512, 14336
+    assert mao.fp8_gemm_workspace_bytes(m, n, K) > 0
+    A, sa, a = operand(m, K, "e4m3", 81, small_ints=True)
+    B, sb, b = operand(n, K, "e4m3", 82, small_ints=True)
+    want = torch.from_numpy((a @ b.T).astype(np.float32)).cuda()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    words = mao.fp8_gemm_workspace_bytes(m, n, K) // 4
+    for handle in (side, side.cuda_stream):
+        outs = [torch.zeros((m, n), device="cuda") for _ in range(10)]
+        side.wait_stream(torch.cuda.current_stream())
+        for C in outs:
+            mao.fp8_gemm(A, sa, B, sb, C, stream=handle)
+            torch.full((words,), float("nan"), device="cuda")
+        torch.cuda.synchronize()
+        assert all(torch.equal(C, want) for C in outs)
