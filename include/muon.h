@@ -494,12 +494,13 @@ int dion_step(const muon_dion_problem* probs, int count, int rank, float mu, flo
  *   q  codes, one byte per entry, row-major with a row pitch ldq (a multiple
  *      of 16, at least cols rounded up to MUON_FP8_GROUP); OCP e4m3 or e5m2.
  *      Columns from cols up to the next multiple of 128 hold zeros.
- *   s  scale bytes (E8M0: byte b stands for 2^(b - 127); 255 is NaN), one per
+ *   s  scale bytes (E8M0: byte b, 1 .. 254, stands for 2^(b - 127)), one per
  *      row and group of 128 columns.  Byte (row, group g) is at
  *          s[((g / 4) * R4 + row) * 4 + g % 4],  R4 = rows rounded up to 4,
  *      fp8_scale_bytes(rows, cols) bytes in all.
- * Entry (i, j) has the value q[i][j] * 2^(s(i, j / 128) - 127).  A block of
- * 128 x 128 under one scale is 128 rows with equal bytes.
+ * Entry (i, j) has the value q[i][j] * 2^(s(i, j / 128) - 127), which must
+ * lie within fp32's range.  A block of 128 x 128 under one scale is 128 rows
+ * with equal bytes.
  *
  * fp8_quantize  x [rows][cols] (row pitch ldx entries, F32 or BF16) -> (q, s)
  *               and/or (qt, st), the same matrix transposed: qt [cols][ldqt]

@@ -22,10 +22,10 @@
 // products of parts that reach 2^-24, added in fp32: six matrix instructions where
 // fp32 ones would take the time of sixteen.  (Two fp16 parts, three products, were half
 // as exact as fp32: square blocks with small singular values showed it.)  An fp32 M is
-// split in the same way, a bf16 M is taken as it is.  T enters
-// the last product in two bf16 parts (2^-17 of U, under half a step of a bf16 output)
-// or three (fp32 outputs), M there in as many at most; products of parts beyond the
-// last one kept are left out.
+// split in the same way, a bf16 M is taken as it is.  T enters the last product in two
+// bf16 parts (2^-17 of U, far under half a step of a bf16 output) or three (fp32
+// outputs), M there in as many at most; products of parts beyond the last one kept are
+// left out.
 #include <algorithm>
 
 #include "common.h"
@@ -362,7 +362,6 @@ template <int NY, int NS>
 __device__ __forceinline__ void sym_product(const char* buf, int lane, const SymOperand<NY> (&o)[NS],
                                             f32x4_t (&out)[NS][NY]) {
   constexpr int NT = NY / 2, PIECES = NY * NT, DEPTH = PIECES < 4 ? 1 : 3;
-  constexpr int CHAINS = 2;   // sums per strip: two independent ones follow each other either way
   const char* row = buf + (lane & 15) * SymLds<NY>::PITCH + 16 * (lane >> 4);
   bf16x8_t f[DEPTH + 1][kParts];
   auto read = [&](int k) __attribute__((always_inline)) {
@@ -375,11 +374,9 @@ __device__ __forceinline__ void sym_product(const char* buf, int lane, const Sym
   for (int k = 0; k < DEPTH; ++k) read(k);
 #pragma unroll
   for (int y = 0; y < NY; ++y) {
-    f32x4_t acc[CHAINS][NS];
+    f32x4_t acc[2][NS];   // two sums per strip, neither waiting for the other
 #pragma unroll
-    for (int h = 0; h < CHAINS; ++h)
-#pragma unroll
-      for (int i = 0; i < NS; ++i) acc[h][i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int i = 0; i < NS; ++i) acc[0][i] = acc[1][i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       const int k = y * NT + t;
@@ -391,16 +388,13 @@ __device__ __forceinline__ void sym_product(const char* buf, int lane, const Sym
         for (int r = 0; p + r < kParts; ++r)
 #pragma unroll
           for (int i = 0; i < NS; ++i) {
-            f32x4_t& to = acc[(p + r) == 2 ? CHAINS - 1 : 0][i];
+            f32x4_t& to = acc[(p + r) == 2 ? 1 : 0][i];
             to = __builtin_amdgcn_mfma_f32_16x16x32_bf16(s[p], o[i].p[r][t], to, 0, 0, 0);
           }
       __builtin_amdgcn_sched_barrier(0);
     }
 #pragma unroll
-    for (int i = 0; i < NS; ++i) {
-      if constexpr (CHAINS == 2) out[i][y] = acc[0][i] + acc[1][i];
-      else out[i][y] = acc[0][i];
-    }
+    for (int i = 0; i < NS; ++i) out[i][y] = acc[0][i] + acc[1][i];
   }
 }
 
