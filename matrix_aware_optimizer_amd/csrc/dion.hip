@@ -247,9 +247,9 @@ constexpr int kZeroPageFloats = 4096;          // the workspace's page of zeros:
 #pragma clang diagnostic ignored "-Winline-asm"
 // 16 bytes per lane from global memory to LDS bytes [lds_addr + 16 lane).  M0
 // is set here and used by nothing else in the kernel (no other LDS-DMA, no
-// relative register indexing, no messages).
+// relative register indexing, no messages); the load needs one wait state after it.
 __device__ __forceinline__ void dion_dma16(const void* g, uint32_t lds_addr) {
-  asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(g),
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(g),
                "s"(__builtin_amdgcn_readfirstlane(lds_addr))
                : "memory", "m0");
 }

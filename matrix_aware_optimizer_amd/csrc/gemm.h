@@ -474,10 +474,12 @@ __device__ __forceinline__ void wait_vm_barrier() {
 // M0 is reserved by the compiler; these kernels contain no other M0 user (no
 // LDS-DMA builtins, no relative register indexing, no messages -- checked in
 // the generated assembly), so setting it here cannot disturb compiled code.
+// The s_nop is the wait state that a load to LDS needs after a scalar write of
+// M0; inside asm the compiler does not put it there.
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void dma16(const void* g, uint32_t lds_addr) {
-  asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(g),
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(g),
                "s"(__builtin_amdgcn_readfirstlane(lds_addr))
                : "memory", "m0");
 }
