@@ -570,10 +570,10 @@ int fp8_gemm(const void* A, int a_fmt, int64_t lda, const void* sa, const void* 
  *   ns_blocks         out = U (F32 or BF16)
  *   ns_blocks_update  out <- (1 - eta decay) out - eta scale U, the decoupled
  *                     weight decay and the step in one pass (out = W)
- * M is F32 or BF16 and read only.  The iterations run on T with U = T M, in
- * fp32 (polynomials of A commute, so the long side is read only twice); U is
- * rounded once, to the type of out.  Sums of squares must lie within fp32's
- * normal range.  NaN or infinity in a block make that block's U NaN.
+ * M is F32 or BF16 and read only.  The iterations run on T with U = T M
+ * (polynomials of A commute, so the long side is read only twice).  A holds
+ * squares of singular values, so A and T are computed in fp64.  |M|_F must lie
+ * within 2^-100 .. 2^100.  NaN or infinity in a block make that block's U NaN.
  *
  *   workspace  ns_blocks_workspace_bytes(probs, nprobs) bytes, 16-byte
  *              aligned; contents on entry do not matter.  Calls that share one

@@ -6,26 +6,23 @@
 // every later A; polynomials of one symmetric matrix are symmetric and commute:
 //     P = a I + b A + c A A,   T' = P T,   A' = X' X'^T = P (P A).
 // The long side is therefore touched twice only: once for A0, once for U = T X0.
-// All iterations between work on s x s matrices, one workgroup per block.  A is made
-// symmetric again in every iteration: what rounding leaves in it that is not symmetric
-// would grow sevenfold per iteration where A has converged, while symmetric errors
-// shrink there.
+// All iterations between work on s x s matrices, one workgroup per block.
 // X0 = M / |M|_F, and |M|_F^2 is the trace of M M^T.  Three launches serve every block
 // of a call:
-//   gram   partial M M^T over chunks of the long side (lower 32 x 32 tiles only)
+//   gram   partial M M^T over chunks of the long side (lower 16 x 16 tiles only)
 //   poly   sums the chunks in order, scales by the trace, iterates, writes T / |M|_F
 //   apply  U = T M, or W <- (1 - eta decay) W - eta scale U
 //
-// Rounding.  A relative error d of A0 grows by at most a^2 per iteration where A is
-// small, so A and T are held in fp32 and multiplied as such: every s x s product takes
-// its operands as sums of three bf16 parts (24 bits and the range of fp32), the six
-// products of parts that reach 2^-24, added in fp32: six matrix instructions where
-// fp32 ones would take the time of sixteen.  (Two fp16 parts, three products, were half
-// as exact as fp32: square blocks with small singular values showed it.)  An fp32 M is
-// split in the same way, a bf16 M is taken as it is.  T enters the last product in two
-// bf16 parts (2^-17 of U, far under half a step of a bf16 output) or three (fp32
-// outputs), M there in as many at most; products of parts beyond the last one kept are
-// left out.
+// Rounding.  A holds the squares of the singular values, so what rounding leaves in it
+// in a direction that M lacks (or nearly lacks) grows by up to a^2 per iteration, where an
+// iteration on X would see it grow by a; and a negative leftover grows without end.  In
+// fp32 that is up to 2^-24 11.9^5 = 1% of U after five quintic steps on a block of low
+// rank, and nothing is left of U after ten.  Gram and iterations are therefore computed in fp64, on the fp64
+// matrix instructions: the same leftover is 2^-53 11.9^5.
+//
+// T enters the last product in two bf16 parts (2^-17 of U, far under half a step of a
+// bf16 output) or three (fp32 outputs), M there in as many at most; products of parts
+// beyond the last one kept are left out.
 #include <algorithm>
 
 #include "common.h"
@@ -62,13 +59,23 @@ struct Epilogue {
   int update;
 };
 
-__host__ __device__ constexpr int tiles_of(int nt) { return nt * (nt + 1) / 2; }
+__host__ __device__ constexpr int tiles_of(int ny) { return ny * (ny + 1) / 2; }
 
 // lower tile t -> (row, column)
 __device__ __forceinline__ void tile_rc(int t, int& i, int& j) {
-  i = t >= 6 ? 3 : t >= 3 ? 2 : t >= 1 ? 1 : 0;
-  j = t - i * (i + 1) / 2;
+  i = 0;
+  while (tiles_of(i + 1) <= t) ++i;
+  j = t - tiles_of(i);
 }
+
+// v_mfma_f64_16x16x4: lane 16 g + i gives row i of the first operand and column i of the
+// second, both for k = g, and holds rows 4 v + g of column i of the result.
+typedef double f64x4_t __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ void mma64(double a, double b, f64x4_t& acc) {
+  acc = __builtin_amdgcn_mfma_f64_16x16x4f64(a, b, acc, 0, 0, 0);
+}
+
+typedef double f64x2_t __attribute__((ext_vector_type(2)));
 
 // unit `u` of a launch -> its run and the index within it (uniform)
 __device__ __forceinline__ const Run& find_run(const Runs& runs, int& u, int units_per_count) {
@@ -81,6 +88,8 @@ __device__ __forceinline__ const Run& find_run(const Runs& runs, int& u, int uni
   }
   return runs.r[k];
 }
+
+constexpr int kParts = 3;   // bf16 parts of T
 
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 typedef float f32x2_t __attribute__((ext_vector_type(2)));
@@ -95,65 +104,85 @@ __device__ __forceinline__ uint32_t leading_part(f32x2_t& x) {
 
 // A region of a row-major matrix on its way from memory to LDS: rows [r0, r0 + NR),
 // columns [c0, c0 + NC), entries outside rows x cols as zeros.  fetch() leaves it in
-// registers (LD 16-byte pieces per thread, 256 threads), so that it is under way while
-// the region before is multiplied; store() writes it as bf16 planes: a bf16 entry as it
-// is, an fp32 entry as its NP leading bf16 parts.
-template <typename T, int LD>
+// registers (LD 16-byte pieces of each of 256 threads), so that it is under way while the
+// region before is multiplied.  Its loads have no branches of their own, in which they
+// would have to be waited for: rows and columns past the end are read at the last place
+// that exists, and put right by piece(), where the values are used.  Rows shorter than a
+// piece are read there altogether.
+// With ANEW the addresses are formed at every fetch, instead of a row's being kept in
+// registers for each piece.
+template <typename T, int LD, bool ANEW = false>
 struct Region {
-  static constexpr int E = 16 / sizeof(T);
-  uint4 w[LD];
+  static constexpr int E = 16 / int(sizeof(T));
+  u32x4_t w[LD];
+  const T* src;
+  int64_t ld;
+  int rows, cols, r0, c0, per, n;
 
-  __device__ __forceinline__ void fetch(const T* src, int64_t ld, int rows, int cols, int r0, int c0, int NR, int NC) {
-    const int per = NC / E, n = NR * per;
+  __device__ __forceinline__ void fetch(const T* from, int64_t pitch, int nrows, int ncols, int row0, int col0, int NR, int NC) {
+    src = from; ld = pitch; rows = nrows; cols = ncols; r0 = row0; c0 = col0;
+    per = NC / E; n = NR * per;
+    if (cols >= E) {
+      int first = threadIdx.x;
+      if (ANEW) asm volatile("" : "+v"(first));
 #pragma unroll
-    for (int q = 0; q < LD; ++q) {
-      const int t = threadIdx.x + 256 * q;
-      w[q] = make_uint4(0, 0, 0, 0);
-      if (t < n) {
-        const int r = t / per, c = (t % per) * E;
-        const T* p = src + int64_t(r0 + r) * ld + c0 + c;
-        if (r0 + r < rows) {
-          if (c0 + c + E <= cols) {
-            w[q] = load16(p);
-          } else {
-            uint32_t e[E];
-#pragma unroll
-            for (int k = 0; k < E; ++k) {
-              e[k] = 0;
-              if (c0 + c + k < cols) {
-                if constexpr (sizeof(T) == 2) e[k] = p[k];
-                else e[k] = __float_as_uint(p[k]);
-              }
-            }
-            if constexpr (sizeof(T) == 2)
-              w[q] = make_uint4(e[0] | (e[1] << 16), e[2] | (e[3] << 16), e[4] | (e[5] << 16), e[6] | (e[7] << 16));
-            else
-              w[q] = make_uint4(e[0], e[1], e[2], e[3]);
-          }
-        }
+      for (int q = 0; q < LD; ++q) {
+        const int t = min(first + 256 * q, n - 1);
+        const uint4 v = load16(src + int64_t(min(r0 + t / per, rows - 1)) * ld + min(c0 + t % per * E, cols - E));
+        w[q] = u32x4_t{v.x, v.y, v.z, v.w};
       }
     }
   }
 
+  // what fetch() got for piece q: row r, columns c .. c + E - 1 of the matrix
+  __device__ __forceinline__ u32x4_t piece(int q, int r, int c) const {
+    u32x4_t v = {0, 0, 0, 0};
+    if (r < rows && c < cols) {
+      if (c + E <= cols) {
+        v = w[q];
+      } else if (cols >= E) {   // the last E columns, of which the first lie before c
+        uint64_t lo = w[q][0] | uint64_t(w[q][1]) << 32, hi = w[q][2] | uint64_t(w[q][3]) << 32;
+        const int bits = (c + E - cols) * int(sizeof(T)) * 8;
+        if (bits >= 64) {
+          lo = hi >> (bits - 64);
+          hi = 0;
+        } else {
+          lo = lo >> bits | hi << (64 - bits);
+          hi >>= bits;
+        }
+        v = u32x4_t{uint32_t(lo), uint32_t(lo >> 32), uint32_t(hi), uint32_t(hi >> 32)};
+      } else {
+        const T* p = src + int64_t(r) * ld + c;
+#pragma unroll
+        for (int k = 0; k < E; ++k)
+          if (c + k < cols) {
+            if constexpr (sizeof(T) == 2) v[k >> 1] |= uint32_t(p[k]) << (16 * (k & 1));
+            else v[k] = __float_as_uint(p[k]);
+          }
+      }
+    }
+    return v;
+  }
+
   // tile holds U for the region: dst = U, or c1 (what fetch() got) - c2 U
-  __device__ __forceinline__ void finish(const float* tile, int tile_ld, T* dst, int64_t ld, int rows, int cols, int r0,
-                                         int c0, int NR, int NC, const Epilogue& e) const {
-    const int per = NC / E, n = NR * per;
+  __device__ __forceinline__ void finish(const float* tile, int tile_ld, T* dst, int64_t pitch, int nrows, int ncols, int row0,
+                                         int col0, int NR, int NC, const Epilogue& e) const {
+    const int pieces = NC / E;
 #pragma unroll
     for (int q = 0; q < LD; ++q) {
       const int t = threadIdx.x + 256 * q;
-      if (t < n) {
-        const int r = t / per, c = (t % per) * E;
-        if (r0 + r >= rows || c0 + c >= cols) continue;
+      if (t < NR * pieces) {
+        const int lr = t / pieces, lc = t % pieces * E, r = row0 + lr, c = col0 + lc;
+        if (r >= nrows || c >= ncols) continue;
         float v[E];
 #pragma unroll
         for (int k = 0; k < E; k += 4) {
-          const f32x4_t x = *reinterpret_cast<const f32x4_t*>(tile + r * tile_ld + c + k);
+          const f32x4_t x = *reinterpret_cast<const f32x4_t*>(tile + lr * tile_ld + lc + k);
 #pragma unroll
           for (int m = 0; m < 4; ++m) v[k + m] = x[m];
         }
-        const uint32_t was[4] = {w[q].x, w[q].y, w[q].z, w[q].w};
         if (e.update) {
+          const u32x4_t was = piece(q, r, c);
 #pragma unroll
           for (int k = 0; k < E; ++k) {
             float o;
@@ -162,8 +191,8 @@ struct Region {
             v[k] = fmaf(e.c1, o, -e.c2 * v[k]);
           }
         }
-        T* p = dst + int64_t(r0 + r) * ld + c0 + c;
-        if (c0 + c + E <= cols) {
+        T* p = dst + int64_t(r) * pitch + c;
+        if (c + E <= ncols) {
           uint4 o;
           if constexpr (sizeof(T) == 2) {
             f32x2_t a = {v[0], v[1]}, b = {v[2], v[3]}, g = {v[4], v[5]}, h = {v[6], v[7]};
@@ -178,26 +207,46 @@ struct Region {
         } else {
 #pragma unroll
           for (int k = 0; k < E; ++k)
-            if (c0 + c + k < cols) p[k] = from_f32<T>(v[k]);
+            if (c + k < ncols) p[k] = from_f32<T>(v[k]);
         }
       }
     }
   }
 
-  template <int NP>
-  __device__ __forceinline__ void store(char* lds, int pitch, int plane, int NR, int NC) const {
-    const int per = NC / E, n = NR * per;
+  // to LDS as fp64: converting takes the same units as the matrix instructions (13 cycles
+  // of their 64), so it is done once for each entry
+  __device__ __forceinline__ void store_f64(char* lds, int pitch) const {
 #pragma unroll
     for (int q = 0; q < LD; ++q) {
       const int t = threadIdx.x + 256 * q;
       if (t < n) {
-        const int r = t / per, c = (t % per) * E;
+        const int r = t / per, c = t % per * E;
+        const u32x4_t x = piece(q, r0 + r, c0 + c);
+        f64x2_t* dst = reinterpret_cast<f64x2_t*>(lds + r * pitch + c * 8);
+#pragma unroll
+        for (int k = 0; k < E / 2; ++k) {
+          if constexpr (sizeof(T) == 2) dst[k] = f64x2_t{__uint_as_float(x[k] << 16), __uint_as_float(x[k] & 0xffff0000u)};
+          else dst[k] = f64x2_t{__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])};
+        }
+      }
+    }
+  }
+
+  // to LDS as bf16 planes: a bf16 entry as it is, an fp32 entry as its NP leading bf16 parts
+  template <int NP>
+  __device__ __forceinline__ void store(char* lds, int pitch, int plane) const {
+#pragma unroll
+    for (int q = 0; q < LD; ++q) {
+      const int t = threadIdx.x + 256 * q;
+      if (t < n) {
+        const int r = t / per, c = t % per * E;
+        const u32x4_t x = piece(q, r0 + r, c0 + c);
         char* dst = lds + r * pitch + c * 2;
         if constexpr (sizeof(T) == 2) {
-          *reinterpret_cast<uint4*>(dst) = w[q];
+          *reinterpret_cast<u32x4_t*>(dst) = x;
         } else {
-          f32x2_t lo = {__uint_as_float(w[q].x), __uint_as_float(w[q].y)};
-          f32x2_t hi = {__uint_as_float(w[q].z), __uint_as_float(w[q].w)};
+          f32x2_t lo = {__uint_as_float(x[0]), __uint_as_float(x[1])};
+          f32x2_t hi = {__uint_as_float(x[2]), __uint_as_float(x[3])};
 #pragma unroll
           for (int p = 0; p < NP; ++p) {
             const uint32_t a = leading_part(lo), b = leading_part(hi);
@@ -230,341 +279,332 @@ __device__ __forceinline__ u32x4_t fragment(const char* plane, int pitch, int fi
 }
 
 // ---------------------------------------------------------------------------
-// gram: tile t of M M^T over one chunk, as it lies in the accumulators: [t][16][64].
-// Bound by reading M (and, for an fp32 M, by its six products and its splitting): 144
-// blocks 768 x 64 bf16 8.5 us; 32 blocks 128 x 4096 11 us in bf16 (3.0 TB/s), 26 in fp32
-// (2.6); 50 blocks 80 x 2309 fp32 18 us.
+// gram: lower 16 x 16 tile t of M M^T over one chunk, in fp64, as it lies in the
+// accumulators: [t][4][64].  Bound by the fp64 matrix instructions (64 cycles each; two
+// thirds of them at most while the next slab is converted and laid out): 144 blocks 768 x 64
+// bf16 21 us, 32 blocks 128 x 4096 fp32 53 us, 50 blocks 80 x 2309 fp32 27 us.
 // ---------------------------------------------------------------------------
-template <typename T> constexpr int gram_slab() { return 128 / sizeof(T); }   // k-values staged at a time
+constexpr int gram_slab(bool big) { return big ? 32 : 64; }   // k-values staged at a time
 
 template <typename T, bool TALL, bool BIG>
-__global__ __launch_bounds__(256) void blocks_gram_kernel(Runs runs, char* ws) {
-  constexpr int SLAB = gram_slab<T>(), NP = sizeof(T) == 2 ? 1 : 3, SIDE = BIG ? 128 : 64;
-  constexpr int PITCH = TALL ? tr_pitch(2 * SIDE) : row_pitch(2 * SLAB);   // tall [SLAB][s], wide [s][SLAB]
-  constexpr int PLANE = (TALL ? SLAB : SIDE) * PITCH;
-  constexpr int NA = BIG ? 3 : 1;   // lower tiles of a wave
-  __shared__ __attribute__((aligned(16))) char lds[NP * PLANE];
+__global__ __launch_bounds__(256, 2) void blocks_gram_kernel(Runs runs, char* ws) {
+  constexpr int SLAB = gram_slab(BIG), SIDE = BIG ? 128 : 64;
+  // fp64; tall [SLAB][s]: 16 entries of two rows at once, so that rows start half the banks
+  // apart; wide [s][SLAB]: 16 bytes of 16 rows at once
+  constexpr int PITCH = 8 * (TALL ? SIDE : SLAB) + (TALL ? 128 : 16);
+  constexpr int NA = BIG ? 9 : 3;   // lower tiles of a wave
+  __shared__ __attribute__((aligned(16))) char lds[(TALL ? SLAB : SIDE) * PITCH];
   int u = blockIdx.x;
   const Run& run = find_run(runs, u, 0);
   const int b = u / run.chunks, chunk = u % run.chunks;
-  const int s = run.s, l = run.l, nt = (s + 31) / 32, sp = nt * 32;
+  const int s = run.s, l = run.l, ny = (s + 15) / 16, sp = 16 * ny;
   const T* M = static_cast<const T*>(run.M) + b * run.stride_m;
   const int64_t ld = run.ld_m;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int nlow = tiles_of(nt);
-  const int k0 = chunk * run.chunk, k1 = min(l, k0 + run.chunk);
-  f32x16_t acc[NA];
+  const int i = lane & 15, g = lane >> 4;
+  const int nlow = tiles_of(ny);
+  const int k0 = chunk * run.chunk, k1 = min(l, k0 + run.chunk);   // chunks are whole slabs, but for the last
+  f64x4_t acc[NA];
 #pragma unroll
-  for (int q = 0; q < NA; ++q)
-#pragma unroll
-    for (int v = 0; v < 16; ++v) acc[q][v] = 0.0f;
-  Region<T, BIG ? 4 : 2> reg;
+  for (int q = 0; q < NA; ++q) acc[q] = f64x4_t{0.0, 0.0, 0.0, 0.0};
+  Region<T, SIDE * SLAB * int(sizeof(T)) / 16 / 256> reg;
   auto fetch = [&](int k) __attribute__((always_inline)) {
-    if (TALL) reg.fetch(M, ld, k1, s, k, 0, SLAB, sp);
-    else reg.fetch(M, ld, s, k1, 0, k, sp, SLAB);
+    if (TALL) reg.fetch(M, ld, l, s, k, 0, SLAB, sp);
+    else reg.fetch(M, ld, s, l, 0, k, sp, SLAB);
   };
   fetch(k0);
+  constexpr int STEPS = SLAB / 8;
+  int at[NA][2];                    // where the operands of the wave's tiles begin
+#pragma unroll
+  for (int q = 0; q < NA; ++q) {
+    int ti, tj;
+    tile_rc(min(wave + 4 * q, nlow - 1), ti, tj);
+    at[q][0] = TALL ? g * PITCH + (16 * ti + i) * 8 : (16 * ti + i) * PITCH + 16 * g;
+    at[q][1] = TALL ? g * PITCH + (16 * tj + i) * 8 : (16 * tj + i) * PITCH + 16 * g;
+  }
   for (int k = k0; k < k1; k += SLAB) {
     __syncthreads();
-    if (TALL) reg.template store<NP>(lds, PITCH, PLANE, SLAB, sp);
-    else reg.template store<NP>(lds, PITCH, PLANE, sp, SLAB);
+    reg.store_f64(lds, PITCH);
     __syncthreads();
     if (k + SLAB < k1) fetch(k + SLAB);
+    // Pairs of k-values (any order will do, as long as both operands have the same), each read
+    // while the pair before is multiplied.
+    f64x2_t f[2][2];
+    auto read = [&](int n) __attribute__((always_inline)) {
+      const int q = n / STEPS, h = n % STEPS;
+      if constexpr (TALL) {
+        const char *pa = lds + at[q][0] + 8 * h * PITCH, *pb = lds + at[q][1] + 8 * h * PITCH;
+        f[n & 1][0] = f64x2_t{*reinterpret_cast<const double*>(pa), *reinterpret_cast<const double*>(pa + 4 * PITCH)};
+        f[n & 1][1] = f64x2_t{*reinterpret_cast<const double*>(pb), *reinterpret_cast<const double*>(pb + 4 * PITCH)};
+      } else {
+        f[n & 1][0] = *reinterpret_cast<const f64x2_t*>(lds + at[q][0] + 64 * h);
+        f[n & 1][1] = *reinterpret_cast<const f64x2_t*>(lds + at[q][1] + 64 * h);
+      }
+    };
+    read(0);
 #pragma unroll
     for (int q = 0; q < NA; ++q) {
-      const int t = wave + 4 * q;
-      if (t < nlow) {
-        int ti, tj;
-        tile_rc(t, ti, tj);
+      if (wave + 4 * q < nlow) {
 #pragma unroll
-        for (int ks = 0; ks < SLAB / 16; ++ks) {
-          u32x4_t fa[NP], fb[NP];
-#pragma unroll
-          for (int p = 0; p < NP; ++p) {
-            fa[p] = fragment<TALL>(lds + p * PLANE, PITCH, ti * 32, ks, lane);
-            fb[p] = fragment<TALL>(lds + p * PLANE, PITCH, tj * 32, ks, lane);
-          }
-#pragma unroll
-          for (int p = 0; p < NP; ++p)
-#pragma unroll
-            for (int r = 0; p + r < NP; ++r) gemm::Mfma<bf16_t>::mma(fa[p], fb[r], acc[q]);
+        for (int n = q * STEPS; n < (q + 1) * STEPS; ++n) {
+          if (n + 1 < NA * STEPS) read(n + 1);
+          __builtin_amdgcn_sched_barrier(0);   // the reads stay in front
+          mma64(f[n & 1][0][0], f[n & 1][1][0], acc[q]);
+          mma64(f[n & 1][0][1], f[n & 1][1][1], acc[q]);
+          __builtin_amdgcn_sched_barrier(0);
         }
       }
     }
   }
-  float* dst = reinterpret_cast<float*>(ws + run.partials) + int64_t(u) * nlow * 1024;
+  double* dst = reinterpret_cast<double*>(ws + run.partials) + int64_t(u) * nlow * 256;
 #pragma unroll
   for (int q = 0; q < NA; ++q) {
     const int t = wave + 4 * q;
     if (t < nlow)
 #pragma unroll
-      for (int v = 0; v < 16; ++v) dst[t * 1024 + v * 64 + lane] = acc[q][v];
+      for (int v = 0; v < 4; ++v) dst[t * 256 + v * 64 + lane] = acc[q][v];
   }
 }
 
 // ---------------------------------------------------------------------------
 // poly: one workgroup per block, one wave per strip of 16 columns
 // ---------------------------------------------------------------------------
-// A wave holds its strip of A, T and P as it comes out of v_mfma_f32_16x16x32_bf16:
-// lane (r, g = lane / 16) has rows 16 y + 4 g .. + 3 of column r of the strip, for every
-// y.  All matrices are symmetric, so that is also row r of the strip, and two of these
-// groups of four (y = 2 t, 2 t + 1) are eight of the 32 k-values of one matrix
-// instruction: a strip is its own second operand without leaving the registers, if the
-// first operand takes the k-values in the same order.  Only A (for A A) and P (for
-// P T, P A and P (P A)) are first operands, and go through LDS as rows.  17 products of
-// a block in five steps, one after another on one CU: 21 us at s = 64, 48 at 80 and 96, 95
-// at 128 (five steps, up to 256 blocks); there matrix instructions take 46% of the cycles,
-// splitting operands and moving accumulators most of the others.
-constexpr int kParts = 3;
-
+// Every matrix here is symmetric, so of NY x NY tiles only those at most NY / 2 below the
+// diagonal, counted cyclically, are computed: wave j computes tile rows j .. j + NY / 2 of
+// strip j (at an even NY the last of them only for j < NY / 2), which is the same work for
+// every SIMD and half of the products.  They go to LDS, where the others are read
+// transposed.  Of the tiles on the diagonal only the lower half is kept, for both: what
+// rounding leaves in A that is not symmetric would grow by a^3 per iteration instead of a^2.
+// A wave holds its strip as it comes out of the matrix instruction, tile slot d being tile
+// row (j + d) % NY: element v of lane 16 g + i is row 4 v + g, column i of the tile.  That is
+// also the second operand of four instructions that contract the tile's 16 rows, so a strip
+// is its own second operand without leaving the registers.  First operands are rows of S,
+// by symmetry columns, and come from LDS in the same layout.
+// 17 products of a block in five steps, one after another on one CU: 40 us at s = 64, 74 at
+// 80, 171 at 128 (up to 256 blocks), 77%, 57% and 82% of it matrix instructions; at 80 five
+// strips leave three of four SIMDs half empty.
 template <int NY>
-struct SymOperand {
-  bf16x8_t p[kParts][NY / 2];
-};
+struct SymTiles {
+  static constexpr int H = NY / 2;                 // slots 0 .. H are computed
+  static constexpr int LD = 17, TILE = 16 * LD;    // doubles; rows of 17, so that transposed reads spread over the banks
+  static constexpr int BYTES = tiles_of(NY) * TILE * 8;
+  static_assert(2 * BYTES <= 160 * 1024, "two matrices fit LDS");
+  int j, i, g;                                     // strip of the wave, lane
 
-template <int NY>
-__device__ __forceinline__ void split_strip(const f32x4_t (&v)[NY], SymOperand<NY>& o) {
-#pragma unroll
-  for (int t = 0; t < NY / 2; ++t) {
-    uint32_t w[kParts][4];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      f32x2_t x = {v[2 * t + (q >> 1)][2 * (q & 1)], v[2 * t + (q >> 1)][2 * (q & 1) + 1]};
-#pragma unroll
-      for (int p = 0; p < kParts; ++p) w[p][q] = leading_part(x);
-    }
-#pragma unroll
-    for (int p = 0; p < kParts; ++p)
-      o.p[p][t] = __builtin_bit_cast(bf16x8_t, make_uint4(w[p][0], w[p][1], w[p][2], w[p][3]));
-  }
-}
-
-template <int NY>
-struct SymLds {
-  static constexpr int PITCH = NY * 32 + 16;        // bytes per row: an odd multiple of 16
-  static constexpr int PLANE = NY * 16 * PITCH;
-  static constexpr int BYTES = kParts * PLANE;
-  static constexpr int BUFFERS = 2 * BYTES <= 150 * 1024 ? 2 : 1;   // two take turns, or one serves all
-};
-
-template <int NY>
-__device__ __forceinline__ void put_strip(char* buf, int wave, int lane, const SymOperand<NY>& o) {
-  char* row = buf + (16 * wave + (lane & 15)) * SymLds<NY>::PITCH + 16 * (lane >> 4);
-#pragma unroll
-  for (int p = 0; p < kParts; ++p)
-#pragma unroll
-    for (int t = 0; t < NY / 2; ++t) *reinterpret_cast<bf16x8_t*>(row + 64 * t + p * SymLds<NY>::PLANE) = o.p[p][t];
-}
-
-// out = S o for the wave's strips, S in LDS.  The parts of the pieces of S are read DEPTH
-// pieces (16 x 32) ahead of their products.
-template <int NY, int NS>
-__device__ __forceinline__ void sym_product(const char* buf, int lane, const SymOperand<NY> (&o)[NS],
-                                            f32x4_t (&out)[NS][NY]) {
-  constexpr int NT = NY / 2, PIECES = NY * NT, DEPTH = PIECES < 4 ? 1 : 3;
-  const char* row = buf + (lane & 15) * SymLds<NY>::PITCH + 16 * (lane >> 4);
-  bf16x8_t f[DEPTH + 1][kParts];
-  auto read = [&](int k) __attribute__((always_inline)) {
-#pragma unroll
-    for (int p = 0; p < kParts; ++p)
-      f[k % (DEPTH + 1)][p] = *reinterpret_cast<const bf16x8_t*>(row + (k / NT) * 16 * SymLds<NY>::PITCH + (k % NT) * 64 +
-                                                                 p * SymLds<NY>::PLANE);
+  __device__ __forceinline__ bool own(int d) const { return 2 * d < NY || (2 * d == NY && j < H); }
+  // where the computed tile `delta` rows below the diagonal of strip c lies
+  __device__ __forceinline__ static int at(int delta, int c) { return (delta * NY + c) * TILE; }
+  // What addresses are made of: the strip, and element v = 0 of the lane in a tile as it is
+  // stored and transposed.  Unknown to the compiler anew for each operation, or it keeps the
+  // addresses of all of them in registers at once.
+  struct Origin {
+    int j, direct, across;
   };
+  __device__ __forceinline__ Origin origin() const {
+    Origin o{j, g * LD + i, i * LD + g};
+    asm volatile("" : "+s"(o.j), "+v"(o.direct), "+v"(o.across));
+    return o;
+  }
+  // element v = 0 of this lane in tile (row, col), row = col + delta (mod NY), and the step to
+  // the next v: in the stored tile itself or, transposed, in tile (col, row)
+  __device__ __forceinline__ static int first(const Origin& o, int delta, int row, int col, int& step) {
+    const bool direct = 2 * delta < NY || (2 * delta == NY && col < H);
+    step = direct ? 4 * LD : 4;
+    return direct ? at(delta, col) + o.direct : at(NY - delta, row) + o.across;
+  }
+  __device__ __forceinline__ int wrap(int t) const { return t >= NY ? t - NY : t; }
+
+  __device__ __forceinline__ void put(double* buf, const f64x4_t (&x)[H + 1]) const {
+    const Origin o = origin();
 #pragma unroll
-  for (int k = 0; k < DEPTH; ++k) read(k);
+    for (int v = 0; v < 4; ++v)
+      if (4 * v + g >= i) {
+        buf[at(0, o.j) + o.direct + 4 * v * LD] = x[0][v];
+        buf[at(0, o.j) + o.across + 4 * v] = x[0][v];
+      }
 #pragma unroll
-  for (int y = 0; y < NY; ++y) {
-    f32x4_t acc[2][NS];   // two sums per strip, neither waiting for the other
+    for (int d = 1; d <= H; ++d)
+      if (own(d))
 #pragma unroll
-    for (int i = 0; i < NS; ++i) acc[0][i] = acc[1][i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int v = 0; v < 4; ++v) buf[at(d, o.j) + o.direct + 4 * v * LD] = x[d][v];
+  }
+  // the whole strip: what the wave computed off the diagonal (unless `all` is read), and the
+  // rest from LDS
+  __device__ __forceinline__ void complete(const double* buf, const f64x4_t (&x)[H + 1], f64x4_t (&to)[NY],
+                                           bool all = false) const {
+    const Origin o = origin();
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      const int k = y * NT + t;
-      if (k + DEPTH < PIECES) read(k + DEPTH);
-      const bf16x8_t(&s)[kParts] = f[k % (DEPTH + 1)];
+    for (int d = 0; d < NY; ++d) {
+      if (d > 0 && d <= H && own(d) && !all) {
+        to[d] = x[d <= H ? d : 0];
+      } else {
+        int step;
+        const double* p = buf + first(o, d, wrap(o.j + d), o.j, step);
 #pragma unroll
-      for (int p = 0; p < kParts; ++p)
+        for (int v = 0; v < 4; ++v) to[d][v] = p[v * step];
+      }
+    }
+  }
+  // the computed tiles of S by, S in LDS; the next first operands are read while the
+  // current ones multiply
+  __device__ __forceinline__ void product(const double* buf, const f64x4_t (&by)[NY], f64x4_t (&out)[H + 1]) const {
+    if (own(H)) multiply<H + 1>(buf, by, out);
+    else multiply<H>(buf, by, out);
+  }
+  template <int N>
+  __device__ __forceinline__ void multiply(const double* buf, const f64x4_t (&by)[NY], f64x4_t (&out)[H + 1]) const {
+    const Origin o = origin();
+    double f[2][N];
+    auto read = [&](int k) __attribute__((always_inline)) {
+      const int e = k >> 2, v = k & 3;
 #pragma unroll
-        for (int r = 0; p + r < kParts; ++r)
+      for (int d = 0; d < N; ++d) {
+        // S's tile (row j + d, column j + e), by symmetry (j + e, j + d)
+        int step;
+        const double* p = buf + first(o, (e - d + NY) % NY, wrap(o.j + e), wrap(o.j + d), step);
+        f[k & 1][d] = p[v * step];
+      }
+    };
 #pragma unroll
-          for (int i = 0; i < NS; ++i) {
-            f32x4_t& to = acc[(p + r) == 2 ? 1 : 0][i];
-            to = __builtin_amdgcn_mfma_f32_16x16x32_bf16(s[p], o[i].p[r][t], to, 0, 0, 0);
-          }
+    for (int d = 0; d < N; ++d) out[d] = f64x4_t{0.0, 0.0, 0.0, 0.0};
+    read(0);
+#pragma unroll
+    for (int k = 0; k < 4 * NY; ++k) {
+      if (k + 1 < 4 * NY) read(k + 1);
+      __builtin_amdgcn_sched_barrier(0);   // the reads stay in front
+#pragma unroll
+      for (int d = 0; d < N; ++d)
+        mma64(f[k & 1][d], by[k >> 2][k & 3], out[d]);
       __builtin_amdgcn_sched_barrier(0);
     }
-#pragma unroll
-    for (int i = 0; i < NS; ++i) out[i][y] = acc[0][i] + acc[1][i];
   }
-}
-
-// Strips of a wave.  One gives the most waves; at s > 96 eight waves would each read all
-// of S for every product, as long as their matrix instructions take, so four waves take
-// two strips each.
-template <int NY> constexpr int strips() { return NY == 8 ? 2 : 1; }
+};
 
 template <int NY>
-__global__ __launch_bounds__(64 * NY / strips<NY>()) void blocks_poly_kernel(Runs runs, char* ws, float a, float b, float c,
-                                                                             int steps) {
+__global__ __launch_bounds__(64 * NY, 2) void blocks_poly_kernel(Runs runs, char* ws, double a, double b, double c, int steps) {
   extern __shared__ __attribute__((aligned(16))) char sm[];
-  constexpr int NS = strips<NY>(), W = NY / NS;
-  constexpr bool SHARED = SymLds<NY>::BUFFERS == 1;
-  char* buf = sm;                                        // what is written next
-  char* other = SHARED ? sm : sm + SymLds<NY>::BYTES;
+  using S_ = SymTiles<NY>;
+  constexpr int H = S_::H, LD = S_::LD, TILE = S_::TILE, NLOW = tiles_of(NY);
+  double* const bufA = reinterpret_cast<double*>(sm);
+  double* const bufP = reinterpret_cast<double*>(sm + S_::BYTES);
   int u = blockIdx.x;
   const Run& run = find_run(runs, u, 1);
-  constexpr int nlow = tiles_of(NY / 2), sp = 16 * NY;
-  constexpr int LD = sp + 4;   // floats per row of a whole fp32 matrix in LDS: rows four apart start a quarter of the banks apart
-  static_assert(sp * LD * 4 <= SymLds<NY>::BYTES, "the matrix fits a buffer");
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int r = lane & 15, g = lane >> 4;
-  f32x4_t A[NS][NY], T[NS][NY];
-  double total = 0.0;                                    // |M|_F^2
-  // f(i, y): the wave's strip i (strip NS wave + i of the matrix, column 16 strip + r of this
-  // lane), rows 16 y + 4 g .. + 3
-  auto each = [&](auto&& f) __attribute__((always_inline)) {
-#pragma unroll
-    for (int i = 0; i < NS; ++i)
-#pragma unroll
-      for (int y = 0; y < NY; ++y) f(i, y);
-  };
-  auto column = [&](int i) { return 16 * (NS * wave + i) + r; };
-  // the identity's entries in a tile on the diagonal (y == strip)
-  float unit[4];
-#pragma unroll
-  for (int v = 0; v < 4; ++v) unit[v] = 4 * g + v == r ? 1.0f : 0.0f;
+  const S_ sym{wave, lane & 15, lane >> 4};
+  const int i = sym.i, g = sym.g;
+  f64x4_t A[NY], T[NY], out[H + 1];
+  double root;                                     // 1 / |M|_F
   {
-    // The partial Grams are lower 32 x 32 tiles as they lay in the accumulators: float4 q of
-    // a tile is value v = q / 16 of lanes 4 (q % 16) .., row 8 (v / 4) + 4 (lane / 32) + v % 4,
-    // columns lane % 32 ... All threads add them up, chunk after chunk (four in flight), and
-    // lay the whole matrix out in LDS.
-    constexpr int THREADS = 64 * W, Q = nlow * 256 / THREADS;   // float4 per thread
-    static_assert(nlow * 256 % THREADS == 0, "whole float4 per thread");
+    // The chunks' Grams, added in their order, pairs of columns by all threads (four chunks'
+    // loads in flight).  Tile (ti, tj) is stored as it is or, where it lies more than half way
+    // down, as the transposed tile of strip ti.
+    constexpr int Q = NY + 1, THREADS = 64 * NY;   // pairs of a thread: 128 in each tile
     const int chunks = run.chunks;
-    const f32x4_t* src = reinterpret_cast<const f32x4_t*>(ws + run.partials) + int64_t(u) * chunks * nlow * 256 + threadIdx.x;
-    f32x4_t sum[Q];
+    const f64x2_t* src = reinterpret_cast<const f64x2_t*>(ws + run.partials) + int64_t(u) * chunks * NLOW * 128 + threadIdx.x;
+    f64x2_t sum[Q];
 #pragma unroll
-    for (int q = 0; q < Q; ++q) sum[q] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int q = 0; q < Q; ++q) sum[q] = f64x2_t{0.0, 0.0};
     int k = 0;
-    for (; k + 4 <= chunks; k += 4, src += 4 * nlow * 256) {
-      f32x4_t w[4][Q];
+    for (; k + 4 <= chunks; k += 4, src += 4 * NLOW * 128) {
+      f64x2_t w[4][Q];
 #pragma unroll
       for (int e = 0; e < 4; ++e)
 #pragma unroll
-        for (int q = 0; q < Q; ++q) w[e][q] = src[e * nlow * 256 + q * THREADS];
+        for (int q = 0; q < Q; ++q) w[e][q] = src[e * NLOW * 128 + q * THREADS];
 #pragma unroll
       for (int e = 0; e < 4; ++e)
 #pragma unroll
         for (int q = 0; q < Q; ++q) sum[q] += w[e][q];
     }
-    for (; k < chunks; ++k, src += nlow * 256)
+    for (; k < chunks; ++k, src += NLOW * 128)
 #pragma unroll
       for (int q = 0; q < Q; ++q) sum[q] += src[q * THREADS];
-    float* full = reinterpret_cast<float*>(sm);
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
-      const int at = threadIdx.x + q * THREADS, tile = at >> 8, v = (at & 255) >> 4, l4 = 4 * (at & 15);
+      const int p = threadIdx.x + q * THREADS, row = (p & 127) >> 3, col = 2 * (p & 7);
       int ti, tj;
-      tile_rc(tile, ti, tj);
-      const int row = 32 * ti + 8 * (v >> 2) + 4 * (l4 >> 5) + (v & 3), col = 32 * tj + (l4 & 31);
-      *reinterpret_cast<f32x4_t*>(full + row * LD + col) = sum[q];
-      if (ti != tj)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) full[(col + e) * LD + row] = sum[q][e];
+      tile_rc(__builtin_amdgcn_readfirstlane(p >> 7), ti, tj);
+      const bool direct = 2 * (ti - tj) <= NY;
+      double* at = bufA + (direct ? S_::at(ti - tj, tj) + row * LD + col : S_::at(NY - (ti - tj), ti) + col * LD + row);
+      at[0] = sum[q][0];
+      at[direct ? 1 : LD] = sum[q][1];
     }
     __syncthreads();
-    each([&](int i, int y) __attribute__((always_inline)) {
-      A[i][y] = *reinterpret_cast<const f32x4_t*>(full + column(i) * LD + 16 * y + 4 * g);
-    });
+    sym.complete(bufA, out, A, true);
+    double total = 0.0;                            // |M|_F^2, the diagonal of the tiles on the diagonal
 #pragma unroll
-    for (int d = 0; d < sp; d += 64)
-      if (d + lane < sp) total += double(full[(d + lane) * LD + d + lane]);
-    total = wave_sum(total);          // every wave adds the same entries in the same order
+    for (int d = 0; d < 16 * NY; d += 64)
+      if (d + lane < 16 * NY) total += bufA[S_::at(0, (d + lane) >> 4) + ((d + lane) & 15) * (LD + 1)];
+    total = wave_sum(total);                       // every wave adds the same entries in the same order
+    // a block of zeros gives U = 0; infinities and NaN make everything NaN
+    const double inv = total == 0.0 ? 0.0 : total - total == 0.0 ? 1.0 / total : __builtin_nan("");
+    root = total == 0.0 ? 0.0 : total - total == 0.0 ? 1.0 / sqrt(total) : __builtin_nan("");
+#pragma unroll
+    for (int d = 0; d < NY; ++d)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        A[d][v] *= inv;
+        if (d <= H) out[d <= H ? d : 0][v] = A[d][v];
+        T[d][v] = d == 0 && 4 * v + g == i ? 1.0 : 0.0;
+      }
+    __syncthreads();
+    sym.put(bufA, out);
     __syncthreads();
   }
-  // a block of zeros gives U = 0
-  const float inv = total == 0.0 ? 0.0f : float(1.0 / total);
-  const float root = total == 0.0 ? 0.0f : float(1.0 / sqrt(total));
-  each([&](int i, int y) __attribute__((always_inline)) {
-    A[i][y] *= inv;
-#pragma unroll
-    for (int v = 0; v < 4; ++v) T[i][y][v] = y == NS * wave + i ? unit[v] : 0.0f;
-  });
-  auto split = [&](const f32x4_t (&v)[NS][NY], SymOperand<NY> (&o)[NS]) __attribute__((always_inline)) {
-#pragma unroll
-    for (int i = 0; i < NS; ++i) split_strip<NY>(v[i], o[i]);
-  };
-  // one buffer: everybody is done reading before it is written; two: the one written now
-  // was read before the last barrier
-  auto put = [&](const SymOperand<NY> (&o)[NS]) __attribute__((always_inline)) {
-    if (SHARED) __syncthreads();
-#pragma unroll
-    for (int i = 0; i < NS; ++i) put_strip<NY>(buf, NS * wave + i, lane, o[i]);
-    __syncthreads();
-    char* const w = buf;
-    buf = other;
-    other = w;
-  };
   for (int it = 0; it < steps; ++it) {
     const bool last = it == steps - 1;
-    SymOperand<NY> oA[NS];
-    f32x4_t P[NS][NY];
-    if (it > 0) {
-      // (A + A^T) / 2: strips as rows in, their rows out
-      if (SHARED) __syncthreads();
-      float* full = reinterpret_cast<float*>(buf);
-      each([&](int i, int y) __attribute__((always_inline)) {
-        *reinterpret_cast<f32x4_t*>(full + column(i) * LD + 16 * y + 4 * g) = A[i][y];
-      });
-      __syncthreads();
-      each([&](int i, int y) __attribute__((always_inline)) {
-#pragma unroll
-        for (int v = 0; v < 4; ++v) A[i][y][v] = 0.5f * (A[i][y][v] + full[(16 * y + 4 * g + v) * LD + column(i)]);
-      });
-      char* const w = buf;
-      buf = other;
-      other = w;
-    }
-    split(A, oA);
-    if (c != 0.0f) {
-      put(oA);
-      sym_product<NY, NS>(other, lane, oA, P);               // A A
+    if (c != 0.0) {
+      sym.product(bufA, A, out);                   // A A
     } else {
-      each([&](int i, int y) __attribute__((always_inline)) { P[i][y] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f}; });
-    }
-    each([&](int i, int y) __attribute__((always_inline)) {
-      const float on = y == NS * wave + i ? a : 0.0f;        // this tile lies on the diagonal
 #pragma unroll
-      for (int v = 0; v < 4; ++v) P[i][y][v] = fmaf(c, P[i][y][v], fmaf(b, A[i][y][v], on * unit[v]));
-    });
-    SymOperand<NY> o[NS];
-    split(P, o);
+      for (int d = 0; d <= H; ++d) out[d] = f64x4_t{0.0, 0.0, 0.0, 0.0};
+    }
+    int on = i - g;                                // a on the diagonal, found anew instead of kept in registers
+    asm volatile("" : "+v"(on));
+#pragma unroll
+    for (int d = 0; d <= H; ++d)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) out[d][v] = fma(c, out[d][v], fma(b, A[d][v], d == 0 && 4 * v == on ? a : 0.0));
+    sym.put(bufP, out);                            // P; its readers of the step before have met since
+    __syncthreads();
     if (it == 0) {
-      each([&](int i, int y) __attribute__((always_inline)) { T[i][y] = P[i][y]; });
-      if (last) break;
-      put(o);
+      sym.complete(bufP, out, T);                  // T = P
     } else {
-      put(o);
-      split(T, o);
-      sym_product<NY, NS>(other, lane, o, T);                // T' = P T
-      if (last) break;
+      sym.product(bufP, T, out);                   // T' = P T, through the buffer that A A has left
+      sym.put(bufA, out);
+      __syncthreads();
+      sym.complete(bufA, out, T);
     }
-    sym_product<NY, NS>(other, lane, oA, P);                 // P A
-    split(P, o);
-    sym_product<NY, NS>(other, lane, o, A);                  // A' = P (P A)
+    if (last) break;
+    sym.product(bufP, A, out);                     // P A
+    __syncthreads();
+    sym.put(bufA, out);
+    __syncthreads();
+    sym.complete(bufA, out, A);
+    sym.product(bufP, A, out);                     // A' = P (P A)
+    __syncthreads();
+    sym.put(bufA, out);
+    __syncthreads();
+    sym.complete(bufA, out, A);
   }
-  // T / |M|_F in three bf16 parts, rows of [part][sp][sp]
-  bf16_t* dst = reinterpret_cast<bf16_t*>(ws + run.parts) + int64_t(u) * 3 * sp * sp + 4 * g;
-  each([&](int i, int y) __attribute__((always_inline)) {
-    f32x2_t lo = {T[i][y][0] * root, T[i][y][1] * root}, hi = {T[i][y][2] * root, T[i][y][3] * root};
+  // T / |M|_F in three bf16 parts, rows of [part][sp][sp] with zeros past the last strip
+  constexpr int sp = (NY + 1) / 2 * 32;
+  bf16_t* dst = reinterpret_cast<bf16_t*>(ws + run.parts) + int64_t(u) * kParts * sp * sp;
 #pragma unroll
-    for (int p = 0; p < kParts; ++p) {
-      uint2 w;
-      w.x = leading_part(lo);
-      w.y = leading_part(hi);
-      *reinterpret_cast<uint2*>(dst + p * sp * sp + column(i) * sp + 16 * y) = w;
+  for (int d = 0; d < NY; ++d)
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      f32x2_t x = {float(T[d][v] * root), 0.0f};
+      bf16_t* at = dst + (16 * sym.wrap(wave + d) + 4 * v + g) * sp + 16 * wave + i;
+#pragma unroll
+      for (int p = 0; p < kParts; ++p) at[p * sp * sp] = bf16_t(leading_part(x));
     }
-  });
+  if (NY % 2 != 0)
+    for (int t = threadIdx.x; t < kParts * 16 * sp; t += 64 * NY) {
+      const int p = t / (16 * sp), row = t / sp % 16, col = t % sp;
+      dst[p * sp * sp + (16 * NY + row) * sp + col] = 0;
+      dst[p * sp * sp + col * sp + 16 * NY + row] = 0;
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -609,8 +649,8 @@ __global__ __launch_bounds__(256, 2) void blocks_apply_kernel(Runs runs, const c
   const int groups = 4 / nt, ti = wave % nt, grp = wave / nt;
   const bool busy = grp < groups;
   const int l0 = unit * run.slabs * LS, l1 = min(l, l0 + run.slabs * LS);
-  Region<T, C_::M_LOADS> reg;
-  Region<TO, C_::OUT_LOADS> old;
+  Region<T, C_::M_LOADS, true> reg;
+  Region<TO, C_::OUT_LOADS, true> old;
   auto fetch = [&](int x) __attribute__((always_inline)) {
     if (TALL) reg.fetch(M, ld, l, s, x, 0, LS, sp);
     else reg.fetch(M, ld, s, l, 0, x, sp, LS);
@@ -628,8 +668,7 @@ __global__ __launch_bounds__(256, 2) void blocks_apply_kernel(Runs runs, const c
     }
   for (int x = l0; x < l1; x += LS) {
     __syncthreads();
-    if (TALL) reg.template store<NPM>(lds, PITCH, PLANE, LS, sp);
-    else reg.template store<NPM>(lds, PITCH, PLANE, sp, LS);
+    reg.template store<NPM>(lds, PITCH, PLANE);
     __syncthreads();
     if (e.update) {
       if (TALL) old.fetch(out, ld_out, l, s, x, 0, LS, sp);
@@ -692,17 +731,20 @@ bool valid_shape(const muon_block_problem& p) {
 }
 bool empty(const muon_block_problem& p) { return p.rows == 0 || p.cols == 0 || p.count == 0; }
 
-// How a problem is cut: chunks of the long side for the Gram, slabs per unit of the
-// last product, chosen so that all blocks of the call together give the 256 CUs
-// about four workgroups each (two over a short side of 64, which need twice the
-// registers), but a chunk is never shorter than 256 entries: each one writes a whole
-// partial Gram, and the one CU that iterates reads them all.
+// How a problem is cut.  Chunks of the long side for the Gram, so that all blocks of the
+// call together give the 256 CUs one workgroup each at most, or two over 128 blocks: it is
+// bound by the matrix instructions, and a second, half filled round costs as much as a whole
+// one.  A chunk is never shorter than twice the short side: each one writes a whole partial
+// Gram, 4 s^2 bytes, and the one CU that iterates reads them all.  Slabs per unit of the
+// last product: about four workgroups for each CU (two over a short side of 64, which need
+// twice the registers).
 void cut(Run& r, int64_t total_blocks) {
-  const int64_t want = std::max<int64_t>(1, ceil_div((r.kind & kBig) ? 512 : 1024, std::max<int64_t>(total_blocks, 1)));
-  const int64_t slab = (r.kind & kF32) ? gram_slab<float>() : gram_slab<bf16_t>();
-  int64_t chunks = std::min<int64_t>(want, ceil_div(r.l, 256));
+  total_blocks = std::max<int64_t>(total_blocks, 1);
+  const int64_t slab = gram_slab((r.kind & kBig) != 0);
+  const int64_t chunks = std::min(std::max<int64_t>((total_blocks <= 128 ? 256 : 512) / total_blocks, 1), ceil_div(r.l, 2 * r.s));
   r.chunk = int(ceil_div(ceil_div(r.l, chunks), slab) * slab);
   r.chunks = int(ceil_div(r.l, r.chunk));
+  const int64_t want = ceil_div((r.kind & kBig) ? 512 : 1024, total_blocks);
   const int64_t ls = apply_slab(!(r.kind & kF32) && !r.out_f32, (r.kind & kBig) != 0);
   const int64_t slabs = ceil_div(r.l, ls);
   r.slabs = int(ceil_div(slabs, std::min<int64_t>(slabs, want)));
@@ -719,11 +761,11 @@ Run make_run(const muon_block_problem& p, int64_t total_blocks, size_t& bytes) {
   r.kind = (tall ? kTall : 0) | (p.m_dtype == MUON_F32 ? kF32 : 0) | (r.s > 64 ? kBig : 0);
   r.out_f32 = p.out_dtype == MUON_F32;
   cut(r, total_blocks);
-  const int64_t nt = ceil_div(r.s, 32), sp = nt * 32;
+  const int64_t sp = ceil_div(r.s, 32) * 32;
   r.partials = int64_t(bytes);
-  bytes += round_up(size_t(r.count) * r.chunks * tiles_of(int(nt)) * 4096, 256);
+  bytes += round_up(size_t(r.count) * r.chunks * tiles_of(int(ceil_div(r.s, 16))) * 2048, 256);
   r.parts = int64_t(bytes);
-  bytes += round_up(size_t(r.count) * sp * sp * 6, 256);
+  bytes += round_up(size_t(r.count) * sp * sp * 2 * kParts, 256);
   return r;
 }
 
@@ -828,19 +870,24 @@ int run_blocks(const muon_block_problem* probs, int nprobs, float a, float b, fl
   if (status != MUON_OK) return status;
   const auto poly = [&](auto ny) {
     constexpr int NY = decltype(ny)::value;
-    return for_runs(all, n, [](const Run& r) { return (r.s + 31) / 32 * 2 == NY; }, [&](const Runs& runs) {
+    return for_runs(all, n, [](const Run& r) { return (r.s + 15) / 16 == NY; }, [&](const Runs& runs) {
       int64_t blocks = 0;
       for (int i = 0; i < runs.n; ++i) blocks += runs.r[i].count;
-      constexpr int LDS = SymLds<NY>::BUFFERS * SymLds<NY>::BYTES;
+      constexpr int LDS = 2 * SymTiles<NY>::BYTES;
       static std::atomic<uint64_t> configured{0};
       if (gemm::set_lds_limit(blocks_poly_kernel<NY>, LDS, configured) != MUON_OK) return int(MUON_ELAUNCH);
-      launch_kernel(blocks_poly_kernel<NY>, dim3(blocks), dim3(64 * NY / strips<NY>()), LDS, st, runs, ws, a, b, c, steps);
+      launch_kernel(blocks_poly_kernel<NY>, dim3(blocks), dim3(64 * NY), LDS, st, runs, ws, double(a), double(b), double(c),
+                    steps);
       return launch_status();
     });
   };
-  status = poly(std::integral_constant<int, 2>{});
+  status = poly(std::integral_constant<int, 1>{});
+  if (status == MUON_OK) status = poly(std::integral_constant<int, 2>{});
+  if (status == MUON_OK) status = poly(std::integral_constant<int, 3>{});
   if (status == MUON_OK) status = poly(std::integral_constant<int, 4>{});
+  if (status == MUON_OK) status = poly(std::integral_constant<int, 5>{});
   if (status == MUON_OK) status = poly(std::integral_constant<int, 6>{});
+  if (status == MUON_OK) status = poly(std::integral_constant<int, 7>{});
   if (status == MUON_OK) status = poly(std::integral_constant<int, 8>{});
   if (status != MUON_OK) return status;
   return every_kind(apply);
