@@ -572,8 +572,11 @@ int fp8_gemm(const void* A, int a_fmt, int64_t lda, const void* sa, const void* 
  *                     weight decay and the step in one pass (out = W)
  * M is F32 or BF16 and read only.  The iterations run on T with U = T M
  * (polynomials of A commute, so the long side is read only twice).  A holds
- * squares of singular values, so A and T are computed in fp64.  |M|_F must lie
- * within 2^-100 .. 2^100.  NaN or infinity in a block make that block's U NaN.
+ * squares of singular values, so A and T are computed in fp64.  With g the
+ * largest factor of a step (max |a + b x + c x x| over x in [0, 1], at least 1),
+ * U is off by 2^-53 g^(2 steps) and, up to g^steps = 512, by 2^-24 g^steps of it
+ * at worst, before one rounding to fp32 and one to the type of out.  |M|_F must
+ * lie within 2^-100 .. 2^100.  NaN or infinity in a block make that block's U NaN.
  *
  *   workspace  ns_blocks_workspace_bytes(probs, nprobs) bytes, 16-byte
  *              aligned; contents on entry do not matter.  Calls that share one

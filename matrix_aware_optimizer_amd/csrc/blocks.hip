@@ -19,11 +19,13 @@
 // fp32 that is up to 2^-24 11.9^5 = 1% of U after five quintic steps on a block of low
 // rank, and nothing is left of U after ten.  Gram and iterations are therefore computed in fp64, on the fp64
 // matrix instructions: the same leftover is 2^-53 11.9^5.
-//
-// T enters the last product in two bf16 parts (2^-17 of U, far under half a step of a
-// bf16 output) or three (fp32 outputs), M there in as many at most; products of parts
-// beyond the last one kept are left out.
+// T reaches a^steps in the directions that M lacks, where its products with M cancel.  Up
+// to 512 (five quintic steps) T and an fp32 M enter the last product in three bf16 parts
+// each, and the six products of parts that reach 2^-24 are added in fp32: 2^-24 512 of U
+// at worst, half of what an iteration on X in fp32 leaves.  (Two parts cost a bf16 U of
+// low rank as much as its own rounding.)  Beyond that the last product is fp64 too.
 #include <algorithm>
+#include <cmath>
 
 #include "common.h"
 #include "gemm.h"
@@ -104,14 +106,14 @@ __device__ __forceinline__ uint32_t leading_part(f32x2_t& x) {
 
 // A region of a row-major matrix on its way from memory to LDS: rows [r0, r0 + NR),
 // columns [c0, c0 + NC), entries outside rows x cols as zeros.  fetch() leaves it in
-// registers (LD 16-byte pieces of each of 256 threads), so that it is under way while the
+// registers (LD 16-byte pieces of each of THREADS threads), so that it is under way while the
 // region before is multiplied.  Its loads have no branches of their own, in which they
 // would have to be waited for: rows and columns past the end are read at the last place
 // that exists, and put right by piece(), where the values are used.  Rows shorter than a
 // piece are read there altogether.
 // With ANEW the addresses are formed at every fetch, instead of a row's being kept in
 // registers for each piece.
-template <typename T, int LD, bool ANEW = false>
+template <typename T, int LD, bool ANEW = false, int THREADS = 256>
 struct Region {
   static constexpr int E = 16 / int(sizeof(T));
   u32x4_t w[LD];
@@ -127,7 +129,7 @@ struct Region {
       if (ANEW) asm volatile("" : "+v"(first));
 #pragma unroll
       for (int q = 0; q < LD; ++q) {
-        const int t = min(first + 256 * q, n - 1);
+        const int t = min(first + THREADS * q, n - 1);
         const uint4 v = load16(src + int64_t(min(r0 + t / per, rows - 1)) * ld + min(c0 + t % per * E, cols - E));
         w[q] = u32x4_t{v.x, v.y, v.z, v.w};
       }
@@ -170,7 +172,7 @@ struct Region {
     const int pieces = NC / E;
 #pragma unroll
     for (int q = 0; q < LD; ++q) {
-      const int t = threadIdx.x + 256 * q;
+      const int t = threadIdx.x + THREADS * q;
       if (t < NR * pieces) {
         const int lr = t / pieces, lc = t % pieces * E, r = row0 + lr, c = col0 + lc;
         if (r >= nrows || c >= ncols) continue;
@@ -218,7 +220,7 @@ struct Region {
   __device__ __forceinline__ void store_f64(char* lds, int pitch) const {
 #pragma unroll
     for (int q = 0; q < LD; ++q) {
-      const int t = threadIdx.x + 256 * q;
+      const int t = threadIdx.x + THREADS * q;
       if (t < n) {
         const int r = t / per, c = t % per * E;
         const u32x4_t x = piece(q, r0 + r, c0 + c);
@@ -237,7 +239,7 @@ struct Region {
   __device__ __forceinline__ void store(char* lds, int pitch, int plane) const {
 #pragma unroll
     for (int q = 0; q < LD; ++q) {
-      const int t = threadIdx.x + 256 * q;
+      const int t = threadIdx.x + THREADS * q;
       if (t < n) {
         const int r = t / per, c = t % per * E;
         const u32x4_t x = piece(q, r0 + r, c0 + c);
@@ -381,8 +383,8 @@ __global__ __launch_bounds__(256, 2) void blocks_gram_kernel(Runs runs, char* ws
 // is its own second operand without leaving the registers.  First operands are rows of S,
 // by symmetry columns, and come from LDS in the same layout.
 // 17 products of a block in five steps, one after another on one CU: 40 us at s = 64, 74 at
-// 80, 171 at 128 (up to 256 blocks), 77%, 57% and 82% of it matrix instructions; at 80 five
-// strips leave three of four SIMDs half empty.
+// 80, 171 at 128 (up to 256 blocks); the SIMDs multiply during 58%, 49% and 82% of it (at 80
+// one of them has two of the five strips).
 template <int NY>
 struct SymTiles {
   static constexpr int H = NY / 2;                 // slots 0 .. H are computed
@@ -481,7 +483,8 @@ struct SymTiles {
 };
 
 template <int NY>
-__global__ __launch_bounds__(64 * NY, 2) void blocks_poly_kernel(Runs runs, char* ws, double a, double b, double c, int steps) {
+__global__ __launch_bounds__(64 * NY, 2) void blocks_poly_kernel(Runs runs, char* ws, double a, double b, double c, int steps,
+                                                                    int exact) {
   extern __shared__ __attribute__((aligned(16))) char sm[];
   using S_ = SymTiles<NY>;
   constexpr int H = S_::H, LD = S_::LD, TILE = S_::TILE, NLOW = tiles_of(NY);
@@ -587,7 +590,15 @@ __global__ __launch_bounds__(64 * NY, 2) void blocks_poly_kernel(Runs runs, char
     __syncthreads();
     sym.complete(bufA, out, A);
   }
-  // T / |M|_F in three bf16 parts, rows of [part][sp][sp] with zeros past the last strip
+  if (exact) {   // T / |M|_F, rows of [16 NY][16 NY]
+    double* dst = reinterpret_cast<double*>(ws + run.parts) + int64_t(u) * (256 * NY * NY) + 16 * wave + i;
+#pragma unroll
+    for (int d = 0; d < NY; ++d)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) dst[(16 * sym.wrap(wave + d) + 4 * v + g) * (16 * NY)] = T[d][v] * root;
+    return;
+  }
+  // or in three bf16 parts, rows of [part][sp][sp] with zeros past the last strip
   constexpr int sp = (NY + 1) / 2 * 32;
   bf16_t* dst = reinterpret_cast<bf16_t*>(ws + run.parts) + int64_t(u) * kParts * sp * sp;
 #pragma unroll
@@ -612,16 +623,16 @@ __global__ __launch_bounds__(64 * NY, 2) void blocks_poly_kernel(Runs runs, char
 // share of a slab of the long side.  The results meet in LDS in the output's own layout
 // (over the slab's operand planes, which are done with), so that the output is read (for
 // an update; fetched while the slab is multiplied) and written in whole rows, 16 bytes
-// per lane.  Bound by memory: 32 blocks 128 x 4096, fp32 M, bf16 W updated: 37 us, 3.6 TB/s
-// (50 us with rows written 8 bytes per lane); 144 blocks 768 x 64 bf16 updated: 15.5 us.
+// per lane.  Bound by memory for a bf16 M: 144 blocks 768 x 64 updated 17.4 us; an fp32 M's
+// splitting and six products take about as long: 32 blocks 128 x 4096, bf16 W updated, 44 us.
 // ---------------------------------------------------------------------------
 // entries of the long side at a time: 64 keep two waves per SIMD in registers
 constexpr int apply_slab(bool all_bf16, bool big) { return all_bf16 && !big ? 128 : 64; }
 template <typename T, typename TO, bool TALL, bool BIG>
 struct ApplyTile {
   static constexpr int LS = apply_slab(sizeof(T) == 2 && sizeof(TO) == 2, BIG), SIDE = BIG ? 128 : 64, NQ = SIDE / 16;
-  static constexpr int NPT = sizeof(TO) == 2 ? 2 : 3;                 // bf16 parts of T
-  static constexpr int NPM = sizeof(T) == 2 ? 1 : NPT;                // and of M
+  static constexpr int NPT = kParts;                       // bf16 parts of T
+  static constexpr int NPM = sizeof(T) == 2 ? 1 : kParts;  // and of M
   static constexpr int PITCH = TALL ? row_pitch(2 * SIDE) : tr_pitch(2 * LS);   // tall [LS][s], wide [s][LS]
   static constexpr int PLANE = (TALL ? LS : SIDE) * PITCH;
   static constexpr int ROWS = TALL ? LS : SIDE, COLS = TALL ? SIDE : LS;        // of the output's tile
@@ -720,6 +731,121 @@ __global__ __launch_bounds__(256, 2) void blocks_apply_kernel(Runs runs, const c
 }
 
 // ---------------------------------------------------------------------------
+// apply in fp64, where T is too large for parts.  A wave keeps 16 rows of T in registers
+// and multiplies them with its share of a slab: four waves, or eight over a short side of
+// 64.  The results meet in LDS as fp32, as above.  32 blocks 128 x 4096, fp32 M, bf16 W
+// updated: 114 us, 50 blocks 80 x 2309 fp32 55, half of it matrix instructions.
+// ---------------------------------------------------------------------------
+constexpr int kExactSlab = 64;   // entries of the long side at a time
+template <typename T, typename TO, bool TALL, bool BIG>
+struct ExactTile {
+  static constexpr int THREADS = BIG ? 512 : 256;
+  static constexpr int LS = kExactSlab, SIDE = BIG ? 128 : 64, NK = SIDE / 16;
+  // fp64; tall [LS][s]: 16 bytes of 16 rows at once; wide [s][LS]: 16 entries of two rows four
+  // apart, which start half the banks apart
+  static constexpr int PITCH = TALL ? 8 * SIDE + 16 : 8 * LS + 32;
+  static constexpr int ROWS = TALL ? LS : SIDE, COLS = TALL ? SIDE : LS;        // of the tiles of M and of the output
+  static constexpr int M_BYTES = ROWS * PITCH;
+  static constexpr int OUT_LD = COLS + 4;
+  static constexpr int LDS_BYTES = M_BYTES + ROWS * OUT_LD * 4;
+  static constexpr int M_LOADS = SIDE * LS * int(sizeof(T)) / 16 / THREADS, OUT_LOADS = SIDE * LS * int(sizeof(TO)) / 16 / THREADS;
+};
+
+template <typename T, typename TO, bool TALL, bool BIG>
+__global__ __launch_bounds__(BIG ? 512 : 256, 2) void blocks_apply_exact_kernel(Runs runs, const char* ws, Epilogue e) {
+  using C_ = ExactTile<T, TO, TALL, BIG>;
+  constexpr int LS = C_::LS, NK = C_::NK, PITCH = C_::PITCH, CT = LS / 16;
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  float* const tile = reinterpret_cast<float*>(lds + C_::M_BYTES);
+  int u = blockIdx.x;
+  const Run& run = find_run(runs, u, 2);
+  const int b = u / run.units, unit = u % run.units;
+  const int s = run.s, l = run.l, ny = (s + 15) / 16, sp = 16 * ny;
+  const T* M = static_cast<const T*>(run.M) + b * run.stride_m;
+  TO* out = static_cast<TO*>(run.out) + b * run.stride_out;
+  const int64_t ld = run.ld_m, ld_out = run.ld_out;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int i = lane & 15, g = lane >> 4;
+  // The wave's row tile of T, and its 16-entry columns of the slab.  Up to four row tiles: a
+  // wave each, the slab shared where there are fewer.  More: waves 0 - 3 take one each, and of
+  // those left over one is cut in four, two in two, three or four are taken whole.
+  int row, first, step, count;
+  if (!BIG || wave < 4) {
+    const int tiles = BIG ? 4 : ny, groups = 4 / tiles;
+    row = wave % tiles; first = wave / tiles; step = groups;
+    count = first < groups ? CT / groups : 0;
+  } else {
+    const int w = wave - 4, extra = ny - 4, groups = extra <= 2 ? 4 / extra : 1;
+    row = 4 + w % (4 / groups); first = w / (4 / groups); step = groups;
+    count = w < extra * groups ? CT / groups : 0;
+  }
+  const int l0 = unit * run.slabs * LS, l1 = min(l, l0 + run.slabs * LS);
+  Region<T, C_::M_LOADS, true, C_::THREADS> reg;
+  Region<TO, C_::OUT_LOADS, true, C_::THREADS> old;
+  auto fetch = [&](int x) __attribute__((always_inline)) {
+    if (TALL) reg.fetch(M, ld, l, s, x, 0, LS, sp);
+    else reg.fetch(M, ld, s, l, 0, x, sp, LS);
+  };
+  fetch(l0);
+  // lane 16 g + i: row i of the tile, k-values 16 q + 4 g .. + 3
+  f64x4_t tf[NK];
+#pragma unroll
+  for (int q = 0; q < NK; ++q) {
+    tf[q] = f64x4_t{0.0, 0.0, 0.0, 0.0};
+    if (q < ny && count > 0)
+      tf[q] = *reinterpret_cast<const f64x4_t*>(reinterpret_cast<const double*>(ws + run.parts) + int64_t(b) * sp * sp +
+                                                (row * 16 + i) * sp + 16 * q + 4 * g);
+  }
+  for (int x = l0; x < l1; x += LS) {
+    reg.store_f64(lds, PITCH);
+    __syncthreads();   // the slab is here, and the tile before has been read
+    if (e.update) {
+      if (TALL) old.fetch(out, ld_out, l, s, x, 0, LS, sp);
+      else old.fetch(out, ld_out, s, l, 0, x, sp, LS);
+    }
+    if (x + LS < l1) fetch(x + LS);
+    for (int k = 0; k < count; ++k) {
+      const int j = first + k * step;
+      f64x4_t acc[2] = {f64x4_t{0.0, 0.0, 0.0, 0.0}, f64x4_t{0.0, 0.0, 0.0, 0.0}};   // neither waits for the other
+      // M's four k-values, each read while the four before are multiplied
+      f64x4_t m[2];
+      auto read = [&](int q) __attribute__((always_inline)) {
+        if constexpr (TALL) {
+          const f64x2_t* p = reinterpret_cast<const f64x2_t*>(lds + (16 * j + i) * PITCH + (16 * q + 4 * g) * 8);
+          const f64x2_t a = p[0], b = p[1];
+          m[q & 1] = f64x4_t{a[0], a[1], b[0], b[1]};
+        } else {
+          const char* p = lds + (16 * q + 4 * g) * PITCH + (16 * j + i) * 8;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) m[q & 1][c] = *reinterpret_cast<const double*>(p + c * PITCH);
+        }
+      };
+      read(0);
+#pragma unroll
+      for (int q = 0; q < NK; ++q) {
+        if (q < ny) {
+          if (q + 1 < NK) read(q + 1);
+          __builtin_amdgcn_sched_barrier(0);   // the reads stay in front
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            // tall: the slab's rows first, as U's rows lie along the long side
+            if (TALL) mma64(m[q & 1][c], tf[q][c], acc[c & 1]);
+            else mma64(tf[q][c], m[q & 1][c], acc[c & 1]);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+      const int r = (TALL ? 16 * j : 16 * row) + g, c = (TALL ? 16 * row : 16 * j) + i;
+#pragma unroll
+      for (int v = 0; v < 4; ++v) tile[(r + 4 * v) * C_::OUT_LD + c] = float(acc[0][v] + acc[1][v]);
+    }
+    __syncthreads();
+    if (TALL) old.finish(tile, C_::OUT_LD, out, ld_out, l, s, x, 0, LS, sp, e);
+    else old.finish(tile, C_::OUT_LD, out, ld_out, s, l, 0, x, sp, LS, e);
+  }
+}
+
+// ---------------------------------------------------------------------------
 // host
 // ---------------------------------------------------------------------------
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -738,21 +864,21 @@ bool empty(const muon_block_problem& p) { return p.rows == 0 || p.cols == 0 || p
 // Gram, 4 s^2 bytes, and the one CU that iterates reads them all.  Slabs per unit of the
 // last product: about four workgroups for each CU (two over a short side of 64, which need
 // twice the registers).
-void cut(Run& r, int64_t total_blocks) {
+void cut(Run& r, int64_t total_blocks, bool exact) {
   total_blocks = std::max<int64_t>(total_blocks, 1);
   const int64_t slab = gram_slab((r.kind & kBig) != 0);
   const int64_t chunks = std::min(std::max<int64_t>((total_blocks <= 128 ? 256 : 512) / total_blocks, 1), ceil_div(r.l, 2 * r.s));
   r.chunk = int(ceil_div(ceil_div(r.l, chunks), slab) * slab);
   r.chunks = int(ceil_div(r.l, r.chunk));
   const int64_t want = ceil_div((r.kind & kBig) ? 512 : 1024, total_blocks);
-  const int64_t ls = apply_slab(!(r.kind & kF32) && !r.out_f32, (r.kind & kBig) != 0);
+  const int64_t ls = exact ? kExactSlab : apply_slab(!(r.kind & kF32) && !r.out_f32, (r.kind & kBig) != 0);
   const int64_t slabs = ceil_div(r.l, ls);
   r.slabs = int(ceil_div(slabs, std::min<int64_t>(slabs, want)));
   r.units = int(ceil_div(slabs, r.slabs));
 }
 
 // Fills the run of one problem and moves `bytes` past its workspace.
-Run make_run(const muon_block_problem& p, int64_t total_blocks, size_t& bytes) {
+Run make_run(const muon_block_problem& p, int64_t total_blocks, bool exact, size_t& bytes) {
   Run r{};
   const bool tall = p.rows > p.cols;
   r.M = p.M; r.out = p.out;
@@ -760,14 +886,24 @@ Run make_run(const muon_block_problem& p, int64_t total_blocks, size_t& bytes) {
   r.s = int(std::min(p.rows, p.cols)); r.l = int(std::max(p.rows, p.cols)); r.count = int(p.count);
   r.kind = (tall ? kTall : 0) | (p.m_dtype == MUON_F32 ? kF32 : 0) | (r.s > 64 ? kBig : 0);
   r.out_f32 = p.out_dtype == MUON_F32;
-  cut(r, total_blocks);
+  cut(r, total_blocks, exact);
   const int64_t sp = ceil_div(r.s, 32) * 32;
   r.partials = int64_t(bytes);
   bytes += round_up(size_t(r.count) * r.chunks * tiles_of(int(ceil_div(r.s, 16))) * 2048, 256);
   r.parts = int64_t(bytes);
-  bytes += round_up(size_t(r.count) * sp * sp * 2 * kParts, 256);
+  bytes += round_up(size_t(r.count) * sp * sp * 8, 256);   // in fp64, or in parts of 6 bytes
   return r;
 }
+
+// Largest factor by which a step scales a singular value of at most 1: the maximum of
+// |a + b x + c x x| over x in [0, 1], at least 1.
+double growth(double a, double b, double c) {
+  double g = std::max(std::max(1.0, std::abs(a)), std::abs(a + b + c));
+  const double x = c != 0.0 ? -b / (2.0 * c) : 0.0;
+  if (x > 0.0 && x < 1.0) g = std::max(g, std::abs(a + b * x + c * x * x));
+  return g;
+}
+constexpr double kPartsGrowth = 9.0;   // log2 of what T may reach for the last product to take it in bf16 parts
 
 int64_t count_blocks(const muon_block_problem* probs, int n) {
   int64_t total = 0;
@@ -784,6 +920,17 @@ int launch_apply(const Runs& runs, const char* ws, const Epilogue& e, hipStream_
   static std::atomic<uint64_t> configured{0};
   if (gemm::set_lds_limit(blocks_apply_kernel<T, TO, TALL, BIG>, LDS, configured) != MUON_OK) return MUON_ELAUNCH;
   launch_kernel(blocks_apply_kernel<T, TO, TALL, BIG>, dim3(units), dim3(256), LDS, st, runs, ws, e);
+  return launch_status();
+}
+
+template <typename T, typename TO, bool TALL, bool BIG>
+int launch_exact(const Runs& runs, const char* ws, const Epilogue& e, hipStream_t st) {
+  int64_t units = 0;
+  for (int i = 0; i < runs.n; ++i) units += int64_t(runs.r[i].count) * runs.r[i].units;
+  using C_ = ExactTile<T, TO, TALL, BIG>;
+  static std::atomic<uint64_t> configured{0};
+  if (gemm::set_lds_limit(blocks_apply_exact_kernel<T, TO, TALL, BIG>, C_::LDS_BYTES, configured) != MUON_OK) return MUON_ELAUNCH;
+  launch_kernel(blocks_apply_exact_kernel<T, TO, TALL, BIG>, dim3(units), dim3(C_::THREADS), C_::LDS_BYTES, st, runs, ws, e);
   return launch_status();
 }
 
@@ -832,11 +979,12 @@ int run_blocks(const muon_block_problem* probs, int nprobs, float a, float b, fl
   if (workspace == nullptr || ws_bytes < need) return MUON_EWORKSPACE;
   if (!aligned16(workspace)) return MUON_EALIGN;
   char* ws = static_cast<char*>(workspace);
+  const bool exact = steps * std::log2(growth(a, b, c)) > kPartsGrowth;
   Run all[MUON_BLOCKS_MAX_PROBLEMS];
   int n = 0;
   size_t bytes = 0;
   for (int i = 0; i < nprobs; ++i)
-    if (!empty(probs[i])) all[n++] = make_run(probs[i], total, bytes);
+    if (!empty(probs[i])) all[n++] = make_run(probs[i], total, exact, bytes);
   // gram and apply: one launch per type, orientation and half of the range of short sides
   const auto gram = [&](auto t_c, auto tall_c, auto big_c) {
     using T = decltype(t_c);
@@ -848,10 +996,16 @@ int run_blocks(const muon_block_problem* probs, int nprobs, float a, float b, fl
     using T = decltype(t_c);
     constexpr bool TALL = decltype(tall_c)::value, BIG = decltype(big_c)::value;
     const int status = for_runs(all, n, [](const Run& r) { return r.kind == kind_of<T, TALL, BIG>() && !r.out_f32; },
-                                [&](const Runs& runs) { return launch_apply<T, bf16_t, TALL, BIG>(runs, ws, e, st); });
+                                [&](const Runs& runs) {
+                                  return exact ? launch_exact<T, bf16_t, TALL, BIG>(runs, ws, e, st)
+                                               : launch_apply<T, bf16_t, TALL, BIG>(runs, ws, e, st);
+                                });
     if (status != MUON_OK) return status;
     return for_runs(all, n, [](const Run& r) { return r.kind == kind_of<T, TALL, BIG>() && r.out_f32; },
-                    [&](const Runs& runs) { return launch_apply<T, float, TALL, BIG>(runs, ws, e, st); });
+                    [&](const Runs& runs) {
+                      return exact ? launch_exact<T, float, TALL, BIG>(runs, ws, e, st)
+                                   : launch_apply<T, float, TALL, BIG>(runs, ws, e, st);
+                    });
   };
   const auto every_kind = [&](const auto& f) {
     using Yes = std::true_type;
@@ -877,7 +1031,7 @@ int run_blocks(const muon_block_problem* probs, int nprobs, float a, float b, fl
       static std::atomic<uint64_t> configured{0};
       if (gemm::set_lds_limit(blocks_poly_kernel<NY>, LDS, configured) != MUON_OK) return int(MUON_ELAUNCH);
       launch_kernel(blocks_poly_kernel<NY>, dim3(blocks), dim3(64 * NY), LDS, st, runs, ws, double(a), double(b), double(c),
-                    steps);
+                    steps, int(exact));
       return launch_status();
     });
   };
@@ -907,7 +1061,7 @@ size_t ns_blocks_workspace_bytes(const muon_block_problem* probs, int nprobs) {
   const int64_t total = count_blocks(probs, nprobs);
   size_t bytes = 0;
   for (int i = 0; i < nprobs; ++i)
-    if (!empty(probs[i])) make_run(probs[i], total, bytes);
+    if (!empty(probs[i])) make_run(probs[i], total, false, bytes);
   return bytes;
 }
 

@@ -73,3 +73,56 @@ def test_blocks_of_any_size(exponent, m_dtype):
     M = M * 2.0 ** (exponent - np.floor(np.log2(float(M.float().norm()))))
     errs = relative_errors(M, "f32", QUINTIC, 5)
     assert max(errs) <= 2.0 ** -24 * (1 + np.sqrt(48) * growth(QUINTIC) ** 5), errs
+
+
+def tolerance(s, out_dtype, coeffs, steps):
+    """Half a step of the output's type and of fp32, and what comes before: the Gram matrix and the iterations in
+    fp64, whose rounding grows by g^2 per step, and the product T M, in 24 bits while T is at most g^steps = 512."""
+    g = growth(coeffs) ** steps
+    before = np.sqrt(s) * (2.0 ** -53 * g * g + (2.0 ** -24 * g if g <= 512 else 0.0))
+    return torch.finfo(DT[out_dtype]).eps / 2 + 2.0 ** -24 + before
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("out_dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("m_dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("s,l", [(64, 768), (128, 1024), (80, 500)])
+def test_little_but_the_output_is_rounded(s, l, kind, m_dtype, out_dtype):
+    M = spectrum(kind, s, l, m_dtype, 1)
+    for coeffs, steps in ((QUINTIC, 1), (QUINTIC, 3), (QUINTIC, 5), (QUINTIC, 6), (QUINTIC, 8), (QUINTIC, 12), (CUBIC, 5),
+                          (CUBIC, 15), (CUBIC, 16), (CUBIC, 30)):
+        tol = tolerance(s, out_dtype, coeffs, steps)
+        errs = relative_errors(M, out_dtype, coeffs, steps)
+        assert max(errs) <= tol, (coeffs, steps, errs, tol)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("w_dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("steps", [5, 7])
+@pytest.mark.parametrize("kind", ["rank1", "rank4", "power"])
+def test_update_of_uneven_spectra(kind, steps, w_dtype):
+    """The update takes the same U: its error stays that of the rounding of W."""
+    s, l, eta, decay, scale = 64, 768, 0.5, 0.25, 4.0
+    M = spectrum(kind, s, l, "f32", 2)
+    W = torch.from_numpy(np.random.default_rng(3).standard_normal((s, l)).astype(np.float32) * 0.02).to(DT[w_dtype])
+    got = W.cuda()
+    mao.ns_blocks_update([(M.cuda(), got)], *QUINTIC, steps, eta=eta, decay=decay, scale=scale)
+    U = O.newton_schulz(M.double().numpy(), *(float(np.float32(v)) for v in QUINTIC), steps)
+    ref = (1 - eta * decay) * W.double().numpy() - eta * scale * U
+    # W's half step; both products and their sum in fp32; U's own error without its rounding to a type
+    tol = (torch.finfo(DT[w_dtype]).eps / 2 + 2.0 ** -23) * np.linalg.norm(ref) + eta * scale * np.linalg.norm(U) * (
+        tolerance(s, "f32", QUINTIC, steps) + 2.0 ** -24)
+    assert np.linalg.norm(got.double().cpu().numpy() - ref) <= tol
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("steps", [5, 6])
+@pytest.mark.parametrize("s", [1, 2, 15, 16, 17, 33, 48, 63, 65, 79, 81, 96, 97, 111, 112, 113, 127, 128])
+def test_every_number_of_strips(s, steps):
+    """Short sides at and next to multiples of 16, long sides that end inside a slab, several chunks of the Gram."""
+    for l, m_dtype in ((s, "f32"), (s + 1, "bf16"), (3 * s + 131, "bf16"), (4 * s + 1100, "f32")):
+        M = torch.from_numpy(np.random.default_rng([s, l]).standard_normal((s, l)).astype(np.float32)).to(DT[m_dtype])
+        tol = tolerance(s, "f32", QUINTIC, steps)
+        errs = relative_errors(M, "f32", QUINTIC, steps)
+        assert max(errs) <= tol, (l, errs, tol)
