@@ -575,7 +575,10 @@ int fp8_gemm(const void* A, int a_fmt, int64_t lda, const void* sa, const void* 
  * squares of singular values, so A and T are computed in fp64.  With g the
  * largest factor of a step (max |a + b x + c x x| over x in [0, 1], at least 1),
  * U is off by 2^-53 g^(2 steps) and, up to g^steps = 512, by 2^-24 g^steps of it
- * at worst, before one rounding to fp32 and one to the type of out.  |M|_F must
+ * at worst, before one rounding to fp32 and one to the type of out.  Steps and
+ * coefficients with g^steps over 2^MUON_BLOCKS_MAX_GROWTH (more than 12 steps of
+ * 3.4445, -4.775, 2.0315, or 37 of 1.5, -0.5, 0) are refused (MUON_EINVAL): a
+ * singular value that is zero in M would come out of the rounding.  |M|_F must
  * lie within 2^-100 .. 2^100.  NaN or infinity in a block make that block's U NaN.
  *
  *   workspace  ns_blocks_workspace_bytes(probs, nprobs) bytes, 16-byte
@@ -594,6 +597,7 @@ int fp8_gemm(const void* A, int a_fmt, int64_t lda, const void* sa, const void* 
 #define MUON_BLOCKS_MAX_LONG (1 << 24)
 #define MUON_BLOCKS_MAX_COUNT (1 << 20)
 #define MUON_BLOCKS_MAX_PROBLEMS 512
+#define MUON_BLOCKS_MAX_GROWTH 22
 
 typedef struct muon_block_problem {
   const void* M;

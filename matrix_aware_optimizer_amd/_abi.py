@@ -744,22 +744,26 @@ class PreparedNSBlocks:
 
     ``problems``: (M, out) pairs of strided views [count, rows, cols] (or [rows, cols]).  Without
     ``eta`` the directions are written to ``out``; with it ``out <- (1 - eta decay) out - eta scale U``.
-    Calling the object only enqueues the work, on ``stream`` (default: the current one)."""
+    Calling the object only enqueues the work, on ``stream`` (default: the current one).  Steps and
+    coefficients that the library refuses (too many steps for fp64) raise at construction."""
 
     def __init__(self, problems, a: float, b: float, c: float, steps: int, eta: Optional[float] = None,
                  decay: float = 0.0, scale: float = 1.0, workspace: Optional[torch.Tensor] = None):
         if len(problems) == 0:
             raise ValueError("no problems")
+        self._name = "ns_blocks" if eta is None else "ns_blocks_update"
+        self._fn = getattr(lib(), self._name)
+        how = (float(a), float(b), float(c), int(steps))
+        if eta is not None:
+            how += (float(eta), float(decay), float(scale))
+        _check(self._name, self._fn(None, 0, *how, None, 0, None))     # no problems: only the numbers are looked at
         self._problems = list(problems)     # keeps the tensors alive
         self._arr = _block_problems(self._problems)
         self._ptr = ctypes.cast(self._arr, _c_void_p)
         need = int(lib().ns_blocks_workspace_bytes(self._ptr, len(self._problems)))
         self.workspace = _workspace(need, self._problems[0][0], workspace)
-        self._name = "ns_blocks" if eta is None else "ns_blocks_update"
-        self._fn = getattr(lib(), self._name)
-        extra = () if eta is None else (float(eta), float(decay), float(scale))
-        self._args = (self._ptr, len(self._problems), float(a), float(b), float(c), int(steps), *extra,
-                      _dev(self.workspace, "workspace"), self.workspace.numel() * self.workspace.element_size())
+        self._args = (self._ptr, len(self._problems), *how, _dev(self.workspace, "workspace"),
+                      self.workspace.numel() * self.workspace.element_size())
 
     def __call__(self, stream=None) -> None:
         _check(self._name, self._fn(*self._args, _stream(stream)))

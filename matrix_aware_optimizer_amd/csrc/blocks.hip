@@ -961,6 +961,8 @@ int for_runs(const Run* all, int n, Pick pick, F f) {
 int run_blocks(const muon_block_problem* probs, int nprobs, float a, float b, float c, int steps, const Epilogue& e,
                void* workspace, size_t ws_bytes, hipStream_t st) {
   if (nprobs < 0 || steps < 0 || (nprobs > 0 && probs == nullptr) || nprobs > MUON_BLOCKS_MAX_PROBLEMS) return MUON_EINVAL;
+  const double t_growth = steps == 0 ? 0.0 : steps * std::log2(growth(a, b, c));   // log2 of what T may reach
+  if (t_growth > MUON_BLOCKS_MAX_GROWTH) return MUON_EINVAL;
   int64_t units = 0;
   for (int i = 0; i < nprobs; ++i) {
     const muon_block_problem& p = probs[i];
@@ -979,7 +981,7 @@ int run_blocks(const muon_block_problem* probs, int nprobs, float a, float b, fl
   if (workspace == nullptr || ws_bytes < need) return MUON_EWORKSPACE;
   if (!aligned16(workspace)) return MUON_EALIGN;
   char* ws = static_cast<char*>(workspace);
-  const bool exact = steps * std::log2(growth(a, b, c)) > kPartsGrowth;
+  const bool exact = t_growth > kPartsGrowth;
   Run all[MUON_BLOCKS_MAX_PROBLEMS];
   int n = 0;
   size_t bytes = 0;
