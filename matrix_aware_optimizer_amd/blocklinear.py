@@ -48,6 +48,7 @@ class BlockLinear:
         self._update = _abi.PreparedNSBlocks([(self._blocks(self.M, heads, head_dim), self._blocks(W, heads, head_dim))],
                                              *coeffs, ns_steps, eta=eta, decay=decay, scale=scale)
         self._accumulating = False      # a backward since the last step: later ones add without beta
+        self._generation = 0            # how often the codes were written: a backward needs those of its forward
         self.requantize()
 
     @staticmethod
@@ -58,6 +59,7 @@ class BlockLinear:
     def requantize(self) -> None:
         """Codes of W and of its transpose, from the current W (after the caller wrote to it)."""
         _abi.fp8_quantize(self.W, self.wq, self.ws, self.wqt, self.wst, block_rows=_abi.MUON_FP8_GROUP)
+        self._generation += 1
 
     def forward(self, x: torch.Tensor, train: bool = True):
         """(y, saved) for x [tokens, in] in bf16 or fp32; ``saved`` (None unless ``train``) goes to backward."""
@@ -67,15 +69,21 @@ class BlockLinear:
         _abi.fp8_quantize(x, xq, xs, *(saved if train else (None, None)))
         y = torch.empty((tokens, self.W.shape[0]), dtype=x.dtype, device=x.device)
         _abi.fp8_gemm(xq, xs, self.wq, self.ws, y)
-        return y, saved
+        return y, (*saved, self._generation) if train else None
 
     def backward(self, dy: torch.Tensor, saved, need_dx: bool = True) -> Optional[torch.Tensor]:
-        """Adds dy^T x to the momentum (decayed by beta once per step) and returns dx."""
+        """Adds dy^T x to the momentum (decayed by beta once per step) and returns dx.
+
+        dx needs the weights of the forward: after a :meth:`step` or :meth:`requantize` in between it raises."""
+        xqt, xst, generation = saved
+        if need_dx and generation != self._generation:
+            raise RuntimeError("the weights were requantised after this forward: their codes, which dx needs, are gone "
+                               "(run backward before step(), or without the input gradient)")
         tokens, out = dy.shape
         dq, ds = _abi.fp8_buffers(tokens, out, "e5m2", device=dy.device) if need_dx else (None, None)
         dqt, dst = _abi.fp8_buffers(out, tokens, "e5m2", device=dy.device)
         _abi.fp8_quantize(dy, dq, ds, dqt, dst)
-        _abi.fp8_gemm(dqt, dst, *saved, self.M, alpha=self.alpha, beta=1.0 if self._accumulating else self.beta)
+        _abi.fp8_gemm(dqt, dst, xqt, xst, self.M, alpha=self.alpha, beta=1.0 if self._accumulating else self.beta)
         self._accumulating = True
         if not need_dx:
             return None
@@ -105,12 +113,12 @@ class _BlockLinearFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, anchor, layer):
         y, saved = layer.forward(x.detach())
-        ctx.layer = layer
-        ctx.save_for_backward(*saved)
+        ctx.layer, ctx.generation = layer, saved[2]
+        ctx.save_for_backward(*saved[:2])
         return y
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
-        dx = ctx.layer.backward(dy.contiguous(), ctx.saved_tensors, ctx.needs_input_grad[0])
+        dx = ctx.layer.backward(dy.contiguous(), (*ctx.saved_tensors, ctx.generation), ctx.needs_input_grad[0])
         return dx, None, None

@@ -1,0 +1,86 @@
+"""BlockLinear where it is used out of the ordinary: order of calls, empty, strided and mismatched inputs."""
+import pytest
+import torch
+
+import matrix_aware_optimizer_amd as mao
+from matrix_aware_optimizer_amd import _abi
+
+
+@pytest.fixture
+def host(monkeypatch):
+    """Layers on the CPU: the kernels are left out and the calls that would be made are recorded."""
+    calls = []
+
+    class Plan:
+        def __init__(self, *args, **how):
+            pass
+
+        def __call__(self):
+            calls.append("update")
+
+    monkeypatch.setattr(_abi, "PreparedNSBlocks", Plan)
+    monkeypatch.setattr(_abi, "fp8_quantize", lambda x, *rest, **how: calls.append(("quantize", x)))
+    monkeypatch.setattr(_abi, "fp8_gemm", lambda a, sa, b, sb, c, **how: (calls.append(("gemm", c)), c.zero_()))
+    return calls
+
+
+def layer(out=64, inp=96, device="cpu", **how):
+    return mao.BlockLinear(torch.ones(out, inp, device=device), head_dim=32, **how)
+
+
+# ---------------------------------------------------------------------------
+# a backward after the weights have changed
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("change", ["step", "requantize"])
+def test_backward_after_a_change_of_the_weights_raises(host, change):
+    lin = layer()
+    x = torch.ones(5, 96, requires_grad=True)
+    y = lin(x)
+    _, saved = lin.forward(x.detach())
+    getattr(lin, change)()
+    del host[:]
+    with pytest.raises(RuntimeError, match="requantised"):
+        y.backward(torch.ones_like(y))
+    with pytest.raises(RuntimeError, match="requantised"):
+        lin.backward(torch.ones(5, 64), saved)
+    assert not host and not lin._accumulating            # the momentum was not touched
+    assert lin.backward(torch.ones(5, 64), saved, need_dx=False) is None
+    lin(torch.ones(5, 96)).backward(torch.ones(5, 64))   # a new forward is free to go back
+    y = lin(x)
+    y.backward(torch.ones_like(y))
+    assert x.grad.shape == x.shape
+
+
+def test_several_forwards_between_steps(host):
+    lin = layer()
+    x = [torch.ones(n, 96, requires_grad=True) for n in (2, 3)]
+    y = [lin(v) for v in x]
+    for v in reversed(y):
+        v.backward(torch.ones_like(v))
+    lin.step()
+    assert all(v.grad is not None for v in x)
+
+
+def test_a_momentum_gradient_alone_may_come_late(host):
+    """Without an input gradient backward reads nothing of the weights."""
+    lin = layer()
+    y = lin(torch.ones(5, 96))
+    lin.step()
+    y.backward(torch.ones_like(y))
+    assert lin._accumulating
+
+
+@pytest.mark.gpu
+def test_stale_weights_on_the_gpu():
+    lin = layer(device="cuda")
+    x = torch.ones(5, 96, device="cuda", requires_grad=True)
+    y = lin(x)
+    y.backward(torch.ones_like(y))
+    assert torch.equal(x.grad, torch.full_like(x, 64.0))
+    y = lin(x)
+    lin.step()
+    M = lin.M.clone()
+    with pytest.raises(RuntimeError, match="requantised"):
+        y.backward(torch.ones_like(y))
+    assert torch.equal(lin.M, M)
