@@ -106,7 +106,7 @@ class BlockLinear:
             y = _BlockLinearFn.apply(flat, anchor, self)
         else:
             y = self.forward(flat, train=False)[0]
-        return y.view(*x.shape[:-1], -1)
+        return y.view(*x.shape[:-1], self.W.shape[0])
 
 
 class _BlockLinearFn(torch.autograd.Function):

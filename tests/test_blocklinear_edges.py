@@ -84,3 +84,32 @@ def test_stale_weights_on_the_gpu():
     with pytest.raises(RuntimeError, match="requantised"):
         y.backward(torch.ones_like(y))
     assert torch.equal(lin.M, M)
+
+
+# ---------------------------------------------------------------------------
+# no tokens
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("shape", [(0, 96), (2, 0, 96), (0, 3, 96)])
+@pytest.mark.parametrize("grad", [False, True])
+def test_no_tokens(host, shape, grad):
+    lin = layer()
+    x = torch.ones(shape, requires_grad=True)
+    with torch.set_grad_enabled(grad):
+        y = lin(x)
+    assert y.shape == (*shape[:-1], 64)
+    if grad:
+        y.backward(torch.ones_like(y))
+        assert x.grad.shape == shape and lin._accumulating
+
+
+@pytest.mark.gpu
+def test_no_tokens_on_the_gpu():
+    """A step without tokens decays the momentum and moves nothing else into it."""
+    lin = layer(device="cuda", beta=0.5)
+    lin.M.fill_(2.0)
+    x = torch.ones(2, 0, 96, device="cuda", dtype=torch.bfloat16, requires_grad=True)
+    y = lin(x)
+    assert y.shape == (2, 0, 64)
+    y.backward(torch.ones_like(y))
+    assert x.grad.shape == x.shape and (lin.M == 1.0).all()
