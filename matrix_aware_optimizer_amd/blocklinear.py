@@ -19,6 +19,14 @@ import torch
 from . import _abi
 
 
+def _rows(t: torch.Tensor) -> torch.Tensor:
+    """``t`` [rows, cols] as the quantiser reads it, contiguous rows from a 16-byte aligned start: a copy where it is not."""
+    rows, cols = t.shape
+    if (cols <= 1 or t.stride(1) == 1) and (rows <= 1 or t.stride(0) >= cols) and t.data_ptr() % 16 == 0:
+        return t
+    return t.clone(memory_format=torch.contiguous_format)
+
+
 class BlockLinear:
     """One projection ``W`` [out, in] with its fp8 codes and its momentum.
 
@@ -63,6 +71,7 @@ class BlockLinear:
 
     def forward(self, x: torch.Tensor, train: bool = True):
         """(y, saved) for x [tokens, in] in bf16 or fp32; ``saved`` (None unless ``train``) goes to backward."""
+        x = _rows(x)
         tokens, inp = x.shape
         xq, xs = _abi.fp8_buffers(tokens, inp, device=x.device)
         saved = _abi.fp8_buffers(inp, tokens, device=x.device) if train else None
@@ -79,6 +88,7 @@ class BlockLinear:
         if need_dx and generation != self._generation:
             raise RuntimeError("the weights were requantised after this forward: their codes, which dx needs, are gone "
                                "(run backward before step(), or without the input gradient)")
+        dy = _rows(dy)
         tokens, out = dy.shape
         dq, ds = _abi.fp8_buffers(tokens, out, "e5m2", device=dy.device) if need_dx else (None, None)
         dqt, dst = _abi.fp8_buffers(out, tokens, "e5m2", device=dy.device)
@@ -120,5 +130,5 @@ class _BlockLinearFn(torch.autograd.Function):
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
-        dx = ctx.layer.backward(dy.contiguous(), (*ctx.saved_tensors, ctx.generation), ctx.needs_input_grad[0])
+        dx = ctx.layer.backward(dy, (*ctx.saved_tensors, ctx.generation), ctx.needs_input_grad[0])
         return dx, None, None

@@ -113,3 +113,51 @@ def test_no_tokens_on_the_gpu():
     assert y.shape == (2, 0, 64)
     y.backward(torch.ones_like(y))
     assert x.grad.shape == x.shape and (lin.M == 1.0).all()
+
+
+# ---------------------------------------------------------------------------
+# rows that are not contiguous or not aligned
+# ---------------------------------------------------------------------------
+
+def odd_views(device, dtype=torch.float32):
+    """Inputs [tokens, 96] as programs have them: transposed, of every other column, repeated rows, an unaligned start."""
+    gen = torch.Generator().manual_seed(1)
+
+    def ints(*shape):
+        return torch.randint(-3, 4, shape, generator=gen).to(device, dtype)
+
+    return {"transposed": ints(96, 7).t(), "every other": ints(7, 192)[:, ::2], "expanded": ints(96).expand(7, 96),
+            "unaligned": ints(7 * 96 + 1)[1:].view(7, 96), "padded": ints(7, 100)[:, 2:98], "aligned": ints(7, 104)[:, 8:],
+            "three": ints(3, 96, 7).transpose(1, 2)}
+
+
+def as_the_kernels_read(t):
+    return t.stride(-1) == 1 and t.stride(0) >= t.shape[1] and t.data_ptr() % 16 == 0
+
+
+@pytest.mark.parametrize("kind", list(odd_views("cpu")))
+def test_rows_reach_the_kernels_contiguous_and_aligned(host, kind):
+    lin = layer()
+    x = odd_views("cpu")[kind].requires_grad_()
+    dy = torch.ones(64).expand(*x.shape[:-1], 64)
+    y = lin(x)
+    y.backward(dy)
+    read = [call[1] for call in host if call[0] == "quantize"][1:]      # the first is W
+    assert len(read) == 2 and all(as_the_kernels_read(t) for t in read)
+    assert torch.equal(read[0], x.detach().reshape(-1, 96)) and torch.equal(read[1], dy.reshape(-1, 64))
+    if kind == "aligned":
+        assert read[0].data_ptr() == x.data_ptr()                       # nothing is copied without need
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("kind", list(odd_views("cpu")))
+def test_odd_rows_on_the_gpu(kind, dtype):
+    x = odd_views("cuda", dtype)[kind]
+    lin, plain = (layer(device="cuda", alpha=1.0) for _ in range(2))
+    got, want = lin(x), plain(x.contiguous().clone())
+    assert torch.equal(got, want)
+    dy = torch.ones(got.numel() + 1, device="cuda", dtype=dtype)[1:].view(-1, 64)      # unaligned
+    got.reshape(-1, 64).backward(dy)
+    want.reshape(-1, 64).backward(dy.clone())
+    assert torch.equal(lin.M, plain.M) and lin.M.abs().sum() > 0
