@@ -71,6 +71,8 @@ class BlockLinear:
 
     def forward(self, x: torch.Tensor, train: bool = True):
         """(y, saved) for x [tokens, in] in bf16 or fp32; ``saved`` (None unless ``train``) goes to backward."""
+        if x.dim() != 2 or x.shape[1] != self.W.shape[1]:
+            raise ValueError(f"x must be [tokens, {self.W.shape[1]}]")
         x = _rows(x)
         tokens, inp = x.shape
         xq, xs = _abi.fp8_buffers(tokens, inp, device=x.device)
@@ -78,18 +80,20 @@ class BlockLinear:
         _abi.fp8_quantize(x, xq, xs, *(saved if train else (None, None)))
         y = torch.empty((tokens, self.W.shape[0]), dtype=x.dtype, device=x.device)
         _abi.fp8_gemm(xq, xs, self.wq, self.ws, y)
-        return y, (*saved, self._generation) if train else None
+        return y, (*saved, tokens, self._generation) if train else None
 
     def backward(self, dy: torch.Tensor, saved, need_dx: bool = True) -> Optional[torch.Tensor]:
         """Adds dy^T x to the momentum (decayed by beta once per step) and returns dx.
 
         dx needs the weights of the forward: after a :meth:`step` or :meth:`requantize` in between it raises."""
-        xqt, xst, generation = saved
+        xqt, xst, tokens, generation = saved
+        out = self.W.shape[0]
+        if dy.shape != (tokens, out):
+            raise ValueError(f"dy must be [{tokens}, {out}], as the forward's y")
         if need_dx and generation != self._generation:
             raise RuntimeError("the weights were requantised after this forward: their codes, which dx needs, are gone "
                                "(run backward before step(), or without the input gradient)")
         dy = _rows(dy)
-        tokens, out = dy.shape
         dq, ds = _abi.fp8_buffers(tokens, out, "e5m2", device=dy.device) if need_dx else (None, None)
         dqt, dst = _abi.fp8_buffers(out, tokens, "e5m2", device=dy.device)
         _abi.fp8_quantize(dy, dq, ds, dqt, dst)
@@ -109,6 +113,8 @@ class BlockLinear:
 
     def __call__(self, x: torch.Tensor) -> torch.Tensor:
         """y for x [..., in], differentiable: backward goes through :meth:`backward`."""
+        if x.dim() == 0 or x.shape[-1] != self.W.shape[1]:
+            raise ValueError(f"x must be [..., {self.W.shape[1]}]")
         flat = x.reshape(-1, x.shape[-1])
         if torch.is_grad_enabled():
             # W is no leaf of autograd (its gradient goes into M), so the node hangs on x or on an empty anchor
@@ -123,12 +129,12 @@ class _BlockLinearFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, anchor, layer):
         y, saved = layer.forward(x.detach())
-        ctx.layer, ctx.generation = layer, saved[2]
+        ctx.layer, ctx.rest = layer, saved[2:]
         ctx.save_for_backward(*saved[:2])
         return y
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
-        dx = ctx.layer.backward(dy, (*ctx.saved_tensors, ctx.generation), ctx.needs_input_grad[0])
+        dx = ctx.layer.backward(dy, (*ctx.saved_tensors, *ctx.rest), ctx.needs_input_grad[0])
         return dx, None, None

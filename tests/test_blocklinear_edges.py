@@ -161,3 +161,33 @@ def test_odd_rows_on_the_gpu(kind, dtype):
     got.reshape(-1, 64).backward(dy)
     want.reshape(-1, 64).backward(dy.clone())
     assert torch.equal(lin.M, plain.M) and lin.M.abs().sum() > 0
+
+
+# ---------------------------------------------------------------------------
+# sizes that do not belong together
+# ---------------------------------------------------------------------------
+
+def test_sizes_of_inputs_and_gradients(host):
+    """Widths are padded to 128 for the products, so that a wrong one within the padding would multiply silently."""
+    lin = layer()                                          # [64, 96]
+    for x in (torch.ones(5, 95), torch.ones(5, 100), torch.ones(2, 5, 128), torch.ones(96)[:95], torch.ones(5, 0)):
+        with pytest.raises(ValueError, match="96"):
+            lin(x)
+    with pytest.raises(ValueError, match="96"):
+        lin.forward(torch.ones(5, 100), train=False)
+    _, saved = lin.forward(torch.ones(5, 96))
+    del host[:]
+    for dy in (torch.ones(5, 65), torch.ones(5, 100), torch.ones(6, 64), torch.ones(100, 64)):
+        for need_dx in (False, True):
+            with pytest.raises(ValueError):
+                lin.backward(dy, saved, need_dx)
+    assert not host and not lin._accumulating
+    lin.backward(torch.ones(5, 64), saved)
+
+
+def test_a_single_row(host):
+    x = torch.ones(96, requires_grad=True)
+    y = layer()(x)
+    assert y.shape == (64,)
+    y.sum().backward()
+    assert x.grad.shape == (96,)
