@@ -179,7 +179,9 @@ def _workspace_on(nbytes: int, like: torch.Tensor, workspace: Optional[torch.Ten
     if workspace is not None or stream is None:
         return _workspace(nbytes, like, workspace)
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream), device=like.device)
+        # handle 0 is the default stream; an ExternalStream of 0 would be a new stream of torch's
+        handle = int(stream)
+        stream = torch.cuda.ExternalStream(handle, device=like.device) if handle else torch.cuda.default_stream(like.device)
     with torch.cuda.stream(stream):
         return _workspace(nbytes, like, None)
 
