@@ -746,7 +746,8 @@ class PreparedNSBlocks:
 
     ``problems``: (M, out) pairs of strided views [count, rows, cols] (or [rows, cols]).  Without
     ``eta`` the directions are written to ``out``; with it ``out <- (1 - eta decay) out - eta scale U``.
-    Calling the object only enqueues the work, on ``stream`` (default: the current one).  Steps and
+    Calling the object only enqueues the work, on ``stream`` (default: the current one), with a workspace
+    of that stream's own memory, kept for its later calls, or ``workspace`` on every stream.  Steps and
     coefficients that the library refuses (too many steps for fp64) raise at construction."""
 
     def __init__(self, problems, a: float, b: float, c: float, steps: int, eta: Optional[float] = None,
@@ -762,13 +763,24 @@ class PreparedNSBlocks:
         self._problems = list(problems)     # keeps the tensors alive
         self._arr = _block_problems(self._problems)
         self._ptr = ctypes.cast(self._arr, _c_void_p)
-        need = int(lib().ns_blocks_workspace_bytes(self._ptr, len(self._problems)))
-        self.workspace = _workspace(need, self._problems[0][0], workspace)
-        self._args = (self._ptr, len(self._problems), *how, _dev(self.workspace, "workspace"),
-                      self.workspace.numel() * self.workspace.element_size())
+        self._need = int(lib().ns_blocks_workspace_bytes(self._ptr, len(self._problems)))
+        self.workspace = _workspace(self._need, self._problems[0][0], workspace)
+        self._given = workspace is not None
+        self._by_stream = {_stream(None): self._entry(self.workspace)}
+        self._args = (self._ptr, len(self._problems), *how)
+
+    @staticmethod
+    def _entry(ws: torch.Tensor):
+        return ws, _dev(ws, "workspace"), ws.numel() * ws.element_size()
 
     def __call__(self, stream=None) -> None:
-        _check(self._name, self._fn(*self._args, _stream(stream)))
+        handle = _stream(stream)
+        entry = self._by_stream.get(handle)
+        if entry is None:
+            # the first call on this stream: memory that is free there (another stream's may still be in use)
+            entry = self._by_stream[handle] = self._entry(
+                self.workspace if self._given else _workspace_on(self._need, self._problems[0][0], None, stream))
+        _check(self._name, self._fn(*self._args, entry[1], entry[2], handle))
 
 
 def ns_blocks(problems, a: float, b: float, c: float, steps: int, workspace: Optional[torch.Tensor] = None,

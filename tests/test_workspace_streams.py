@@ -80,3 +80,65 @@ def test_one_shot_calls(workspaces):
             assert handle == want and stream_of(address) == want
         del workspaces[:]
         torch.cuda.synchronize()
+
+
+def test_a_plan_keeps_a_workspace_for_each_stream(monkeypatch):
+    """The memory that a plan runs on comes from the stream it is called on, whatever stream made the plan."""
+    made, calls = [], []
+    current = [11]
+
+    class Lib:
+        ns_blocks_workspace_bytes = staticmethod(lambda *a: 64)
+        ns_blocks = staticmethod(lambda *a: calls.append((a[-1], a[-3])) or 0)
+
+    def workspace_on(need, like, given, stream):
+        ws = torch.empty(need, dtype=torch.uint8) if given is None else given
+        made.append((_abi._stream(stream), ws.data_ptr()))
+        return ws
+
+    monkeypatch.setattr(_abi, "lib", Lib)
+    monkeypatch.setattr(_abi, "_block_problems", lambda problems: (_abi.BlockProblem * 1)())
+    monkeypatch.setattr(_abi, "_dev", lambda t, name: t.data_ptr())
+    monkeypatch.setattr(_abi, "_stream", lambda stream: current[0] if stream is None else stream)
+    monkeypatch.setattr(_abi, "_workspace_on", workspace_on)
+    monkeypatch.setattr(_abi, "_workspace", lambda need, like, given: workspace_on(need, like, given, None))
+    x = torch.empty(2, 4, 8)
+    plan = mao.PreparedNSBlocks([(x, x)], *QUINTIC, 5)
+    del calls[:]                                         # what the plan asked while it was made
+    for stream in (None, 22, None, 33, 22):
+        plan(stream)
+    current[0] = 44
+    plan()
+    assert [c[0] for c in calls] == [11, 22, 11, 33, 22, 44]
+    owner = {address: handle for handle, address in made}
+    assert all(owner[address] == handle for handle, address in calls)
+    assert len(made) == 4 and plan.workspace.data_ptr() == calls[0][1]
+    # a workspace that the caller gave is used on every stream
+    mine = torch.empty(64, dtype=torch.uint8)
+    plan = mao.PreparedNSBlocks([(x, x)], *QUINTIC, 5, workspace=mine)
+    del calls[:]
+    plan()
+    plan(22)
+    assert [c[1] for c in calls] == [mine.data_ptr()] * 2
+
+
+@pytest.mark.gpu
+def test_plans(workspaces):
+    side, other = torch.cuda.Stream(), torch.cuda.Stream()
+    M, U = blocks()
+    torch.cuda.synchronize()
+    plan = mao.PreparedNSBlocks([(M, U)], *QUINTIC, 5)
+    plan()
+    want = U.clone()
+    default = torch.cuda.current_stream().cuda_stream
+    for stream in (side, other.cuda_stream, 0, None):
+        torch.cuda.synchronize()
+        U.zero_()
+        torch.cuda.synchronize()
+        plan(stream)
+        torch.cuda.synchronize()
+        assert torch.equal(U, want)
+    handles = [handle for handle, _ in workspaces]
+    assert handles == [default, side.cuda_stream, other.cuda_stream, 0, default]
+    for handle, address in workspaces:
+        assert stream_of(address) == handle
