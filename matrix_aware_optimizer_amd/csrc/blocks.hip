@@ -383,7 +383,7 @@ __global__ __launch_bounds__(256, 2) void blocks_gram_kernel(Runs runs, char* ws
 // is its own second operand without leaving the registers.  First operands are rows of S,
 // by symmetry columns, and come from LDS in the same layout.
 // 17 products of a block in five steps, one after another on one CU: 40 us at s = 64, 74 at
-// 80, 171 at 128 (up to 256 blocks); the SIMDs multiply during 58%, 49% and 82% of it (at 80
+// 80, 171 at 128 (up to 256 blocks); the SIMDs multiply during 48%, 49% and 82% of it (at 80
 // one of them has two of the five strips).
 template <int NY>
 struct SymTiles {
