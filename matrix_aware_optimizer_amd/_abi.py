@@ -8,6 +8,7 @@ missing the first call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import functools
 import os
@@ -173,16 +174,23 @@ def _workspace(nbytes: int, like: torch.Tensor, workspace: Optional[torch.Tensor
     return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=like.device)
 
 
+def _allocating_on(stream, like: torch.Tensor):
+    """Context in which torch allocates from ``stream``'s own pool (None: the current stream's) and fills memory on it."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        # handle 0 is the default stream; an ExternalStream of 0 would be a new stream of torch's
+        handle = int(stream)
+        stream = torch.cuda.ExternalStream(handle, device=like.device) if handle else torch.cuda.default_stream(like.device)
+    return torch.cuda.stream(stream)
+
+
 def _workspace_on(nbytes: int, like: torch.Tensor, workspace: Optional[torch.Tensor], stream) -> torch.Tensor:
     """As _workspace, for a call that goes to ``stream``: memory of that stream's own pool, so that it is free
     when the call begins there and is not given to another stream's work while the call runs."""
     if workspace is not None or stream is None:
         return _workspace(nbytes, like, workspace)
-    if not isinstance(stream, torch.cuda.Stream):
-        # handle 0 is the default stream; an ExternalStream of 0 would be a new stream of torch's
-        handle = int(stream)
-        stream = torch.cuda.ExternalStream(handle, device=like.device) if handle else torch.cuda.default_stream(like.device)
-    with torch.cuda.stream(stream):
+    with _allocating_on(stream, like):
         return _workspace(nbytes, like, None)
 
 
@@ -207,7 +215,7 @@ def muon_momentum(M: torch.Tensor, G: torch.Tensor, beta: float, alpha: float,
             raise ValueError("seg_offsets is required with sumsq_out")
         nseg = seg_offsets.numel() - 1
         need = muon_momentum_workspace_bytes(M.numel(), nseg)
-        workspace = _workspace(need, M, workspace)
+        workspace = _workspace_on(need, M, workspace, stream)
         ws_ptr, ws_bytes = _dev(workspace, "workspace"), workspace.numel() * workspace.element_size()
     _check("muon_momentum", lib().muon_momentum(
         _dev(M, "M"), dtype_code(M), _dev(G, "G"), dtype_code(G), M.numel(),
@@ -276,7 +284,7 @@ def ns_orthogonalize(problems: Sequence[ProblemLike], a: float, b: float, c: flo
     arr = _problems(problems)
     prec = precision_code(precision)
     need = int(lib().ns_workspace_bytes(arr, len(problems), prec))
-    workspace = _workspace(need, problems[0][0], workspace)
+    workspace = _workspace_on(need, problems[0][0], workspace, stream)
     _check("ns_orthogonalize", lib().ns_orthogonalize(
         arr, len(problems), float(a), float(b), float(c), int(steps), prec,
         _dev(workspace, "workspace"), workspace.numel() * workspace.element_size(),
@@ -340,12 +348,13 @@ def new_stage_workspace(s: int, l: int, batch: int = 1, precision="bf16", device
     return torch.zeros(max(n, 1024), dtype=torch.uint8, device=device or "cuda")
 
 
-def _stage_ws(workspace, split: bool, s: int, l: int, batch: int, precision, like: torch.Tensor):
+def _stage_ws(workspace, split: bool, s: int, l: int, batch: int, precision, like: torch.Tensor, stream):
     """(pointer, bytes) of the stage workspace: the caller's, a fresh zeroed one, or none."""
     if not split:
         return None, 0
     if workspace is None:
-        workspace = new_stage_workspace(s, l, batch, precision, like.device)
+        with _allocating_on(stream, like):
+            workspace = new_stage_workspace(s, l, batch, precision, like.device)
     return _dev(workspace, "workspace"), workspace.numel() * workspace.element_size()
 
 
@@ -356,7 +365,7 @@ def ns_gram(X: torch.Tensor, A: torch.Tensor, precision="bf16", stream=None,
     (the default) the work is split as ns_orthogonalize splits it, in
     `workspace` (from new_stage_workspace) or a fresh one."""
     batch, s, l = _batch3(X)
-    ws, nbytes = _stage_ws(workspace, split, s, l, batch, precision, X)
+    ws, nbytes = _stage_ws(workspace, split, s, l, batch, precision, X, stream)
     _check("ns_gram", lib().ns_gram(_dev(X, "X"), _dev(A, "A"), s, l, batch,
                                     precision_code(precision), _dev(sumsq, "sumsq"), ws, nbytes,
                                     _stream(stream)))
@@ -366,7 +375,7 @@ def ns_poly(A: torch.Tensor, B: torch.Tensor, b: float, c: float, precision="bf1
             stream=None, workspace: Optional[torch.Tensor] = None, split: bool = True) -> None:
     """B = b A + c A A."""
     batch, s, _ = _batch3(A)
-    ws, nbytes = _stage_ws(workspace, split, s, s, batch, precision, A)
+    ws, nbytes = _stage_ws(workspace, split, s, s, batch, precision, A, stream)
     _check("ns_poly", lib().ns_poly(_dev(A, "A"), _dev(B, "B"), s, batch, float(b), float(c),
                                     precision_code(precision), ws, nbytes, _stream(stream)))
 
@@ -379,7 +388,7 @@ def ns_apply(B: torch.Tensor, X: torch.Tensor, Xout: torch.Tensor, a: float, alp
     With ``X_lo`` the addend is a (X + X_lo); ``Xout_lo`` receives the bf16 rounding
     residual of Xout (bf16 only; the two may be one tensor)."""
     batch, s, l = _batch3(X)
-    ws, nbytes = _stage_ws(workspace, split, s, l, batch, precision, X)
+    ws, nbytes = _stage_ws(workspace, split, s, l, batch, precision, X, stream)
     _check("ns_apply", lib().ns_apply(_dev(B, "B"), _dev(X, "X"), _dev(X_lo, "X_lo"), _dev(Xout, "Xout"),
                                       _dev(Xout_lo, "Xout_lo"), s, l, batch, float(a), float(alpha),
                                       precision_code(precision), _dev(sumsq, "sumsq"), ws, nbytes,
@@ -395,7 +404,7 @@ def ns_apply_signs(B: torch.Tensor, X: torch.Tensor, Xout: Optional[torch.Tensor
     batch, s, l = _batch3(X)
     if bits.element_size() != 8 or bits.numel() < batch * (s * l // 64):
         raise ValueError("bits must hold batch * s * l / 64 64-bit words")
-    ws, nbytes = _stage_ws(workspace, split, s, l, batch, precision, X)
+    ws, nbytes = _stage_ws(workspace, split, s, l, batch, precision, X, stream)
     _check("ns_apply_signs", lib().ns_apply_signs(
         _dev(B, "B"), _dev(X, "X"), _dev(X_lo, "X_lo"), _dev(Xout, "Xout"), _dev(bits, "bits"), s, l,
         batch, float(a), float(alpha), precision_code(precision), _dev(sumsq, "sumsq"), ws, nbytes,
@@ -588,7 +597,7 @@ def dion_step(problems, rank: int, mu: float, eta: float, workspace: Optional[to
         return
     arr = _dion_problems(problems)
     nbytes = int(lib().dion_workspace_bytes(ctypes.cast(arr, ctypes.c_void_p), len(problems), int(rank)))
-    ws = _workspace(nbytes, problems[0][0], workspace)
+    ws = _workspace_on(nbytes, problems[0][0], workspace, stream)
     _check("dion_step", lib().dion_step(ctypes.cast(arr, ctypes.c_void_p), len(problems), int(rank),
                                         float(mu), float(eta), _dev(ws, "workspace"),
                                         ws.numel() * ws.element_size(), _stream(stream)))

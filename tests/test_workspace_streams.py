@@ -35,13 +35,13 @@ def stream_of(address):
 
 @pytest.fixture
 def workspaces(monkeypatch):
-    """(stream, workspace address) of every call of fp8_gemm, ns_blocks and ns_blocks_update, and the calls go on."""
+    """(stream, workspace address) of every call that takes a workspace, and the calls go on."""
     seen, L = [], mao.lib()
 
     class Recording:
         def __getattr__(self, name):
             real = getattr(L, name)
-            if name not in ("fp8_gemm", "ns_blocks", "ns_blocks_update"):
+            if name not in ("fp8_gemm", "ns_blocks", "ns_blocks_update", "muon_momentum", "ns_orthogonalize", "ns_gram", "dion_step"):
                 return real
 
             def call(*args):
@@ -142,3 +142,28 @@ def test_plans(workspaces):
     assert handles == [default, side.cuda_stream, other.cuda_stream, 0, default]
     for handle, address in workspaces:
         assert stream_of(address) == handle
+
+
+@pytest.mark.gpu
+def test_calls_of_the_optimizer_steps(workspaces):
+    """muon_momentum, ns_orthogonalize, a stage call (its fresh workspace is cleared on the call's stream) and dion_step."""
+    side, other = torch.cuda.Stream(), torch.cuda.Stream()
+    M, G = (torch.randn(256, 512, device="cuda") for _ in range(2))
+    U, sums = torch.empty_like(M), torch.empty(1, device="cuda")
+    offsets = torch.tensor([0, M.numel()], device="cuda")
+    X = torch.randn(1, 256, 512, device="cuda").to(torch.bfloat16)
+    A = torch.empty(1, 256, 256, device="cuda", dtype=torch.bfloat16)
+    Q = torch.linalg.qr(torch.randn(512, 16, device="cuda"))[0].contiguous()
+    torch.cuda.synchronize()
+    for stream in (None, 0, side, side.cuda_stream):
+        with torch.cuda.stream(other):
+            mao.muon_momentum(M, G, 0.9, 0.1, offsets, sums, stream=stream)
+            mao.ns_orthogonalize([(M, U, None)], *QUINTIC, 5, stream=stream)
+            mao.ns_gram(X, A, stream=stream)
+            mao.dion_step([(M, G, U, Q)], 16, 0.95, 0.01, stream=stream)
+        want = other.cuda_stream if stream is None else stream if isinstance(stream, int) else stream.cuda_stream
+        assert len(workspaces) == 4
+        for handle, address in workspaces:
+            assert handle == want and stream_of(address) == want
+        del workspaces[:]
+        torch.cuda.synchronize()
