@@ -619,6 +619,104 @@ int ns_blocks(const muon_block_problem* probs, int nprobs, float a, float b, flo
 int ns_blocks_update(const muon_block_problem* probs, int nprobs, float a, float b, float c, int steps, float eta,
                      float decay, float scale, void* workspace, size_t ws_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * 8-bit integer matrices with a scale for each row, and their products: what
+ * trained weights (a scale for each output channel) answer with, for tokens
+ * quantised on the way (a scale for each token).
+ *
+ * Format.  A matrix [rows][cols] is a pair of device arrays:
+ *   q  codes, int8, row-major with a row pitch ldq (a multiple of 16, at least
+ *      cols rounded up to MUON_INT8_STEP).  Columns from cols up to the next
+ *      multiple of 64 hold zeros.
+ *   s  fp32 scales, one per row.  Entry (i, j) has the value q[i][j] s[i].
+ *
+ * int8_quantize  x [rows][cols] (row pitch ldx entries, F32 or BF16) -> (q, s):
+ *                s[i] = max_j |x[i][j]| * (1 / 127), two fp32 factors and their
+ *                product rounded to fp32, and at least 2^-126;
+ *                q = x / s of the exact quotient, rounded to nearest, ties to
+ *                even (so |q| <= 127).  An infinity or NaN in a row makes its
+ *                scale NaN and its codes 0: what is multiplied with it is NaN.
+ * int8_gemm      C[i][j] = sa[i] sb[j] sum_k A[i][k] B[j][k], A [m][K], B [n][K],
+ *                both with K columns stored (a multiple of 64, at most
+ *                MUON_INT8_MAX_K), C [m][n] with row pitch ldc, F32 or BF16.  The
+ *                sum is exact in int32 for any codes; it is rounded to fp32,
+ *                times the fp32 product of the scales, and rounded to C.
+ * int8_glu       H = act(g) * u with g = sa sg (A Bg^T) and u = sa su (A Bu^T) as
+ *                int8_gemm computes them in fp32: the gated block below on 8-bit
+ *                operands.  Bg and Bu [n][K] have one row pitch ldb.
+ *   workspace    int8_gemm_workspace_bytes / int8_glu_workspace_bytes(m, n, K)
+ *                bytes (may be 0), 16-byte aligned; contents on entry do not
+ *                matter.  Calls that share one must not overlap in time.
+ * K = 0 gives zeros.  lda and ldb are multiples of 16 under 2^24.  m, n, rows and
+ * cols are at most MUON_GLU_MAX_SIDE (MUON_EINVAL).  Pointers 16-byte aligned
+ * (MUON_EALIGN); unknown dtypes give MUON_EDTYPE, unknown activations
+ * MUON_EINVAL, a missing or short workspace MUON_EWORKSPACE.  A zero rows, cols,
+ * m or n is MUON_OK and launches nothing.  Outputs may not overlap inputs.
+ * ------------------------------------------------------------------------- */
+#define MUON_INT8_STEP 64
+#define MUON_INT8_MAX_K 131008
+#define MUON_GLU_MAX_SIDE 4194240
+
+enum muon_act {
+  MUON_ACT_SILU = 0,      /* x / (1 + exp(-x))                                  */
+  MUON_ACT_GELU = 1,      /* x P(X <= x), X normal                              */
+  MUON_ACT_GELU_TANH = 2, /* x (1 + tanh(sqrt(2 / pi) (x + 0.044715 x^3))) / 2  */
+  MUON_ACT_RELU = 3       /* max(x, 0); its slope at 0 is 0                     */
+};
+
+int int8_quantize(const void* x, int x_dtype, int64_t rows, int64_t cols, int64_t ldx, void* q, int64_t ldq, float* s,
+                  void* stream);
+size_t int8_gemm_workspace_bytes(int64_t m, int64_t n, int64_t K);
+int int8_gemm(const void* A, int64_t lda, const float* sa, const void* B, int64_t ldb, const float* sb, void* C,
+              int c_dtype, int64_t ldc, int64_t m, int64_t n, int64_t K, void* workspace, size_t ws_bytes, void* stream);
+size_t int8_glu_workspace_bytes(int64_t m, int64_t n, int64_t K);
+int int8_glu(const void* A, int64_t lda, const float* sa, const void* Bg, const float* sg, const void* Bu, const float* su,
+             int64_t ldb, int act, void* H, int h_dtype, int64_t ldh, int64_t m, int64_t n, int64_t K, void* workspace,
+             size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * The gated feed-forward block in bf16: h = act(x Wg^T) * (x Wu^T) for tokens
+ * x [tokens][in] and weights Wg, Wu [out][in], and its gradients.  Every matrix
+ * is BF16 with rows of any pitch (in entries, at least the row's length); the
+ * two weights share one pitch, and so do G and U, dG and dU, and Mg and Mu.
+ *
+ * glu_forward      H = act(g) * u with g = x Wg^T, u = x Wu^T: both products, the
+ *                  activation and their product in one kernel, from fp32 sums, H
+ *                  rounded once.  G and U (both or neither) receive g and u, each
+ *                  rounded once, for the backward.
+ * glu_backward     dG = dH * U * act'(G), dU = dH * act(G), each computed in fp32
+ *                  and rounded once; H (may be NULL) = act(G) * U again, for the
+ *                  gradient of what reads it.  dX (may be NULL) = dG Wg + dU Wu,
+ *                  of dG and dU as stored, summed in fp32 and rounded once; Wg, Wu
+ *                  and the workspace are used for dX only.  dG, dU and H may each
+ *                  be one of dH, G or U itself (same pointer and pitch).
+ * glu_weight_grad  Mg <- beta Mg + alpha dG^T x, Mu <- beta Mu + alpha dU^T x, Mg
+ *                  and Mu [out][in] F32 or BF16: the weight gradients straight
+ *                  into the momentum.  Sums are fp32 over all tokens, the result
+ *                  is rounded once.  With beta = 0, Mg and Mu are not read.
+ *   workspace      the matching *_workspace_bytes(tokens, out, in) bytes (may be
+ *                  0), 16-byte aligned; contents on entry do not matter.  Calls
+ *                  that share one must not overlap in time.
+ * A product without terms (in = 0, out = 0 or tokens = 0 on the summed side) gives
+ * zeros, or beta M.  Rows that start at 16 bytes (pitches, and sides that a product
+ * walks across, multiples of 8) take the fast path; others are right and slower.
+ * Sides are at most MUON_GLU_MAX_SIDE, the pitches of x, Wg, Wu, dG and dU under
+ * 2^23 entries (MUON_EINVAL).  Pointers 16-byte aligned (MUON_EALIGN); unknown
+ * dtypes give MUON_EDTYPE, unknown activations MUON_EINVAL, a missing or short
+ * workspace MUON_EWORKSPACE.  Where there is nothing to write the call is MUON_OK
+ * and launches nothing.  Outputs may not overlap inputs but where said above.
+ * ------------------------------------------------------------------------- */
+size_t glu_forward_workspace_bytes(int64_t tokens, int64_t out, int64_t in);
+int glu_forward(const void* X, int64_t ldx, const void* Wg, const void* Wu, int64_t ldw, int act, void* H, int64_t ldh, void* G,
+                void* U, int64_t ldg, int64_t tokens, int64_t out, int64_t in, void* workspace, size_t ws_bytes, void* stream);
+size_t glu_backward_workspace_bytes(int64_t tokens, int64_t out, int64_t in);
+int glu_backward(const void* dH, int64_t lddh, const void* G, const void* U, int64_t ldg, int act, void* dG, void* dU, int64_t ldd,
+                 void* H, int64_t ldh, const void* Wg, const void* Wu, int64_t ldw, void* dX, int64_t lddx, int64_t tokens,
+                 int64_t out, int64_t in, void* workspace, size_t ws_bytes, void* stream);
+size_t glu_weight_grad_workspace_bytes(int64_t tokens, int64_t out, int64_t in);
+int glu_weight_grad(const void* dG, const void* dU, int64_t ldd, const void* X, int64_t ldx, void* Mg, void* Mu, int m_dtype, int64_t ldm,
+                    int64_t tokens, int64_t out, int64_t in, float alpha, float beta, void* workspace, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

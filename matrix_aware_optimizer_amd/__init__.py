@@ -22,3 +22,7 @@ from ._abi import fp8_quantize, fp8_scale_shape  # noqa: F401
 from ._abi import MUON_BLOCKS_MAX_SHORT, PreparedNSBlocks, ns_blocks, ns_blocks_update  # noqa: F401
 from ._abi import ns_blocks_workspace_bytes  # noqa: F401
 from .blocklinear import BlockLinear  # noqa: F401
+from ._abi import MUON_GLU_MAX_SIDE, MUON_INT8_MAX_K, MUON_INT8_STEP, int8_buffers, int8_gemm  # noqa: F401
+from ._abi import int8_gemm_workspace_bytes, int8_glu, int8_glu_workspace_bytes, int8_quantize  # noqa: F401
+from ._abi import glu_backward, glu_backward_workspace_bytes, glu_forward, glu_forward_workspace_bytes  # noqa: F401
+from ._abi import glu_weight_grad, glu_weight_grad_workspace_bytes  # noqa: F401

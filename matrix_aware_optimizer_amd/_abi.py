@@ -98,6 +98,23 @@ SIGNATURES = {
     "ns_blocks": (_c_int, [_c_void_p, _c_int, _c_float, _c_float, _c_float, _c_int, _c_void_p, _c_size, _c_void_p]),
     "ns_blocks_update": (_c_int, [_c_void_p, _c_int, _c_float, _c_float, _c_float, _c_int, _c_float, _c_float,
                                   _c_float, _c_void_p, _c_size, _c_void_p]),
+    "int8_quantize": (_c_int, [_c_void_p, _c_int, _c_i64, _c_i64, _c_i64, _c_void_p, _c_i64, _c_void_p, _c_void_p]),
+    "int8_gemm_workspace_bytes": (_c_size, [_c_i64, _c_i64, _c_i64]),
+    "int8_gemm": (_c_int, [_c_void_p, _c_i64, _c_void_p, _c_void_p, _c_i64, _c_void_p, _c_void_p, _c_int, _c_i64,
+                           _c_i64, _c_i64, _c_i64, _c_void_p, _c_size, _c_void_p]),
+    "int8_glu_workspace_bytes": (_c_size, [_c_i64, _c_i64, _c_i64]),
+    "int8_glu": (_c_int, [_c_void_p, _c_i64, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_i64, _c_int,
+                          _c_void_p, _c_int, _c_i64, _c_i64, _c_i64, _c_i64, _c_void_p, _c_size, _c_void_p]),
+    "glu_forward_workspace_bytes": (_c_size, [_c_i64, _c_i64, _c_i64]),
+    "glu_forward": (_c_int, [_c_void_p, _c_i64, _c_void_p, _c_void_p, _c_i64, _c_int, _c_void_p, _c_i64, _c_void_p,
+                             _c_void_p, _c_i64, _c_i64, _c_i64, _c_i64, _c_void_p, _c_size, _c_void_p]),
+    "glu_backward_workspace_bytes": (_c_size, [_c_i64, _c_i64, _c_i64]),
+    "glu_backward": (_c_int, [_c_void_p, _c_i64, _c_void_p, _c_void_p, _c_i64, _c_int, _c_void_p, _c_void_p, _c_i64,
+                              _c_void_p, _c_i64, _c_void_p, _c_void_p, _c_i64, _c_void_p, _c_i64, _c_i64, _c_i64,
+                              _c_i64, _c_void_p, _c_size, _c_void_p]),
+    "glu_weight_grad_workspace_bytes": (_c_size, [_c_i64, _c_i64, _c_i64]),
+    "glu_weight_grad": (_c_int, [_c_void_p, _c_void_p, _c_i64, _c_void_p, _c_i64, _c_void_p, _c_void_p, _c_int, _c_i64,
+                                 _c_i64, _c_i64, _c_i64, _c_float, _c_float, _c_void_p, _c_size, _c_void_p]),
 }
 
 _LIB: Optional[ctypes.CDLL] = None
@@ -806,3 +823,229 @@ def ns_blocks_update(problems, a: float, b: float, c: float, steps: int, eta: fl
     if len(problems) > 0:
         workspace = _workspace_on(ns_blocks_workspace_bytes(problems), problems[0][0], workspace, stream)
         PreparedNSBlocks(problems, a, b, c, steps, eta, decay, scale, workspace)(stream)
+
+
+# ---------------------------------------------------------------------------
+# 8-bit integer matrices with a scale for each row
+# ---------------------------------------------------------------------------
+
+MUON_INT8_STEP = 64
+MUON_INT8_MAX_K = 131008
+MUON_GLU_MAX_SIDE = 4194240
+_ACTS = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "relu": 3}
+
+
+def _act_code(act: str) -> int:
+    code = _ACTS.get(act)
+    if code is None:
+        raise ValueError(f"act must be one of {', '.join(_ACTS)}")
+    return code
+
+
+def _same_device(first: torch.Tensor, *rest: Optional[torch.Tensor]) -> None:
+    """All tensors on one device, the current one, whose stream and pool the call uses."""
+    where = first.get_device()
+    for t in rest:
+        if t is not None and t.get_device() != where:
+            raise ValueError("all tensors must be on one device")
+    if where >= 0 and where != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on cuda:{where}, which is not the current device (use torch.cuda.device)")
+
+
+def _matrix(t: torch.Tensor, dtype: torch.dtype, rows: int, cols: int, name: str) -> Tuple[int, int]:
+    """(pointer, row pitch) of a rows x cols device matrix of one type."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}")
+    if t.shape != (rows, cols):
+        raise ValueError(f"{name} must be [{rows}, {cols}]")
+    ptr, ld = _rows2(t, name)
+    return ptr, ld if ld > cols else cols
+
+
+def _pair(a: torch.Tensor, b: torch.Tensor, dtype: torch.dtype, rows: int, cols: int, names: str) -> Tuple[int, int, int]:
+    """(pointers, common row pitch) of two rows x cols matrices of one type."""
+    ap, lda = _matrix(a, dtype, rows, cols, f"each of {names}")
+    bp, ldb = _matrix(b, dtype, rows, cols, f"each of {names}")
+    if lda != ldb:
+        raise ValueError(f"{names} must have one row pitch")
+    return ap, bp, lda
+
+
+def _space(need: int, like: torch.Tensor, workspace: Optional[torch.Tensor], stream):
+    """(workspace that is kept alive, pointer, bytes) for a call that needs ``need`` bytes."""
+    if need == 0:
+        return None, None, 0
+    workspace = _workspace_on(need, like, workspace, stream)
+    return workspace, _dev(workspace, "workspace"), workspace.numel() * workspace.element_size()
+
+
+def int8_buffers(rows: int, cols: int, device="cuda") -> Tuple[torch.Tensor, torch.Tensor]:
+    """Uninitialised (codes [rows, cols rounded up to 64], scales [rows]) for a rows x cols matrix."""
+    q = torch.empty((rows, _ceil_to(cols, MUON_INT8_STEP)), dtype=torch.int8, device=device)
+    return q, torch.empty(rows, dtype=torch.float32, device=device)
+
+
+def _int8_operand(q: torch.Tensor, s: torch.Tensor, rows: int, cols: int, name: str) -> Tuple[int, int, int]:
+    """(codes, pitch, scales) of an int8 matrix that holds rows x cols."""
+    if q.dtype != torch.int8:
+        raise TypeError(f"{name} must be int8")
+    ptr, ld = _rows2(q, name)
+    held, width = q.shape
+    need = _ceil_to(cols, MUON_INT8_STEP)
+    if held != rows or width < need:
+        raise ValueError(f"{name} must hold {rows} rows of at least {need} codes")
+    if s.dtype != torch.float32 or s.shape != (rows,):
+        raise ValueError(f"the scales of {name} must be float32 of shape ({rows},)")
+    if rows <= 1 or width == 0:     # the pitch is not used, the library wants a multiple of 16
+        ld = _ceil_to(max(width, need), 16)
+    return ptr, ld, _dev(s, f"the scales of {name}")
+
+
+def int8_quantize(x: torch.Tensor, q: torch.Tensor, s: torch.Tensor, stream=None) -> None:
+    """Codes and scales of ``x`` [rows, cols] into (q, s): ``x / s`` rounded to nearest even, s = max |row| * (1 / 127)."""
+    _same_device(x, q, s)
+    xp, ldx = _rows2(x, "x")
+    rows, cols = x.shape
+    qp, ldq, sp = _int8_operand(q, s, rows, cols, "q")
+    status = lib().int8_quantize(xp, dtype_code(x), rows, cols, ldx if ldx > cols else cols, qp, ldq, sp, _stream(stream))
+    if status:
+        _check("int8_quantize", status)
+
+
+@functools.lru_cache(maxsize=1024)
+def int8_gemm_workspace_bytes(m: int, n: int, K: int) -> int:
+    return int(lib().int8_gemm_workspace_bytes(m, n, K))
+
+
+@functools.lru_cache(maxsize=1024)
+def int8_glu_workspace_bytes(m: int, n: int, K: int) -> int:
+    return int(lib().int8_glu_workspace_bytes(m, n, K))
+
+
+def int8_gemm(A: torch.Tensor, sa: torch.Tensor, B: torch.Tensor, sb: torch.Tensor, C: torch.Tensor,
+              workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    """``C = (A B^T) sa sb`` for int8 operands (codes, scales) with K = ``A.shape[1]`` columns; C fp32 or bf16."""
+    _same_device(C, A, sa, B, sb, workspace)
+    m, K = A.shape
+    n, kb = B.shape
+    if kb != K or K % MUON_INT8_STEP or C.shape != (m, n):
+        raise ValueError(f"A is m x K, B n x K and C m x n, K a multiple of {MUON_INT8_STEP}")
+    ap, lda, sap = _int8_operand(A, sa, m, K, "A")
+    bp, ldb, sbp = _int8_operand(B, sb, n, K, "B")
+    cp, ldc = _rows2(C, "C")
+    workspace, ws, nbytes = _space(int8_gemm_workspace_bytes(m, n, K), C, workspace, stream)
+    status = lib().int8_gemm(ap, lda, sap, bp, ldb, sbp, cp, dtype_code(C), ldc if ldc > n else n, m, n, K, ws, nbytes,
+                             _stream(stream))
+    if status:
+        _check("int8_gemm", status)
+
+
+def int8_glu(A: torch.Tensor, sa: torch.Tensor, Bg: torch.Tensor, sg: torch.Tensor, Bu: torch.Tensor, su: torch.Tensor,
+             H: torch.Tensor, act: str = "silu", workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    """``H = act(g) * u``, ``g = (A Bg^T) sa sg`` and ``u = (A Bu^T) sa su``, for int8 operands; H fp32 or bf16."""
+    _same_device(H, A, sa, Bg, sg, Bu, su, workspace)
+    m, K = A.shape
+    n, kb = Bg.shape
+    if kb != K or K % MUON_INT8_STEP or Bu.shape != (n, K) or H.shape != (m, n):
+        raise ValueError(f"A is m x K, Bg and Bu n x K and H m x n, K a multiple of {MUON_INT8_STEP}")
+    ap, lda, sap = _int8_operand(A, sa, m, K, "A")
+    gp, ldg, sgp = _int8_operand(Bg, sg, n, K, "Bg")
+    up, ldu, sup = _int8_operand(Bu, su, n, K, "Bu")
+    if ldg != ldu:
+        raise ValueError("Bg and Bu must have one row pitch")
+    hp, ldh = _rows2(H, "H")
+    workspace, ws, nbytes = _space(int8_glu_workspace_bytes(m, n, K), H, workspace, stream)
+    status = lib().int8_glu(ap, lda, sap, gp, sgp, up, sup, ldg, _act_code(act), hp, dtype_code(H), ldh if ldh > n else n, m, n, K,
+                            ws, nbytes, _stream(stream))
+    if status:
+        _check("int8_glu", status)
+
+
+# ---------------------------------------------------------------------------
+# The gated feed-forward block in bf16
+# ---------------------------------------------------------------------------
+
+@functools.lru_cache(maxsize=1024)
+def glu_forward_workspace_bytes(tokens: int, out: int, inp: int) -> int:
+    return int(lib().glu_forward_workspace_bytes(tokens, out, inp))
+
+
+@functools.lru_cache(maxsize=1024)
+def glu_backward_workspace_bytes(tokens: int, out: int, inp: int) -> int:
+    return int(lib().glu_backward_workspace_bytes(tokens, out, inp))
+
+
+@functools.lru_cache(maxsize=1024)
+def glu_weight_grad_workspace_bytes(tokens: int, out: int, inp: int) -> int:
+    return int(lib().glu_weight_grad_workspace_bytes(tokens, out, inp))
+
+
+def _two_sides(t: torch.Tensor, name: str) -> Tuple[int, int]:
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D")
+    return t.shape
+
+
+def glu_forward(x: torch.Tensor, wg: torch.Tensor, wu: torch.Tensor, h: torch.Tensor, g: Optional[torch.Tensor] = None,
+                u: Optional[torch.Tensor] = None, act: str = "silu", workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    """``h = act(x wg^T) * (x wu^T)`` in bf16; ``g`` and ``u`` (both or neither) receive the two products for the backward."""
+    _same_device(h, x, wg, wu, g, u, workspace)
+    tokens, inp = _two_sides(x, "x")
+    out = _two_sides(wg, "wg")[0]
+    if (g is None) != (u is None):
+        raise ValueError("give g and u or neither")
+    bf = torch.bfloat16
+    xp, ldx = _matrix(x, bf, tokens, inp, "x")
+    gp, up, ldw = _pair(wg, wu, bf, out, inp, "wg and wu")
+    hp, ldh = _matrix(h, bf, tokens, out, "h")
+    sg, su, lds = _pair(g, u, bf, tokens, out, "g and u") if g is not None else (None, None, 0)
+    workspace, ws, nbytes = _space(glu_forward_workspace_bytes(tokens, out, inp), h, workspace, stream)
+    status = lib().glu_forward(xp, ldx, gp, up, ldw, _act_code(act), hp, ldh, sg, su, lds, tokens, out, inp, ws, nbytes,
+                               _stream(stream))
+    if status:
+        _check("glu_forward", status)
+
+
+def glu_backward(dh: torch.Tensor, g: torch.Tensor, u: torch.Tensor, dg: torch.Tensor, du: torch.Tensor,
+                 wg: Optional[torch.Tensor] = None, wu: Optional[torch.Tensor] = None, dx: Optional[torch.Tensor] = None,
+                 h: Optional[torch.Tensor] = None, act: str = "silu", workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    """``dg = dh u act'(g)``, ``du = dh act(g)``; ``dx = dg wg + du wu`` where ``dx`` is given, and ``h`` again where it is.
+
+    dg, du and h may each be dh, g or u itself."""
+    _same_device(dh, g, u, dg, du, wg, wu, dx, h, workspace)
+    tokens, out = _two_sides(dh, "dh")
+    if (wg is None) != (wu is None) or (dx is not None and wg is None):
+        raise ValueError("dx needs wg and wu")
+    bf = torch.bfloat16
+    dhp, lddh = _matrix(dh, bf, tokens, out, "dh")
+    gp, up, ldg = _pair(g, u, bf, tokens, out, "g and u")
+    dgp, dup, ldd = _pair(dg, du, bf, tokens, out, "dg and du")
+    hp, ldh = _matrix(h, bf, tokens, out, "h") if h is not None else (None, 0)
+    inp, wgp, wup, ldw, dxp, lddx, ws, nbytes = 0, None, None, 0, None, 0, None, 0
+    if dx is not None:
+        inp = _two_sides(dx, "dx")[1]
+        wgp, wup, ldw = _pair(wg, wu, bf, out, inp, "wg and wu")
+        dxp, lddx = _matrix(dx, bf, tokens, inp, "dx")
+        workspace, ws, nbytes = _space(glu_backward_workspace_bytes(tokens, out, inp), dx, workspace, stream)
+    status = lib().glu_backward(dhp, lddh, gp, up, ldg, _act_code(act), dgp, dup, ldd, hp, ldh, wgp, wup, ldw, dxp, lddx, tokens,
+                                out, inp, ws, nbytes, _stream(stream))
+    if status:
+        _check("glu_backward", status)
+
+
+def glu_weight_grad(dg: torch.Tensor, du: torch.Tensor, x: torch.Tensor, mg: torch.Tensor, mu: torch.Tensor, alpha: float = 1.0,
+                    beta: float = 0.0, workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    """``mg <- beta mg + alpha dg^T x`` and ``mu <- beta mu + alpha du^T x``, mg and mu fp32 or bf16."""
+    _same_device(mg, mu, dg, du, x, workspace)
+    tokens, out = _two_sides(dg, "dg")
+    inp = _two_sides(x, "x")[1]
+    bf = torch.bfloat16
+    dgp, dup, ldd = _pair(dg, du, bf, tokens, out, "dg and du")
+    xp, ldx = _matrix(x, bf, tokens, inp, "x")
+    code = dtype_code(mg)
+    gp, up, ldm = _pair(mg, mu, mg.dtype, out, inp, "mg and mu")
+    workspace, ws, nbytes = _space(glu_weight_grad_workspace_bytes(tokens, out, inp), mg, workspace, stream)
+    status = lib().glu_weight_grad(dgp, dup, ldd, xp, ldx, gp, up, code, ldm, tokens, out, inp, alpha, beta, ws, nbytes,
+                                   _stream(stream))
+    if status:
+        _check("glu_weight_grad", status)

@@ -1,0 +1,225 @@
+// The gated feed-forward block h = act(x Wg^T) * (x Wu^T) in bf16: forward, gradients of both
+// products, of the input and of the weights.
+//
+//   forward   g = x Wg^T, u = x Wu^T, h = a(g) u
+//   backward  dg = dh u a'(g), du = dh a(g), dx = dg Wg + du Wu
+//   weights   Mg <- beta Mg + alpha dg^T x, Mu <- beta Mu + alpha du^T x
+#include <algorithm>
+
+#include "act.h"
+#include "common.h"
+#include "tile.h"
+
+namespace muon {
+namespace {
+
+using tile::ceil_div;
+using tile::kBf16;
+
+// C <- beta C + alpha sum, one rounding to the stored type; z says which of two outputs
+template <typename TC>
+struct AxpbyOut {
+  using sum_t = float;
+  static constexpr int E = 16 / int(sizeof(TC));
+  TC *C, *C1;
+  int64_t ldc, width;
+  float alpha, beta;
+
+  template <int N> struct Cols {};
+  template <int N> struct Pre { float c[N]; };
+  __device__ __forceinline__ AxpbyOut at(int z) const {
+    AxpbyOut o = *this;
+    if (z) o.C = C1;
+    return o;
+  }
+  template <int N> __device__ __forceinline__ Cols<N> cols(int64_t) const { return {}; }
+  template <int N> __device__ __forceinline__ Pre<N> pre(int64_t row, int64_t col) const {
+    Pre<N> p;
+    if (beta != 0.0f) load_n<N>(C + row * ldc + col, p.c);
+    return p;
+  }
+  template <int N>
+  __device__ __forceinline__ void store(int64_t row, int64_t col, const float (&v)[1][N], const Cols<N>&, const Pre<N>& p) const {
+    float o[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k) o[k] = alpha * v[0][k];
+    if (beta != 0.0f)
+#pragma unroll
+      for (int k = 0; k < N; ++k) o[k] = fmaf(beta, p.c[k], o[k]);
+    store_n<N>(C + row * ldc + col, o);
+  }
+};
+
+struct GradArgs {
+  const bf16_t *dH, *G, *U;
+  bf16_t *dG, *dU, *H;   // H may be null
+  int64_t rows, cols, lddh, ldg, ldd, ldh;
+};
+
+// dg, du and h of N entries; everything is read before anything is written
+template <int ACT, int N>
+__device__ __forceinline__ void gradients(const GradArgs& a, int64_t row, int64_t col) {
+  float dh[N], g[N], u[N], dg[N], du[N], h[N];
+  load_n<N>(a.dH + row * a.lddh + col, dh);
+  load_n<N>(a.G + row * a.ldg + col, g);
+  load_n<N>(a.U + row * a.ldg + col, u);
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    float slope;
+    const float act = activate<true>(ACT, g[k], slope);
+    dg[k] = dh[k] * u[k] * slope;
+    du[k] = dh[k] * act;
+    h[k] = act * u[k];
+  }
+  store_n<N>(a.dG + row * a.ldd + col, dg);
+  store_n<N>(a.dU + row * a.ldd + col, du);
+  if (a.H != nullptr) store_n<N>(a.H + row * a.ldh + col, h);
+}
+
+// Eight columns of one row per thread.  Bound by memory: 6 bytes read and 4 (6 with h) written
+// per entry.
+template <int ACT>
+__global__ __launch_bounds__(256) void glu_gradients_kernel(GradArgs a) {
+  const int64_t per = (a.cols + 7) / 8, t = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  const int64_t row = t / per, col = (t % per) * 8;
+  if (row >= a.rows) return;
+  if (col + 8 <= a.cols) gradients<ACT, 8>(a, row, col);
+  else
+    for (int64_t c = col; c < a.cols; ++c) gradients<ACT, 1>(a, row, c);
+}
+
+// A product on tiles: the sizes of `plan`, through the DMA where rows start at 16 bytes
+template <bool AT, bool BT, bool DUAL, class Out>
+int launch_tiled(const tile::Source& g, const Out& out, const tile::Plan& plan, const tile::Split& sp, bool whole, hipStream_t st) {
+  if (!whole) return tile::launch_sized<tile::Config<kBf16, 128, 128, 64, 64, 4, AT, BT, DUAL>, true>(g, out, sp, st);
+  if constexpr (!AT) {
+    if (plan.kind == tile::kNarrow) return tile::launch_sized<tile::Config<kBf16, 64, 128, 32, 64, 4, AT, BT, DUAL>, false>(g, out, sp, st);
+  }
+  if (plan.kind == tile::kSmall) return tile::launch_sized<tile::Config<kBf16, 128, 128, 64, 64, 4, AT, BT, DUAL>, false>(g, out, sp, st);
+  return tile::launch_tiles<tile::Config<kBf16, 256, 256, 128, 128, 4, AT, BT, DUAL>, false, false>(g, out, sp, st);
+}
+
+bool sides_ok(int64_t tokens, int64_t out, int64_t in) {
+  return tokens >= 0 && out >= 0 && in >= 0 && tokens <= MUON_GLU_MAX_SIDE && out <= MUON_GLU_MAX_SIDE && in <= MUON_GLU_MAX_SIDE;
+}
+bool pitch_ok(int64_t ld, int64_t cols) { return ld >= cols && ld * 2 <= tile::kMaxPitch; }
+bool run8(int64_t v) { return v % 8 == 0; }
+
+tile::Plan forward_plan(int64_t tokens, int64_t out, int64_t in) { return tile::plan_product(tokens, out, in / 32, 2, 1, true); }
+tile::Plan input_plan(int64_t tokens, int64_t out, int64_t in) { return tile::plan_product(tokens, in, 2 * (out / 32), 1, 1, false); }
+tile::Plan weight_plan(int64_t tokens, int64_t out, int64_t in) {
+  return tile::plan_product(out, in, tokens / 32, 1, 2, false, false);
+}
+
+// MUON_OK where the workspace serves `need` bytes
+int workspace_status(const void* workspace, size_t bytes, size_t need) {
+  if (need == 0) return MUON_OK;
+  if (workspace == nullptr || bytes < need) return MUON_EWORKSPACE;
+  return aligned16(workspace) ? MUON_OK : MUON_EALIGN;
+}
+
+}  // namespace
+}  // namespace muon
+
+using namespace muon;
+
+extern "C" {
+
+size_t glu_forward_workspace_bytes(int64_t tokens, int64_t out, int64_t in) {
+  if (!sides_ok(tokens, out, in) || tokens == 0 || out == 0) return 0;
+  return tile::sum_bytes(forward_plan(tokens, out, in), tokens, out, 2, 1);
+}
+
+int glu_forward(const void* X, int64_t ldx, const void* Wg, const void* Wu, int64_t ldw, int act, void* H, int64_t ldh, void* G,
+                void* U, int64_t ldg, int64_t tokens, int64_t out, int64_t in, void* workspace, size_t ws_bytes, void* stream) {
+  if (!sides_ok(tokens, out, in) || !valid_act(act)) return MUON_EINVAL;
+  if (tokens == 0 || out == 0) return MUON_OK;
+  if (H == nullptr || ldh < out || (in > 0 && (X == nullptr || Wg == nullptr || Wu == nullptr))) return MUON_EINVAL;
+  if (!pitch_ok(ldx, in) || !pitch_ok(ldw, in) || (G == nullptr) != (U == nullptr) || (G != nullptr && ldg < out)) return MUON_EINVAL;
+  if (!aligned16(X) || !aligned16(Wg) || !aligned16(Wu) || !aligned16(H) || !aligned16(G) || !aligned16(U)) return MUON_EALIGN;
+  const tile::Plan plan = forward_plan(tokens, out, in);
+  const int ws = workspace_status(workspace, ws_bytes, glu_forward_workspace_bytes(tokens, out, in));
+  if (ws != MUON_OK) return ws;
+  const char* x = static_cast<const char*>(X);
+  const tile::Source g{{x, x}, {static_cast<const char*>(Wg), static_cast<const char*>(Wu)}, ldx * 2, ldw * 2, tokens, out, in, 1};
+  const GluOut<bf16_t, false> o{static_cast<bf16_t*>(H), static_cast<bf16_t*>(G), static_cast<bf16_t*>(U), ldh, ldg, out, act,
+                                nullptr, nullptr, nullptr};
+  const tile::Split sp{plan.parts, 1, workspace, ceil_div(out, 4) * 4};
+  hipStream_t hs = static_cast<hipStream_t>(stream);
+  if (plan.kind == tile::kDirect) return tile::launch_direct<kBf16, 2>(g, o, hs);
+  return launch_tiled<false, false, true>(g, o, plan, sp, run8(ldx) && run8(ldw), hs);
+}
+
+size_t glu_backward_workspace_bytes(int64_t tokens, int64_t out, int64_t in) {
+  if (!sides_ok(tokens, out, in) || tokens == 0 || in == 0) return 0;
+  return tile::sum_bytes(input_plan(tokens, out, in), tokens, in, 1, 1);
+}
+
+int glu_backward(const void* dH, int64_t lddh, const void* G, const void* U, int64_t ldg, int act, void* dG, void* dU, int64_t ldd,
+                 void* H, int64_t ldh, const void* Wg, const void* Wu, int64_t ldw, void* dX, int64_t lddx, int64_t tokens,
+                 int64_t out, int64_t in, void* workspace, size_t ws_bytes, void* stream) {
+  if (!sides_ok(tokens, out, in) || !valid_act(act)) return MUON_EINVAL;
+  const bool input = dX != nullptr && in > 0;
+  if (tokens == 0) return MUON_OK;
+  if (out > 0 && (dH == nullptr || G == nullptr || U == nullptr || dG == nullptr || dU == nullptr)) return MUON_EINVAL;
+  if (lddh < out || ldg < out || !pitch_ok(ldd, out) || (H != nullptr && ldh < out)) return MUON_EINVAL;
+  if (input && (lddx < in || !pitch_ok(ldw, in) || (out > 0 && (Wg == nullptr || Wu == nullptr)))) return MUON_EINVAL;
+  if (!aligned16(dH) || !aligned16(G) || !aligned16(U) || !aligned16(dG) || !aligned16(dU) || !aligned16(H)) return MUON_EALIGN;
+  if (input && (!aligned16(Wg) || !aligned16(Wu) || !aligned16(dX))) return MUON_EALIGN;
+  if (input) {
+    const int ws = workspace_status(workspace, ws_bytes, glu_backward_workspace_bytes(tokens, out, in));
+    if (ws != MUON_OK) return ws;
+  }
+  const int64_t blocks = ceil_div(tokens * ceil_div(out, 8), 256);
+  if (blocks > INT32_MAX) return MUON_EINVAL;
+  hipStream_t hs = static_cast<hipStream_t>(stream);
+  if (out > 0) {
+    const GradArgs a{static_cast<const bf16_t*>(dH), static_cast<const bf16_t*>(G), static_cast<const bf16_t*>(U), static_cast<bf16_t*>(dG),
+                     static_cast<bf16_t*>(dU), static_cast<bf16_t*>(H), tokens, out, lddh, ldg, ldd, ldh};
+    void (*kern)(GradArgs) = act == MUON_ACT_SILU        ? glu_gradients_kernel<MUON_ACT_SILU>
+                             : act == MUON_ACT_GELU      ? glu_gradients_kernel<MUON_ACT_GELU>
+                             : act == MUON_ACT_GELU_TANH ? glu_gradients_kernel<MUON_ACT_GELU_TANH>
+                                                         : glu_gradients_kernel<MUON_ACT_RELU>;
+    launch_kernel(kern, dim3(blocks), dim3(256), 0, hs, a);
+    const int status = launch_status();
+    if (status != MUON_OK) return status;
+  }
+  if (!input) return MUON_OK;
+  const tile::Plan plan = input_plan(tokens, out, in);
+  const tile::Source g{{static_cast<const char*>(dG), static_cast<const char*>(dU)},
+                       {static_cast<const char*>(Wg), static_cast<const char*>(Wu)}, ldd * 2, ldw * 2, tokens, in, out, 2};
+  const AxpbyOut<bf16_t> o{static_cast<bf16_t*>(dX), nullptr, lddx, in, 1.0f, 0.0f};
+  const tile::Split sp{plan.parts, 1, workspace, ceil_div(in, 4) * 4};
+  return launch_tiled<false, true, false>(g, o, plan, sp, run8(ldd) && run8(ldw) && run8(in), hs);
+}
+
+size_t glu_weight_grad_workspace_bytes(int64_t tokens, int64_t out, int64_t in) {
+  if (!sides_ok(tokens, out, in) || out == 0 || in == 0) return 0;
+  return tile::sum_bytes(weight_plan(tokens, out, in), out, in, 1, 2);
+}
+
+int glu_weight_grad(const void* dG, const void* dU, int64_t ldd, const void* X, int64_t ldx, void* Mg, void* Mu, int m_dtype, int64_t ldm,
+                    int64_t tokens, int64_t out, int64_t in, float alpha, float beta, void* workspace, size_t ws_bytes, void* stream) {
+  if (!sides_ok(tokens, out, in)) return MUON_EINVAL;
+  if (!valid_dtype(m_dtype)) return MUON_EDTYPE;
+  if (out == 0 || in == 0) return MUON_OK;
+  if (Mg == nullptr || Mu == nullptr || ldm < in || (tokens > 0 && (dG == nullptr || dU == nullptr || X == nullptr))) return MUON_EINVAL;
+  if (!pitch_ok(ldd, out) || !pitch_ok(ldx, in)) return MUON_EINVAL;
+  if (!aligned16(dG) || !aligned16(dU) || !aligned16(X) || !aligned16(Mg) || !aligned16(Mu)) return MUON_EALIGN;
+  const tile::Plan plan = weight_plan(tokens, out, in);
+  const int ws = workspace_status(workspace, ws_bytes, glu_weight_grad_workspace_bytes(tokens, out, in));
+  if (ws != MUON_OK) return ws;
+  const char* x = static_cast<const char*>(X);
+  const tile::Source g{{static_cast<const char*>(dG), static_cast<const char*>(dU)}, {x, x}, ldd * 2, ldx * 2, out, in, tokens, 1};
+  const tile::Split sp{plan.parts, 2, workspace, ceil_div(in, 4) * 4};
+  const bool whole = run8(ldd) && run8(ldx) && run8(out) && run8(in);
+  hipStream_t hs = static_cast<hipStream_t>(stream);
+  if (m_dtype == MUON_F32) {
+    const AxpbyOut<float> o{static_cast<float*>(Mg), static_cast<float*>(Mu), ldm, in, alpha, beta};
+    return launch_tiled<true, true, false>(g, o, plan, sp, whole, hs);
+  }
+  const AxpbyOut<bf16_t> o{static_cast<bf16_t*>(Mg), static_cast<bf16_t*>(Mu), ldm, in, alpha, beta};
+  return launch_tiled<true, true, false>(g, o, plan, sp, whole, hs);
+}
+
+}  // extern "C"

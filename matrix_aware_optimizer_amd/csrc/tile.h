@@ -1,0 +1,684 @@
+// Products C = A B^T on matrix cores for the gated block (bf16) and the 8-bit integer
+// products (gfx950, wave64): one tile unit for every operand layout, and a kernel for few
+// rows.  What happens to a sum (scales, activation, momentum) is an `Out` of the caller.
+//
+// Operands.  A step of the contraction is 64 bytes of every row: 32 bf16 or 64 int8 values.
+//   rows      [row][k], k contiguous.  LDS: 64-byte rows of four 16-byte chunks, chunk c of
+//             row r at slot c ^ ((r / 4) % 4).
+//   k-major   [k][row] (bf16 only), rows contiguous along the tile's side.  LDS: 32 k-rows of
+//             2 x side bytes, chunk c of k-row k at slot c ^ (4 (k % 4)), read transposed by
+//             ds_read_b64_tr_b16: lane i of 16 gets the four k-values of column i.
+// Both put the k-values 8 (2 p + h) .. + 7 of a step (int8: 16 of them) into lane half h of
+// matrix instruction p, so operands of different layouts go together.
+//
+// Unit.  BM x BN of C by (BM / WM) (BN / WN) waves.  A ring of S stages in LDS is filled by
+// global -> LDS DMA, 16 bytes per lane.  Per step: wait until this wave's copies of the next
+// stage have landed, s_barrier (everybody's have, and everybody is done with the stage
+// before), then multiply this step's operands, and between the matrix instructions read the
+// next step's from LDS and start the copy S - 1 steps ahead.
+//   DUAL      the tile's columns are halves of two matrices B[0], B[1]: in every wave's WN the
+//             first half are columns of B[0], the second the same columns of B[1], so that one
+//             lane holds both sums of an output.
+//   segments  the contraction runs over (A[0], B[0]) and then (A[1], B[1]).
+//   masked    steps that the DMA cannot copy (the last one of a K that is not whole steps, and
+//             every step where rows do not start at 16 bytes) go through registers, with zeros
+//             past the ends.
+#pragma once
+
+#include <algorithm>
+
+#include "common.h"
+#include "gemm.h"
+
+namespace muon {
+namespace tile {
+
+typedef int i32x4_t __attribute__((ext_vector_type(4)));
+typedef int i32x16_t __attribute__((ext_vector_type(16)));
+
+enum Kind { kBf16, kI8 };
+
+template <int KIND> struct Math;
+template <> struct Math<kBf16> {
+  using acc16_t = f32x16_t;   // 32 x 32 block
+  using acc4_t = f32x4_t;     // 16 x 16 block
+  using sum_t = float;
+  static constexpr int kBytes = 2;
+  __device__ __forceinline__ static acc16_t mma32(const u32x4_t& a, const u32x4_t& b, const acc16_t& c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
+  }
+  __device__ __forceinline__ static acc4_t mma16(const u32x4_t& a, const u32x4_t& b, const acc4_t& c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
+  }
+};
+template <> struct Math<kI8> {
+  using acc16_t = i32x16_t;
+  using acc4_t = i32x4_t;
+  using sum_t = int;
+  static constexpr int kBytes = 1;
+  __device__ __forceinline__ static acc16_t mma32(const u32x4_t& a, const u32x4_t& b, const acc16_t& c) {
+    return __builtin_amdgcn_mfma_i32_32x32x32_i8(__builtin_bit_cast(i32x4_t, a), __builtin_bit_cast(i32x4_t, b), c, 0, 0, 0);
+  }
+  __device__ __forceinline__ static acc4_t mma16(const u32x4_t& a, const u32x4_t& b, const acc4_t& c) {
+    return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4_t, a), __builtin_bit_cast(i32x4_t, b), c, 0, 0, 0);
+  }
+};
+
+__host__ __device__ inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+struct Source {
+  const char* A[2];
+  const char* B[2];
+  int64_t lda, ldb;   // pitches in bytes
+  int64_t m, n, K;    // n: columns of one B
+  int segs;           // segments of the contraction (1 or 2)
+};
+
+template <int KIND_, int BM_, int BN_, int WM_, int WN_, int S_, bool AT_, bool BT_, bool DUAL_>
+struct Config {
+  static constexpr int KIND = KIND_, BM = BM_, BN = BN_, WM = WM_, WN = WN_, S = S_;
+  static constexpr bool AT = AT_, BT = BT_, DUAL = DUAL_;
+  static constexpr int NB = DUAL ? 2 : 1, COLS = BN / NB;   // columns of C
+  static constexpr int W = (BM / WM) * (BN / WN), NT = W * kWave;
+  static constexpr int FM = WM / 32, FN = WN / 32;
+  static constexpr int A_BYTES = BM * 64, B_BYTES = BN * 64, STAGE = A_BYTES + B_BYTES;
+  static constexpr int LDW = WN + 4;                        // row pitch of the epilogue's slab, in floats
+  static constexpr int LDS_BYTES = S * STAGE > W * 32 * LDW * 4 ? S * STAGE : W * 32 * LDW * 4;
+  static constexpr int A_DMA = A_BYTES / 1024 / W, B_DMA = B_BYTES / 1024 / W, D = A_DMA + B_DMA;
+  static constexpr int CHUNKS = STAGE / 16 / NT;            // 16-byte chunks per thread of a masked step
+  static_assert(A_BYTES % (1024 * W) == 0 && B_BYTES % (1024 * W) == 0, "DMA split");
+  static_assert(S >= 3 && D * (S - 2) <= 63 && LDS_BYTES <= 160 * 1024, "ring");
+  static_assert((!AT || (BM >= 128 && KIND == kBf16)) && (!BT || (BN >= 128 && KIND == kBf16)), "k-major rows of 256 bytes or more");
+  static_assert(!DUAL || (!BT && WN >= 64), "gate and up columns in one wave");
+};
+
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+// 16 bytes per lane from base + off to LDS bytes [lds_addr + 16 * lane), with the wait state
+// that a load to LDS needs after a scalar write of M0
+__device__ __forceinline__ void dma16_at(const char* base, uint32_t off, uint32_t lds_addr) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base),
+               "s"(__builtin_amdgcn_readfirstlane(lds_addr))
+               : "memory", "m0");
+}
+#pragma clang diagnostic pop
+
+// a pointer that is the same in every lane, in scalar registers
+__device__ __forceinline__ const char* scalar(const char* p) {
+  const uint64_t v = reinterpret_cast<uint64_t>(p);
+  const uint32_t lo = __builtin_amdgcn_readfirstlane(uint32_t(v)), hi = __builtin_amdgcn_readfirstlane(uint32_t(v >> 32));
+  return reinterpret_cast<const char*>((uint64_t(hi) << 32) | lo);
+}
+
+// This wave's copies but the last N have landed and all its LDS reads are done, then all
+// waves meet: what lands next may overwrite the stage that was read before.
+template <int N>
+__device__ __forceinline__ void ring_barrier() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
+// 16 bytes of bf16 values at p, of which `left` lie inside the matrix: zeros past them
+__device__ __forceinline__ u32x4_t masked16(const bf16_t* p, int64_t left) {
+  u32x4_t r = {0, 0, 0, 0};
+  if (left >= 8) {
+    const uint4 v = load16(p);
+    r = u32x4_t{v.x, v.y, v.z, v.w};
+  } else if (left > 0) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t lo = 2 * j < left ? p[2 * j] : 0u, hi = 2 * j + 1 < left ? p[2 * j + 1] : 0u;
+      r[j] = lo | (hi << 16);
+    }
+  }
+  return r;
+}
+
+// One tile at rows m0 and columns n0 over steps [s0, s1) of the contraction's whole steps
+// (MASKED: of all its steps, all through registers); `tail`: then the last, partial step of
+// every segment.
+template <class C_, bool MASKED, class Out>
+__device__ __forceinline__ void unit(const Source& g, int64_t m0, int64_t n0, int s0, int s1, bool tail, const Out& out, char* lds) {
+  using M_ = Math<C_::KIND>;
+  constexpr int BM = C_::BM, BN = C_::BN, WM = C_::WM, WN = C_::WN, S = C_::S, FM = C_::FM, FN = C_::FN;
+  constexpr int PER_STEP = 64 / M_::kBytes;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int fr = lane & 31, h = lane >> 5;
+  const int wm0 = (wave / (BN / WN)) * WM, wn0 = (wave % (BN / WN)) * WN;
+  const int per = __builtin_amdgcn_readfirstlane(int(MASKED ? (g.K + PER_STEP - 1) / PER_STEP : g.K / PER_STEP));
+  // column of C of B's LDS row (or k-major column) r, and which B it is of
+  auto col_of = [](int r) { return C_::DUAL ? (r / WN) * (WN / 2) + r % (WN / 2) : r; };
+  auto is_up = [](int r) { return C_::DUAL && r % WN >= WN / 2; };
+  // rows past the matrix read its last row; what they compute is not stored
+  const int mlast = int(min(g.m - 1 - m0, int64_t(BM - 1))), nlast = int(min(g.n - 1 - n0, int64_t(C_::COLS - 1)));
+
+  typename M_::acc16_t acc[FM][FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) acc[i][j][v] = 0;
+
+  struct Frags {
+    u32x4_t a[FM][2], b[FN][2];
+  };
+  // where a lane's operands lie in a stage
+  constexpr int ROW_A = 2 * BM, ROW_B = 2 * BN;   // bytes of a k-row
+  int a_at[C_::AT ? FM : 2], b_at[C_::BT ? FN : 2];
+  const int tq = lane & 3, tj = (lane >> 2) & 3, ts = (lane >> 4) & 1;
+  if constexpr (C_::AT) {
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+      a_at[i] = (8 * h + tj) * ROW_A + ((((wm0 >> 3) + 4 * i + 2 * ts + (tq >> 1)) ^ (4 * tj)) << 4) + (tq & 1) * 8;
+  } else {
+    a_at[0] = gemm::krow_off(wm0 + fr, h);
+    a_at[1] = gemm::krow_off(wm0 + fr, 2 + h);
+  }
+  if constexpr (C_::BT) {
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+      b_at[j] = C_::A_BYTES + (8 * h + tj) * ROW_B + ((((wn0 >> 3) + 4 * j + 2 * ts + (tq >> 1)) ^ (4 * tj)) << 4) + (tq & 1) * 8;
+  } else {
+    b_at[0] = C_::A_BYTES + gemm::krow_off(wn0 + fr, h);
+    b_at[1] = C_::A_BYTES + gemm::krow_off(wn0 + fr, 2 + h);
+  }
+  constexpr int READS = 2 * (FM + FN);
+  auto read_one = [&](int q, const char* st, Frags& f) __attribute__((always_inline)) {
+    // the operands of the first matrix instructions come first: phase 0 of B and A, then phase 1
+    const int p = q / (FM + FN), k = q % (FM + FN);
+    if (k < FN) {
+      if constexpr (C_::BT) f.b[k][p] = gemm::read_tr_pair(st + b_at[k] + 16 * p * ROW_B, st + b_at[k] + (16 * p + 4) * ROW_B);
+      else f.b[k][p] = *reinterpret_cast<const u32x4_t*>(st + b_at[p] + 2048 * k);
+    } else {
+      const int i = k - FN;
+      if constexpr (C_::AT) f.a[i][p] = gemm::read_tr_pair(st + a_at[i] + 16 * p * ROW_A, st + a_at[i] + (16 * p + 4) * ROW_A);
+      else f.a[i][p] = *reinterpret_cast<const u32x4_t*>(st + a_at[p] + 2048 * i);
+    }
+  };
+  // one step's products; `between(n)` is what the wave issues after matrix instruction n
+  constexpr int N = 2 * FM * FN;
+  auto mma = [&](const Frags& f, auto&& between) __attribute__((always_inline)) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const int p = n / (FM * FN), i = n % (FM * FN) / FN, j = n % FN;
+      acc[i][j] = M_::mma32(f.b[j][p], f.a[i][p], acc[i][j]);
+      between(n);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+
+  if constexpr (!MASKED) {
+    // sources of this wave's copies
+    uint32_t a_off[C_::A_DMA], b_off[C_::B_DMA];
+#pragma unroll
+    for (int i = 0; i < C_::A_DMA; ++i) {
+      const int b = wave * C_::A_DMA + i;
+      if constexpr (C_::AT) {
+        constexpr int RC = BM / 8, RB = 64 / RC;
+        const int r = RB * b + lane / RC, c = (lane % RC) ^ (4 * (r & 3));
+        a_off[i] = uint32_t(r) * uint32_t(g.lda) + (min(c, (mlast + 1) / 8 - 1) << 4);
+      } else {
+        const int r = 16 * b + (lane >> 2);
+        a_off[i] = uint32_t(min(r, mlast)) * uint32_t(g.lda) + (((lane & 3) ^ ((r >> 2) & 3)) << 4);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < C_::B_DMA; ++i) {
+      const int b = wave * C_::B_DMA + i;
+      if constexpr (C_::BT) {
+        constexpr int RC = BN / 8, RB = 64 / RC;
+        const int r = RB * b + lane / RC, c = (lane % RC) ^ (4 * (r & 3));
+        b_off[i] = uint32_t(r) * uint32_t(g.ldb) + (min(c, (nlast + 1) / 8 - 1) << 4);
+      } else {
+        const int r = 16 * b + (lane >> 2);
+        b_off[i] = uint32_t(min(col_of(r), nlast)) * uint32_t(g.ldb) + (((lane & 3) ^ ((r >> 2) & 3)) << 4);
+      }
+    }
+    const int64_t a_start = C_::AT ? m0 * 2 : m0 * g.lda, b_start = C_::BT ? n0 * 2 : n0 * g.ldb;
+    const int64_t a_step = C_::AT ? 32 * g.lda : 64, b_step = C_::BT ? 32 * g.ldb : 64;
+    const uint32_t lds_base =
+        static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char*)lds));
+    const int nk = s1 - s0;
+    auto issue_one = [&](int q, int kt, uint32_t off) __attribute__((always_inline)) {
+      const int seg = kt >= per ? 1 : 0;
+      const int64_t k = kt - seg * per;
+      const uint32_t st = lds_base + off;
+      if (q < C_::A_DMA) {
+        dma16_at(scalar((seg ? g.A[1] : g.A[0]) + a_start + k * a_step), a_off[q], st + (wave * C_::A_DMA + q) * 1024);
+      } else {
+        const int b = q - C_::A_DMA;
+        const bool second = C_::DUAL ? is_up(16 * (wave * C_::B_DMA + b)) : seg != 0;
+        dma16_at(scalar((second ? g.B[1] : g.B[0]) + b_start + k * b_step), b_off[b], st + C_::A_BYTES + (wave * C_::B_DMA + b) * 1024);
+      }
+    };
+    auto ring_next = [](uint32_t o) {
+      o += C_::STAGE;
+      return o == uint32_t(S * C_::STAGE) ? 0u : o;
+    };
+    if (nk > 0) {
+#pragma unroll
+      for (int s = 0; s < S - 1; ++s)
+        if (s < nk)
+#pragma unroll
+          for (int q = 0; q < C_::D; ++q) issue_one(q, s0 + s, uint32_t(s) * C_::STAGE);
+      if (nk >= S - 1) ring_barrier<C_::D * (S - 2)>();
+      else ring_barrier<0>();
+      Frags f0, f1;
+#pragma unroll
+      for (int q = 0; q < READS; ++q) read_one(q, lds, f0);
+      uint32_t o_cur = 0, o_iss = uint32_t(S - 1) * C_::STAGE;
+      int it = 0;
+      constexpr int RPM = (READS + N * 3 / 4 - 1) / (N * 3 / 4);   // reads per MFMA, done after three quarters of them
+      auto steady = [&](Frags& cur, Frags& nxt) __attribute__((always_inline)) {
+        const char* st = lds + ring_next(o_cur);
+        ring_barrier<C_::D * (S - 3)>();
+        mma(cur, [&](int n) __attribute__((always_inline)) {
+#pragma unroll
+          for (int r = 0; r < RPM; ++r)
+            if (RPM * n + r < READS) read_one(RPM * n + r, st, nxt);
+#pragma unroll
+          for (int q = 0; q < C_::D; ++q)
+            if (q * N / C_::D == n) issue_one(q, s0 + it + S - 1, o_iss);
+        });
+        o_cur = ring_next(o_cur);
+        o_iss = ring_next(o_iss);
+        ++it;
+      };
+      auto drain = [&](Frags& cur, Frags& nxt) __attribute__((always_inline)) {
+        if (it + 1 < nk) {
+          ring_barrier<0>();
+          const char* st = lds + ring_next(o_cur);
+#pragma unroll
+          for (int q = 0; q < READS; ++q) read_one(q, st, nxt);
+        }
+        mma(cur, [](int) {});
+        o_cur = ring_next(o_cur);
+        ++it;
+      };
+      while (it + S < nk) {   // two steps that both still copy a stage
+        steady(f0, f1);
+        steady(f1, f0);
+      }
+      if (it + S - 1 < nk) {   // one more copy is due
+        steady(f0, f1);
+        f0 = f1;
+      }
+      while (it < nk) {
+        drain(f0, f1);
+        if (it < nk) drain(f1, f0);
+      }
+    }
+  }
+
+  if constexpr (C_::KIND == kBf16) {
+    // steps through registers: every step of [s0, s1) (MASKED), or the segments' partial last steps
+    const int first = MASKED ? s0 : 0, last = MASKED ? s1 : (tail && g.K % PER_STEP != 0 ? g.segs : 0);
+    u32x4_t held[C_::CHUNKS];
+    auto fetch = [&](int s) __attribute__((always_inline)) {
+      const int seg = MASKED ? (s >= per ? 1 : 0) : s;
+      const int64_t k0 = int64_t(MASKED ? s - seg * per : per) * PER_STEP;
+#pragma unroll
+      for (int i = 0; i < C_::CHUNKS; ++i) {
+        const int idx = threadIdx.x + i * C_::NT;
+        const bool of_a = idx < BM * 4;   // uniform: NT divides both operands' chunks
+        const int x = of_a ? idx : idx - BM * 4;
+        if (of_a) {
+          const int r = C_::AT ? x / (BM / 8) : x >> 2, c = C_::AT ? x % (BM / 8) : x & 3;
+          const int64_t k = k0 + (C_::AT ? r : 8 * c), row = m0 + (C_::AT ? 8 * c : min(r, mlast));
+          const char* p = (seg ? g.A[1] : g.A[0]) + (C_::AT ? k * g.lda + row * 2 : row * g.lda + k * 2);
+          held[i] = masked16(reinterpret_cast<const bf16_t*>(p), C_::AT ? (k < g.K ? g.m - row : 0) : g.K - k);
+        } else {
+          const int r = C_::BT ? x / (BN / 8) : x >> 2, c = C_::BT ? x % (BN / 8) : x & 3;
+          const int64_t k = k0 + (C_::BT ? r : 8 * c), row = n0 + (C_::BT ? 8 * c : min(col_of(r), nlast));
+          const char* p = ((C_::DUAL ? is_up(r) : seg != 0) ? g.B[1] : g.B[0]) + (C_::BT ? k * g.ldb + row * 2 : row * g.ldb + k * 2);
+          held[i] = masked16(reinterpret_cast<const bf16_t*>(p), C_::BT ? (k < g.K ? g.n - row : 0) : g.K - k);
+        }
+      }
+    };
+    if (first < last) fetch(first);
+    for (int s = first; s < last; ++s) {
+      __syncthreads();   // everybody is done with the stage
+#pragma unroll
+      for (int i = 0; i < C_::CHUNKS; ++i) {
+        const int idx = threadIdx.x + i * C_::NT;
+        const bool of_a = idx < BM * 4;
+        const int x = of_a ? idx : idx - BM * 4;
+        const bool t = of_a ? C_::AT : C_::BT;
+        const int side = of_a ? BM : BN;
+        const int r = t ? x / (side / 8) : x >> 2, c = t ? x % (side / 8) : x & 3;
+        const int at = (of_a ? 0 : C_::A_BYTES) + (t ? r * 2 * side + ((c ^ (4 * (r & 3))) << 4) : gemm::krow_off(r, c));
+        *reinterpret_cast<u32x4_t*>(lds + at) = held[i];
+      }
+      __syncthreads();
+      if (s + 1 < last) fetch(s + 1);
+      Frags f;
+#pragma unroll
+      for (int q = 0; q < READS; ++q) read_one(q, lds, f);
+      mma(f, [](int) {});
+    }
+  }
+
+  // The tile leaves through LDS, 32 rows at a time and each wave through its own part of the
+  // ring, so that rows are read and written 16 bytes per lane and whole lines at a time.
+  // Accumulator v of a lane: column 8 (v / 4) + 4 h + v % 4 of B's block, row fr of A's.
+  ring_barrier<0>();
+  constexpr int E = Out::E, NB = C_::NB, HALF = WN / NB, LPR = HALF / E, RPP = 64 / LPR, PASSES = 32 / RPP;
+  using sum_t = typename Out::sum_t;
+  sum_t* slab = reinterpret_cast<sum_t*>(lds) + wave * 32 * C_::LDW;
+  const int pr = lane / LPR, pc = (lane % LPR) * E;
+  const int64_t col = n0 + wn0 / NB + pc;
+  typedef sum_t sum4_t __attribute__((ext_vector_type(4)));
+  const typename Out::template Cols<E> cols = out.template cols<E>(col);
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        sum4_t v;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) v[r] = sum_t(acc[i][j][4 * q + r]);
+        *reinterpret_cast<sum4_t*>(slab + fr * C_::LDW + 32 * j + 8 * q + 4 * h) = v;
+      }
+    const int64_t row0 = m0 + wm0 + 32 * i + pr;
+    if (col + E <= out.width) {
+      typename Out::template Pre<E> pre[PASSES];
+#pragma unroll
+      for (int p = 0; p < PASSES; ++p) pre[p] = out.template pre<E>(min(row0 + RPP * p, g.m - 1), col);
+#pragma unroll
+      for (int p = 0; p < PASSES; ++p) {
+        sum_t v[NB][E];
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int k = 0; k < E; k += 4) {
+            const sum4_t x = *reinterpret_cast<const sum4_t*>(slab + (pr + RPP * p) * C_::LDW + b * HALF + pc + k);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[b][k + e] = x[e];
+          }
+        if (row0 + RPP * p < g.m) out.template store<E>(row0 + RPP * p, col, v, cols, pre[p]);
+      }
+    } else {
+      for (int p = 0; p < PASSES; ++p)
+        if (row0 + RPP * p < g.m)
+          for (int k = 0; k < E; ++k)
+            if (col + k < out.width) {
+              sum_t v[NB][1];
+#pragma unroll
+              for (int b = 0; b < NB; ++b) v[b][0] = slab[(pr + RPP * p) * C_::LDW + b * HALF + pc + k];
+              out.template store<1>(row0 + RPP * p, col + k, v, out.template cols<1>(col + k), out.template pre<1>(row0 + RPP * p, col + k));
+            }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Parts of a split contraction
+// ---------------------------------------------------------------------------
+// Unjoined sums of one part: [part][batch][row][b][ldp]
+template <int KIND, int NB>
+struct Partial {
+  using sum_t = typename Math<KIND>::sum_t;
+  static constexpr int E = 4;
+  sum_t* p;
+  int64_t ldp, width;
+  template <int N> struct Cols {};
+  template <int N> struct Pre {};
+  template <int N> __device__ __forceinline__ Cols<N> cols(int64_t) const { return {}; }
+  template <int N> __device__ __forceinline__ Pre<N> pre(int64_t, int64_t) const { return {}; }
+  template <int N>
+  __device__ __forceinline__ void store(int64_t row, int64_t col, const sum_t (&v)[NB][N], const Cols<N>&, const Pre<N>&) const {
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      sum_t* dst = p + (row * NB + b) * ldp + col;
+      if constexpr (N == 4) {
+        typedef sum_t sum4_t __attribute__((ext_vector_type(4)));
+        *reinterpret_cast<sum4_t*>(dst) = sum4_t{v[b][0], v[b][1], v[b][2], v[b][3]};
+      } else {
+        dst[0] = v[b][0];
+      }
+    }
+  }
+};
+
+constexpr int kGroupRows = 8;   // tile rows walked together, column by column
+
+// tile t of the grid of TM x TN tiles: groups of kGroupRows tile rows, column by column
+__device__ __forceinline__ void tile_at(int64_t t, int64_t TM, int64_t TN, int64_t& tm, int64_t& tn) {
+  const int64_t per = int64_t(kGroupRows) * TN, first = (t / per) * kGroupRows;
+  const int64_t size = min(TM - first, int64_t(kGroupRows)), r = t % per;
+  tm = __builtin_amdgcn_readfirstlane(int(first + r % size));
+  tn = __builtin_amdgcn_readfirstlane(int(r / size));
+}
+
+struct Split {
+  int parts;     // of the contraction
+  int batch;     // products of the launch: A[z] with B[0] (weight gradients), 1 otherwise
+  void* sums;    // [parts][batch][m][NB][ldp]
+  int64_t ldp;
+};
+
+// product z of a batch
+__device__ __forceinline__ Source source_at(const Source& g, int z) {
+  Source s = g;
+  if (z) s.A[0] = g.A[1];
+  return s;
+}
+
+// All tiles of one size; with SPLIT each is sp.parts units along the contraction, whose sums
+// lie one after another in sp.sums.
+template <class C_, bool MASKED, bool SPLIT, class Out>
+__global__ __launch_bounds__(C_::NT) void tile_kernel(Source g, Out out, Split sp) {
+  extern __shared__ __attribute__((aligned(1024))) char lds[];
+  constexpr int PER_STEP = 64 / Math<C_::KIND>::kBytes;
+  const int64_t TM = (g.m + C_::BM - 1) / C_::BM, TN = (g.n + C_::COLS - 1) / C_::COLS, tiles = TM * TN;
+  const int64_t u = gemm::xcd_remap(blockIdx.x, gridDim.x);
+  const int z = __builtin_amdgcn_readfirstlane(int(u / tiles % sp.batch));
+  int64_t tm, tn;
+  tile_at(u % tiles, TM, TN, tm, tn);
+  const int steps = __builtin_amdgcn_readfirstlane(int((MASKED ? (g.K + PER_STEP - 1) / PER_STEP : g.K / PER_STEP) * g.segs));
+  const Source s = source_at(g, z);
+  if constexpr (SPLIT) {
+    // a part's tiles are neighbours
+    const int64_t part = u / (tiles * sp.batch);
+    const int s0 = __builtin_amdgcn_readfirstlane(int(part * steps / sp.parts));
+    const int s1 = __builtin_amdgcn_readfirstlane(int((part + 1) * steps / sp.parts));
+    using P = Partial<C_::KIND, C_::NB>;
+    const P po{static_cast<typename P::sum_t*>(sp.sums) + (part * sp.batch + z) * g.m * C_::NB * sp.ldp, sp.ldp, sp.ldp};
+    unit<C_, MASKED>(s, tm * C_::BM, tn * C_::COLS, s0, s1, part == sp.parts - 1, po, lds);
+  } else {
+    unit<C_, MASKED>(s, tm * C_::BM, tn * C_::COLS, 0, steps, true, out.at(z), lds);
+  }
+}
+
+// Sums of the parts, added in their order, to the output
+template <int KIND, int NB, class Out>
+__global__ __launch_bounds__(256) void join_kernel(Out out, Split sp, int64_t m) {
+  using sum_t = typename Math<KIND>::sum_t;
+  typedef sum_t sum4_t __attribute__((ext_vector_type(4)));
+  const int64_t per = sp.ldp / 4, t = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  if (t >= m * per * sp.batch) return;
+  const int64_t zr = t / per, col = (t % per) * 4;   // row of the batch
+  const sum_t* src = static_cast<const sum_t*>(sp.sums) + zr * NB * sp.ldp + col;
+  const int64_t stride = sp.batch * m * NB * sp.ldp;
+  sum_t v[NB][4];
+#pragma unroll
+  for (int b = 0; b < NB; ++b) {
+    sum4_t sum = *reinterpret_cast<const sum4_t*>(src + b * sp.ldp);
+    for (int p = 1; p < sp.parts; ++p) sum += *reinterpret_cast<const sum4_t*>(src + b * sp.ldp + p * stride);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[b][e] = sum[e];
+  }
+  const int z = int(zr / m);
+  const int64_t row = zr % m;
+  const Out o = out.at(z);
+  if (col + 4 <= o.width) {
+    o.template store<4>(row, col, v, o.template cols<4>(col), o.template pre<4>(row, col));
+  } else {
+    for (int e = 0; e < 4; ++e)
+      if (col + e < o.width) {
+        sum_t w[NB][1];
+#pragma unroll
+        for (int b = 0; b < NB; ++b) w[b][0] = v[b][e];
+        o.template store<1>(row, col + e, w, o.template cols<1>(col + e), o.template pre<1>(row, col + e));
+      }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Few rows
+// ---------------------------------------------------------------------------
+// Up to 16 rows, straight from memory: no tile is staged, each wave reads 16 rows of every B
+// and the rows of A, 128 bytes of each at a time, and multiplies them on 16 x 16 blocks.  The
+// waves of a workgroup take the 128-byte groups of the contraction in turn; their sums meet in
+// LDS and are added in the order of the waves.  B is the first operand: a lane holds four
+// consecutive columns of one row of C.
+template <int KIND, int NB, class Out>
+__global__ __launch_bounds__(512) void direct_kernel(Source g, Out out) {
+  using M_ = Math<KIND>;
+  using sum_t = typename M_::sum_t;
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  sum_t* red = reinterpret_cast<sum_t*>(lds);   // [waves][NB * 4][64]
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+  const int r = lane & 15, kq = lane >> 4;
+  const int64_t n0 = int64_t(blockIdx.x) * 16;
+  // 16 bytes at 16 kq and at 64 + 16 kq of the group: the same k-values for both operands
+  const char *pb[NB], *pa = g.A[0] + min(int64_t(r), g.m - 1) * g.lda + 16 * kq;
+#pragma unroll
+  for (int b = 0; b < NB; ++b) pb[b] = g.B[b] + min(n0 + r, g.n - 1) * g.ldb + 16 * kq;
+  typename M_::acc4_t acc[NB];
+#pragma unroll
+  for (int b = 0; b < NB; ++b) acc[b] = typename M_::acc4_t{0, 0, 0, 0};
+  const int64_t bytes = g.K * M_::kBytes, groups = bytes / 128;
+  auto load = [](const char* p) __attribute__((always_inline)) {
+    const uint4 v = load16(reinterpret_cast<const bf16_t*>(p));
+    return u32x4_t{v.x, v.y, v.z, v.w};
+  };
+  constexpr int U = 4;   // groups whose loads are in flight together
+  for (int64_t kb0 = wave; kb0 < groups; kb0 += U * waves) {
+    u32x4_t fb[U][NB][2], fa[U][2];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t at = min(kb0 + u * waves, groups - 1) * 128;   // past the end: read again, not used
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+#pragma unroll
+        for (int b = 0; b < NB; ++b) fb[u][b][c] = load(pb[b] + at + 64 * c);
+        fa[u][c] = load(pa + at + 64 * c);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (kb0 + u * waves >= groups) break;
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int b = 0; b < NB; ++b) acc[b] = M_::mma16(fb[u][b][c], fa[u][c], acc[b]);
+    }
+  }
+  if (wave == waves - 1 && bytes % 128 != 0) {   // the last, partial group
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int64_t at = groups * 128 + 64 * c, left = (bytes - at - 16 * kq) / 2;
+      const u32x4_t fa = masked16(reinterpret_cast<const bf16_t*>(pa + at), left);
+#pragma unroll
+      for (int b = 0; b < NB; ++b) acc[b] = M_::mma16(masked16(reinterpret_cast<const bf16_t*>(pb[b] + at), left), fa, acc[b]);
+    }
+  }
+  if (waves > 1) {
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) red[((wave * NB + b) * 4 + v) * 64 + lane] = acc[b][v];
+    __syncthreads();
+    if (wave > 0) return;
+  }
+  sum_t o[NB][4];
+#pragma unroll
+  for (int b = 0; b < NB; ++b)
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      o[b][v] = acc[b][v];
+      for (int w = 1; w < waves; ++w) o[b][v] += red[((w * NB + b) * 4 + v) * 64 + lane];
+    }
+  const int64_t row = r, col = n0 + 4 * kq;
+  if (row >= g.m || col >= g.n) return;
+  if (col + 4 <= g.n) {
+    out.template store<4>(row, col, o, out.template cols<4>(col), out.template pre<4>(row, col));
+  } else {
+    for (int e = 0; e < 4; ++e)
+      if (col + e < g.n) {
+        sum_t w[NB][1];
+#pragma unroll
+        for (int b = 0; b < NB; ++b) w[b][0] = o[b][e];
+        out.template store<1>(row, col + e, w, out.template cols<1>(col + e), out.template pre<1>(row, col + e));
+      }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Launches
+// ---------------------------------------------------------------------------
+// the tiles address the rows of a stage with 32-bit offsets (256 rows of under 2^24 bytes)
+constexpr int64_t kMaxPitch = (int64_t(1) << 24) - 16;
+constexpr int64_t kCus = 256;
+
+// How a product is cut, by its sizes alone.
+//  direct  up to 16 rows: bound by reading B once, straight from memory
+//  narrow  up to 64 rows: 64 x 128 tiles
+//  small   128 x 128 tiles where 256 x 256 ones would leave more than half the CUs idle
+//  large   256 x 256 tiles
+// Tiles of the first two sizes that are fewer than half the CUs are cut along the contraction
+// into `parts` of at least 8 steps, about two per CU, joined by a second kernel.
+enum PlanKind { kDirect, kNarrow, kSmall, kLarge };
+struct Plan {
+  PlanKind kind;
+  int parts;
+};
+// m, n at least 1; rows_only: both operands lie in rows, a_rows: A does
+inline Plan plan_product(int64_t m, int64_t n, int64_t steps, int mats, int batch, bool rows_only, bool a_rows = true) {
+  if (m <= 16 && rows_only) return {kDirect, 1};
+  const int64_t cols = n * mats;
+  const bool narrow = m <= 64 && a_rows;
+  const int64_t tiles = ceil_div(m, narrow ? 64 : 128) * ceil_div(cols, 128) * batch;
+  const int64_t parts = std::min<int64_t>(std::min<int64_t>(16, steps / 8), ceil_div(2 * kCus, tiles));
+  const int p = 2 * tiles <= kCus && parts > 1 ? int(parts) : 1;
+  if (narrow) return {kNarrow, p};
+  if (p > 1 || 2 * ceil_div(m, 256) * ceil_div(cols, 256) * batch < kCus) return {kSmall, p};
+  return {kLarge, 1};
+}
+// bytes of the parts' sums
+inline size_t sum_bytes(const Plan& p, int64_t m, int64_t n, int mats, int batch) {
+  return p.parts > 1 ? size_t(p.parts) * batch * size_t(m) * mats * size_t(ceil_div(n, 4) * 4) * 4 : 0;
+}
+
+template <class C_, bool MASKED, bool SPLIT, class Out>
+int launch_tiles(const Source& g, const Out& out, const Split& sp, hipStream_t st) {
+  auto kern = tile_kernel<C_, MASKED, SPLIT, Out>;
+  static std::atomic<uint64_t> configured{0};   // devices with the LDS limit set
+  if (gemm::set_lds_limit(kern, C_::LDS_BYTES, configured) != MUON_OK) return MUON_ELAUNCH;
+  const int64_t units = ceil_div(g.m, C_::BM) * ceil_div(g.n, C_::COLS) * sp.batch * sp.parts;
+  if (units > INT32_MAX) return MUON_EINVAL;
+  launch_kernel(kern, dim3(units), dim3(C_::NT), C_::LDS_BYTES, st, g, out, sp);
+  const int status = launch_status();
+  if (!SPLIT || status != MUON_OK) return status;
+  launch_kernel(join_kernel<C_::KIND, C_::NB, Out>, dim3(ceil_div(g.m * sp.batch * (sp.ldp / 4), 256)), dim3(256), 0, st, out, sp, g.m);
+  return launch_status();
+}
+template <class C_, bool MASKED, class Out>
+int launch_sized(const Source& g, const Out& out, const Split& sp, hipStream_t st) {
+  return sp.parts > 1 ? launch_tiles<C_, MASKED, true>(g, out, sp, st) : launch_tiles<C_, MASKED, false>(g, out, sp, st);
+}
+
+template <int KIND, int NB, class Out>
+int launch_direct(const Source& g, const Out& out, hipStream_t st) {
+  const int64_t groups = g.K * Math<KIND>::kBytes / 128;
+  const int waves = int(std::max<int64_t>(1, std::min<int64_t>(groups / 8, 8)));   // eight groups each, up to eight waves
+  const uint32_t lds = waves > 1 ? uint32_t(waves) * NB * 4 * 64 * 4 : 0;
+  launch_kernel(direct_kernel<KIND, NB, Out>, dim3(ceil_div(g.n, 16)), dim3(64 * waves), lds, st, g, out);
+  return launch_status();
+}
+
+}  // namespace tile
+}  // namespace muon
