@@ -26,3 +26,4 @@ from ._abi import MUON_GLU_MAX_SIDE, MUON_INT8_MAX_K, MUON_INT8_STEP, int8_buffe
 from ._abi import int8_gemm_workspace_bytes, int8_glu, int8_glu_workspace_bytes, int8_quantize  # noqa: F401
 from ._abi import glu_backward, glu_backward_workspace_bytes, glu_forward, glu_forward_workspace_bytes  # noqa: F401
 from ._abi import glu_weight_grad, glu_weight_grad_workspace_bytes  # noqa: F401
+from .gatedlinear import GatedLinear  # noqa: F401

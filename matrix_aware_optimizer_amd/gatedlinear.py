@@ -1,0 +1,135 @@
+"""The two projections of a gated feed-forward block, trained with Muon and answering in 8 bits.
+
+Host-side orchestration of glu_forward, glu_backward, glu_weight_grad,
+ns_orthogonalize and apply_update_dense for one block, and of int8_quantize and
+int8_glu for its answers.  All arithmetic runs in libmuon's kernels.
+
+    h  = act(x Wg^T) * (x Wu^T)                          forward
+    dx, and M <- beta M + alpha dW for both matrices     backward (the gradients are never written)
+    W <- W - eta NS(M) for both                          step     (each matrix orthogonalised by itself)
+    h from int8 codes, a scale per output and token      quantize, answer
+"""
+from __future__ import annotations
+
+from typing import Optional
+
+import torch
+
+from . import _abi
+from .blocklinear import _rows
+
+
+class GatedLinear:
+    """``Wg`` and ``Wu`` [out, in] (contiguous, bf16) with their momenta; updated in place.
+
+    The momenta are fp32 unless ``m_dtype`` says otherwise; ``act`` is one of silu, gelu, gelu_tanh, relu."""
+
+    def __init__(self, Wg: torch.Tensor, Wu: torch.Tensor, act: str = "silu", m_dtype=torch.float32, beta: float = 0.95,
+                 alpha: Optional[float] = None, eta: float = 0.02, coeffs=(3.4445, -4.7750, 2.0315), ns_steps: int = 5):
+        for W in (Wg, Wu):
+            if W.dim() != 2 or not W.is_contiguous() or W.dtype != torch.bfloat16 or W.shape != Wg.shape or W.device != Wg.device:
+                raise ValueError("Wg and Wu must be contiguous bf16 [out, in] matrices of one shape on one device")
+        if Wg.data_ptr() == Wu.data_ptr() and Wg.numel() > 0:
+            raise ValueError("Wg and Wu must be two matrices")
+        _abi._act_code(act)
+        self.Wg, self.Wu, self.act = Wg, Wu, act
+        self.Mg, self.Mu = (torch.zeros(W.shape, dtype=m_dtype, device=W.device) for W in (Wg, Wu))
+        self.beta = float(beta)
+        self.alpha = float(1.0 - beta if alpha is None else alpha)
+        self.eta, self.coeffs, self.ns_steps = float(eta), tuple(float(c) for c in coeffs), int(ns_steps)
+        self._accumulating = False      # a backward since the last step: later ones add without beta
+        self._steps = 0
+        self._codes = None              # (weights' state, codes and scales of Wg, of Wu)
+
+    def _state(self):
+        """Changes whenever the weights do, by step() or by torch operations on them."""
+        return self._steps, self.Wg._version, self.Wu._version
+
+    def _flat(self, x: torch.Tensor) -> torch.Tensor:
+        if x.dim() != 2 or x.shape[1] != self.Wg.shape[1]:
+            raise ValueError(f"x must be [tokens, {self.Wg.shape[1]}]")
+        return _rows(x)
+
+    def forward(self, x: torch.Tensor, train: bool = True):
+        """(h, saved) for x [tokens, in] in bf16; ``saved`` (None unless ``train``) goes to backward and holds x itself."""
+        x = self._flat(x)
+        shape = (x.shape[0], self.Wg.shape[0])
+        h = torch.empty(shape, dtype=x.dtype, device=x.device)
+        g, u = (torch.empty_like(h), torch.empty_like(h)) if train else (None, None)
+        _abi.glu_forward(x, self.Wg, self.Wu, h, g, u, act=self.act)
+        return h, (x, g, u, self._state()) if train else None
+
+    def backward(self, dh: torch.Tensor, saved, need_dx: bool = True) -> Optional[torch.Tensor]:
+        """Adds both weight gradients to the momenta (decayed by beta once per step) and returns dx.
+
+        dx needs the weights of the forward: after a change of them in between it raises."""
+        x, g, u, state = saved
+        if dh.shape != g.shape:
+            raise ValueError(f"dh must be [{g.shape[0]}, {g.shape[1]}], as the forward's h")
+        if need_dx and state != self._state():
+            raise RuntimeError("the weights changed after this forward: dx needs those that it used "
+                               "(run backward before step(), or without the input gradient)")
+        dh = _rows(dh)
+        dg, du = torch.empty_like(g), torch.empty_like(u)
+        dx = torch.empty_like(x, memory_format=torch.contiguous_format) if need_dx else None
+        _abi.glu_backward(dh, g, u, dg, du, *((self.Wg, self.Wu, dx) if need_dx else ()), act=self.act)
+        _abi.glu_weight_grad(dg, du, x, self.Mg, self.Mu, alpha=self.alpha, beta=1.0 if self._accumulating else self.beta)
+        self._accumulating = True
+        return dx
+
+    def step(self) -> None:
+        """The update of both weights from their momenta, each orthogonalised as a whole."""
+        U = [torch.empty_like(W) for W in (self.Wg, self.Wu)]
+        _abi.ns_orthogonalize([(self.Mg, U[0], None), (self.Mu, U[1], None)], *self.coeffs, self.ns_steps)
+        for W, direction in zip((self.Wg, self.Wu), U):
+            _abi.apply_update_dense(W, direction, self.eta)
+        self._steps += 1
+        self._accumulating = False
+
+    def quantize(self) -> None:
+        """int8 codes of the current weights, for :meth:`answer`."""
+        codes = []
+        for W in (self.Wg, self.Wu):
+            q, s = _abi.int8_buffers(*W.shape, device=W.device)
+            _abi.int8_quantize(W, q, s)
+            codes += [q, s]
+        self._codes = (self._state(), *codes)
+
+    def answer(self, x: torch.Tensor) -> torch.Tensor:
+        """h for x [tokens, in] (bf16 or fp32) on int8 codes of the tokens and of the weights as of :meth:`quantize`."""
+        if self._codes is None or self._codes[0] != self._state():
+            raise RuntimeError("the weights have no codes, or changed after quantize()")
+        x = self._flat(x)
+        q, s = _abi.int8_buffers(*x.shape, device=x.device)
+        _abi.int8_quantize(x, q, s)
+        h = torch.empty((x.shape[0], self.Wg.shape[0]), dtype=x.dtype, device=x.device)
+        _abi.int8_glu(q, s, *self._codes[1:], h, act=self.act)
+        return h
+
+    def __call__(self, x: torch.Tensor) -> torch.Tensor:
+        """h for x [..., in], differentiable: backward goes through :meth:`backward`."""
+        if x.dim() == 0 or x.shape[-1] != self.Wg.shape[1]:
+            raise ValueError(f"x must be [..., {self.Wg.shape[1]}]")
+        flat = x.reshape(-1, x.shape[-1]) if x.shape[-1] else x.new_empty((x.shape[:-1].numel(), 0))
+        if torch.is_grad_enabled():
+            # the weights are no leaves of autograd (their gradients go into the momenta), so the node hangs on x or on an empty anchor
+            anchor = torch.empty(0, device=x.device, requires_grad=True)
+            h = _GatedLinearFn.apply(flat, anchor, self)
+        else:
+            h = self.forward(flat, train=False)[0]
+        return h.view(*x.shape[:-1], self.Wg.shape[0])
+
+
+class _GatedLinearFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, anchor, block):
+        h, saved = block.forward(x.detach())
+        ctx.block, ctx.state = block, saved[3]
+        ctx.save_for_backward(*saved[:3])
+        return h
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dh):
+        dx = ctx.block.backward(dh, (*ctx.saved_tensors, ctx.state), ctx.needs_input_grad[0])
+        return dx, None, None
