@@ -41,31 +41,147 @@ __device__ __forceinline__ int quotient(float x, float s, float inv) {
   return int(k);
 }
 
-template <typename T>
-__global__ __launch_bounds__(256) void int8_quantize_kernel(QuantArgs g) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  __shared__ float part[4];
-  const int64_t row = blockIdx.x;
-  const T* x = static_cast<const T*>(g.x) + row * g.ldx;
-  float m = 0.0f;
-  bool bad = false;
-  for (int64_t c = threadIdx.x; c < g.cols; c += 256) {
-    const float v = fabsf(to_f32(x[c]));
-    bad |= !(v < INFINITY);
-    m = fmaxf(m, v);
+// Eight codes.  x * inv + 3 * 2^22 rounds x * inv to an integer, ties to even, and its low byte
+// is the code in two's complement.  inv is off by 2^-24 of itself, so the integer is that of
+// the exact quotient unless x * inv lies within 127 * 2^-24 of a half; a wave that holds such
+// an entry (one in a hundred, by chance) takes the remainders.
+__device__ __forceinline__ uint2 codes8(const float (&x)[8], float s, float inv) {
+  constexpr float kShift = 12582912.0f;
+  float k[8], far = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    k[i] = fmaf(x[i], inv, kShift);
+    far = fmaxf(far, fabsf(fmaf(x[i], inv, kShift - k[i])));
   }
-  if (bad) m = INFINITY;
+  if (__any(far > 0.49999f)) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) k[i] = kShift + float(quotient(x[i], s, inv));
+  }
+  uint32_t w[4];   // bytes 0 of neighbours
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = __builtin_amdgcn_perm(__float_as_uint(k[2 * i + 1]), __float_as_uint(k[2 * i]), 0x0c0c0400u);
+  return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+}
+
+// Eight neighbouring columns of a row as loaded.  top(): the largest magnitude as fp32 bits (NaN
+// and infinity are the largest).
+template <typename T> struct Eight;
+template <> struct Eight<bf16_t> {
+  uint32_t w[4];
+  __device__ __forceinline__ void load(const bf16_t* p, int64_t left) {
+    if (left >= 8) {
+      const uint4 r = load16(p);
+      w[0] = r.x; w[1] = r.y; w[2] = r.z; w[3] = r.w;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t lo = 2 * j < left ? p[2 * j] : 0u, hi = 2 * j + 1 < left ? p[2 * j + 1] : 0u;
+        w[j] = lo | (hi << 16);
+      }
+    }
+  }
+  __device__ __forceinline__ uint32_t top() const {
+    typedef unsigned short u16x2_t __attribute__((ext_vector_type(2)));
+    u16x2_t m = {0, 0};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2_t, w[j] & 0x7fff7fffu));
+    return uint32_t(m[0] > m[1] ? m[0] : m[1]) << 16;
+  }
+  __device__ __forceinline__ void values(float (&v)[8]) const {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = __uint_as_float((k & 1) ? w[k >> 1] & 0xffff0000u : w[k >> 1] << 16);
+  }
+};
+template <> struct Eight<float> {
+  float x[8];
+  __device__ __forceinline__ void load(const float* p, int64_t left) {
+    if (left >= 8) load_n<8>(p, x);
+    else
+#pragma unroll
+      for (int k = 0; k < 8; ++k) x[k] = k < left ? p[k] : 0.0f;
+  }
+  __device__ __forceinline__ uint32_t top() const {
+    uint32_t m = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const uint32_t a = __float_as_uint(x[k]) & 0x7fffffffu;
+      m = a > m ? a : m;
+    }
+    return m;
+  }
+  __device__ __forceinline__ void values(float (&v)[8]) const {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = x[k];
+  }
+};
+
+// Rows of W waves, four waves to a workgroup, eight neighbouring columns per thread and chunk.
+// Up to 512 W CH columns a row is read once and stays in registers (CH chunks of a thread);
+// longer rows (CH = 0) are read twice, the second time from the caches.
+template <typename T, int W, int CH>
+__global__ __launch_bounds__(256) void int8_quantize_kernel(QuantArgs g) {
+  constexpr int NT = 64 * W, N = CH > 0 ? CH : 1;
+  __shared__ float part[4];
+  const int lane = threadIdx.x & 63, t = threadIdx.x % NT;
+  const int64_t row = int64_t(blockIdx.x) * (4 / W) + threadIdx.x / NT;
+  if (W == 1 && row >= g.rows) return;
+  const T* x = static_cast<const T*>(g.x) + row * g.ldx;
+  uint32_t bits = 0;
+  Eight<T> v[N];
+  if constexpr (CH > 0) {
+#pragma unroll
+    for (int i = 0; i < CH; ++i) v[i].load(x + (t + i * NT) * 8, g.cols - (t + i * NT) * 8);
+#pragma unroll
+    for (int i = 0; i < CH; ++i) bits = max(bits, v[i].top());
+  } else {
+    for (int64_t c = int64_t(t) * 8; c < g.cols; c += NT * 8) {
+      v[0].load(x + c, g.cols - c);
+      bits = max(bits, v[0].top());
+    }
+  }
+  float m = __uint_as_float(min(bits, 0x7f800000u));   // infinite or NaN: infinity
 #pragma unroll
   for (int o = 32; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor(m, o, kWave));
-  if (lane == 0) part[wave] = m;
-  __syncthreads();
-  m = fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
+  if constexpr (W > 1) {
+    if (lane == 0) part[threadIdx.x >> 6] = m;
+    __syncthreads();
+    m = fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
+  }
   const bool finite = m < INFINITY;
   const float s = fmaxf(m * (1.0f / 127.0f), 0x1p-126f), inv = 1.0f / s;
   const int64_t padded = ceil_div(g.cols, kStep) * kStep;
-  for (int64_t c = threadIdx.x; c < padded; c += 256)
-    g.q[row * g.ldq + c] = finite && c < g.cols ? int8_t(quotient(to_f32(x[c]), s, inv)) : int8_t(0);
-  if (threadIdx.x == 0) g.s[row] = finite ? s : NAN;
+  int8_t* q = g.q + row * g.ldq;
+  auto write = [&](int64_t c, const Eight<T>& e) __attribute__((always_inline)) {
+    float r[8];
+    e.values(r);
+    const uint2 w = codes8(r, s, inv);
+    if (c < padded) *reinterpret_cast<uint2*>(q + c) = finite ? w : make_uint2(0, 0);
+  };
+  if constexpr (CH > 0) {
+#pragma unroll
+    for (int i = 0; i < CH; ++i) write((t + i * NT) * 8, v[i]);
+  } else {
+    for (int64_t c = int64_t(t) * 8; c < padded; c += NT * 8) {
+      v[0].load(x + c, g.cols - c);
+      write(c, v[0]);
+    }
+  }
+  if (t == 0) g.s[row] = finite ? s : NAN;
+}
+
+template <typename T, int W, int CH>
+int launch_quantize(const QuantArgs& g, hipStream_t st) {
+  launch_kernel(int8_quantize_kernel<T, W, CH>, dim3(ceil_div(g.rows, 4 / W)), dim3(256), 0, st, g);
+  return launch_status();
+}
+template <typename T>
+int quantize(const QuantArgs& g, hipStream_t st) {
+  if (g.cols <= 512) return launch_quantize<T, 1, 1>(g, st);
+  if (g.cols <= 2048) return launch_quantize<T, 4, 1>(g, st);
+  if (g.cols <= 4096) return launch_quantize<T, 4, 2>(g, st);
+  if (g.cols <= 8192) return launch_quantize<T, 4, 4>(g, st);
+  if (g.cols <= 16384) return launch_quantize<T, 4, 8>(g, st);
+  return launch_quantize<T, 4, 0>(g, st);
 }
 
 // ---------------------------------------------------------------------------
@@ -141,9 +257,7 @@ int int8_quantize(const void* x, int x_dtype, int64_t rows, int64_t cols, int64_
   if (!aligned16(x) || !aligned16(q) || !aligned16(s)) return MUON_EALIGN;
   const QuantArgs g{x, rows, cols, ldx, static_cast<int8_t*>(q), ldq, s};
   hipStream_t hs = static_cast<hipStream_t>(stream);
-  if (x_dtype == MUON_F32) launch_kernel(int8_quantize_kernel<float>, dim3(rows), dim3(256), 0, hs, g);
-  else launch_kernel(int8_quantize_kernel<bf16_t>, dim3(rows), dim3(256), 0, hs, g);
-  return launch_status();
+  return x_dtype == MUON_F32 ? quantize<float>(g, hs) : quantize<bf16_t>(g, hs);
 }
 
 size_t int8_gemm_workspace_bytes(int64_t m, int64_t n, int64_t K) { return workspace_bytes(m, n, K, 1); }
