@@ -91,12 +91,13 @@ __global__ __launch_bounds__(256) void glu_gradients_kernel(GradArgs a) {
 // A product on tiles: the sizes of `plan`, through the DMA where rows start at 16 bytes
 template <bool AT, bool BT, bool DUAL, class Out>
 int launch_tiled(const tile::Source& g, const Out& out, const tile::Plan& plan, const tile::Split& sp, bool whole, hipStream_t st) {
+  if ((AT ? g.m : g.K) < 8 || (BT ? g.n : g.K) < 8) return tile::launch_plain<DUAL ? 2 : 1>(g, out, sp.batch, AT, BT, st);
   if (!whole) return tile::launch_sized<tile::Config<kBf16, 128, 128, 64, 64, 4, AT, BT, DUAL>, true>(g, out, sp, st);
   if constexpr (!AT) {
-    if (plan.kind == tile::kNarrow) return tile::launch_sized<tile::Config<kBf16, 64, 128, 32, 64, 4, AT, BT, DUAL>, false>(g, out, sp, st);
+    if (plan.kind == tile::kNarrow) return tile::launch_sized<tile::Config<kBf16, 64, 128, 32, 64, 8, AT, BT, DUAL>, false>(g, out, sp, st);
   }
   if (plan.kind == tile::kSmall) return tile::launch_sized<tile::Config<kBf16, 128, 128, 64, 64, 4, AT, BT, DUAL>, false>(g, out, sp, st);
-  return tile::launch_tiles<tile::Config<kBf16, 256, 256, 128, 128, 4, AT, BT, DUAL>, false, false>(g, out, sp, st);
+  return tile::launch_mixed<kBf16, AT, BT, DUAL>(g, out, sp.batch, st);
 }
 
 bool sides_ok(int64_t tokens, int64_t out, int64_t in) {

@@ -225,11 +225,11 @@ int launch_product(const tile::Source& g, const Out& out, const tile::Plan& plan
     case tile::kDirect:
       return tile::launch_direct<kI8, NB>(g, out, st);
     case tile::kNarrow:
-      return tile::launch_sized<tile::Config<kI8, 64, 128, 32, 64, 4, false, false, DUAL>, false>(g, out, sp, st);
+      return tile::launch_sized<tile::Config<kI8, 64, 128, 32, 64, 8, false, false, DUAL>, false>(g, out, sp, st);
     case tile::kSmall:
       return tile::launch_sized<tile::Config<kI8, 128, 128, 64, 64, 4, false, false, DUAL>, false>(g, out, sp, st);
     default:
-      return tile::launch_tiles<tile::Config<kI8, 256, 256, 128, 128, 4, false, false, DUAL>, false, false>(g, out, sp, st);
+      return tile::launch_mixed<kI8, false, false, DUAL>(g, out, 1, st);
   }
 }
 

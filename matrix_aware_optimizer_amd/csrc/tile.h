@@ -117,6 +117,9 @@ __device__ __forceinline__ void ring_barrier() {
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
+// all LDS accesses of the wave are done, then all waves meet; loads to registers stay under way
+__device__ __forceinline__ void ring_barrier_lds() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
 // 16 bytes of bf16 values at p, of which `left` lie inside the matrix: zeros past them
 __device__ __forceinline__ u32x4_t masked16(const bf16_t* p, int64_t left) {
   u32x4_t r = {0, 0, 0, 0};
@@ -314,48 +317,88 @@ __device__ __forceinline__ void unit(const Source& g, int64_t m0, int64_t n0, in
   if constexpr (C_::KIND == kBf16) {
     // steps through registers: every step of [s0, s1) (MASKED), or the segments' partial last steps
     const int first = MASKED ? s0 : 0, last = MASKED ? s1 : (tail && g.K % PER_STEP != 0 ? g.segs : 0);
-    u32x4_t held[C_::CHUNKS];
-    auto fetch = [&](int s) __attribute__((always_inline)) {
+    // chunk i of this thread: whether it is A's, its LDS row and chunk; uniform parts stay scalar (NT divides both operands' chunks)
+    auto place = [&](int i, bool& of_a, int& r, int& c) __attribute__((always_inline)) {
+      of_a = i * C_::NT < BM * 4;
+      const int x = threadIdx.x + i * C_::NT - (of_a ? 0 : BM * 4);
+      const bool t = of_a ? C_::AT : C_::BT;
+      const int side = of_a ? BM : BN;
+      r = t ? x / (side / 8) : x >> 2;
+      c = t ? x % (side / 8) : x & 3;
+    };
+    // Sixteen bytes are loaded from inside the row (rows have at least eight entries), moved back
+    // where it ends, and put right in put(): no load stands in a branch, where it would be waited for.
+    struct Held {
+      u32x4_t v[C_::CHUNKS];
+      int back[C_::CHUNKS];   // entries that the start was moved back; 8: all of it lies outside
+    };
+    auto fetch = [&](int s, Held& f) __attribute__((always_inline)) {
       const int seg = MASKED ? (s >= per ? 1 : 0) : s;
       const int64_t k0 = int64_t(MASKED ? s - seg * per : per) * PER_STEP;
 #pragma unroll
       for (int i = 0; i < C_::CHUNKS; ++i) {
-        const int idx = threadIdx.x + i * C_::NT;
-        const bool of_a = idx < BM * 4;   // uniform: NT divides both operands' chunks
-        const int x = of_a ? idx : idx - BM * 4;
-        if (of_a) {
-          const int r = C_::AT ? x / (BM / 8) : x >> 2, c = C_::AT ? x % (BM / 8) : x & 3;
-          const int64_t k = k0 + (C_::AT ? r : 8 * c), row = m0 + (C_::AT ? 8 * c : min(r, mlast));
-          const char* p = (seg ? g.A[1] : g.A[0]) + (C_::AT ? k * g.lda + row * 2 : row * g.lda + k * 2);
-          held[i] = masked16(reinterpret_cast<const bf16_t*>(p), C_::AT ? (k < g.K ? g.m - row : 0) : g.K - k);
-        } else {
-          const int r = C_::BT ? x / (BN / 8) : x >> 2, c = C_::BT ? x % (BN / 8) : x & 3;
-          const int64_t k = k0 + (C_::BT ? r : 8 * c), row = n0 + (C_::BT ? 8 * c : min(col_of(r), nlast));
-          const char* p = ((C_::DUAL ? is_up(r) : seg != 0) ? g.B[1] : g.B[0]) + (C_::BT ? k * g.ldb + row * 2 : row * g.ldb + k * 2);
-          held[i] = masked16(reinterpret_cast<const bf16_t*>(p), C_::BT ? (k < g.K ? g.n - row : 0) : g.K - k);
-        }
+        bool of_a;
+        int r, c;
+        place(i, of_a, r, c);
+        const bool t = of_a ? C_::AT : C_::BT;
+        const bool second = of_a || !C_::DUAL ? seg != 0 : is_up(r);
+        const char* base = of_a ? (second ? g.A[1] : g.A[0]) : (second ? g.B[1] : g.B[0]);
+        const int64_t ld = of_a ? g.lda : g.ldb, end = of_a ? g.m : g.n;
+        // row of memory, entry in it, and how long the row is
+        const int64_t row = t ? min(k0 + r, g.K - 1) : of_a ? m0 + min(r, mlast) : n0 + min(col_of(r), nlast);
+        const int64_t at = t ? (of_a ? m0 : n0) + 8 * c : k0 + 8 * c, len = t ? end : g.K;
+        const bf16_t* p = reinterpret_cast<const bf16_t*>(base + row * ld);
+        const bool out_of = at >= len || (t && k0 + r >= g.K);
+        const int64_t from = min(at, len - 8);
+        const uint4 v = load16(p + from);
+        f.v[i] = u32x4_t{v.x, v.y, v.z, v.w};
+        f.back[i] = out_of ? 8 : int(at - from);
       }
     };
-    if (first < last) fetch(first);
-    for (int s = first; s < last; ++s) {
-      __syncthreads();   // everybody is done with the stage
+    auto put = [&](Held& f, char* stage) __attribute__((always_inline)) {
 #pragma unroll
       for (int i = 0; i < C_::CHUNKS; ++i) {
-        const int idx = threadIdx.x + i * C_::NT;
-        const bool of_a = idx < BM * 4;
-        const int x = of_a ? idx : idx - BM * 4;
+        bool of_a;
+        int r, c;
+        place(i, of_a, r, c);
         const bool t = of_a ? C_::AT : C_::BT;
         const int side = of_a ? BM : BN;
-        const int r = t ? x / (side / 8) : x >> 2, c = t ? x % (side / 8) : x & 3;
+        if (f.back[i] != 0) {   // at the ends only: entries down by `back`, zeros behind them
+          const int by = f.back[i];
+          u32x4_t v = f.v[i];
+          if (by & 4) v = u32x4_t{v[2], v[3], 0, 0};
+          if (by & 2) v = u32x4_t{v[1], v[2], v[3], 0};
+          if (by & 1) v = u32x4_t{(v[0] >> 16) | (v[1] << 16), (v[1] >> 16) | (v[2] << 16), (v[2] >> 16) | (v[3] << 16), v[3] >> 16};
+          if (by >= 8) v = u32x4_t{0, 0, 0, 0};
+          f.v[i] = v;
+        }
         const int at = (of_a ? 0 : C_::A_BYTES) + (t ? r * 2 * side + ((c ^ (4 * (r & 3))) << 4) : gemm::krow_off(r, c));
-        *reinterpret_cast<u32x4_t*>(lds + at) = held[i];
+        *reinterpret_cast<u32x4_t*>(stage + at) = f.v[i];
       }
-      __syncthreads();
-      if (s + 1 < last) fetch(s + 1);
+    };
+    // Step s is read from stage s % 2 while the registers of step s + 1 go to the other one and
+    // the loads of step s + 2 are under way.
+    if (first < last) {
+      Held h0, h1;
       Frags f;
+      __syncthreads();   // everybody is done with the ring
+      fetch(first, h0);
+      if (first + 1 < last) fetch(first + 1, h1);
+      put(h0, lds);
+      ring_barrier_lds();
+      auto step = [&](int s, Held& next, Held& free) __attribute__((always_inline)) {
+        const char* st = lds + ((s - first) & 1) * C_::STAGE;
+        if (s + 2 < last) fetch(s + 2, free);
 #pragma unroll
-      for (int q = 0; q < READS; ++q) read_one(q, lds, f);
-      mma(f, [](int) {});
+        for (int q = 0; q < READS; ++q) read_one(q, st, f);
+        mma(f, [](int) {});
+        if (s + 1 < last) put(next, lds + ((s + 1 - first) & 1) * C_::STAGE);
+        ring_barrier_lds();
+      };
+      for (int s = first; s < last; s += 2) {
+        step(s, h1, h0);
+        if (s + 1 < last) step(s + 1, h0, h1);
+      }
     }
   }
 
@@ -492,6 +535,39 @@ __global__ __launch_bounds__(C_::NT) void tile_kernel(Source g, Out out, Split s
   }
 }
 
+// 256 x 256 tiles in rounds of one per CU; those of the last, partial round come in `parts`
+// (2: 128 x 256, 4: 128 x 128) so that they fill the CUs.  Workgroups [0, whole) take whole tiles.
+template <int KIND, bool AT, bool BT, bool DUAL, class Out>
+__global__ __launch_bounds__(256) void mixed_kernel(Source g, Out out, int batch, int64_t whole, int parts) {
+  using L = Config<KIND, 256, 256, 128, 128, 4, AT, BT, DUAL>;
+  using H = Config<KIND, 128, 256, 64, 128, 4, AT, BT, DUAL>;
+  using Q = Config<KIND, 128, 128, 64, 64, 4, AT, BT, DUAL>;
+  extern __shared__ __attribute__((aligned(1024))) char lds[];
+  const int64_t TM = (g.m + 255) / 256, TN = (g.n + L::COLS - 1) / L::COLS, tiles = TM * TN;
+  const int steps = __builtin_amdgcn_readfirstlane(int(g.K / (64 / Math<KIND>::kBytes) * g.segs));
+  const int64_t b = blockIdx.x;
+  int64_t t, part = 0, tm, tn;
+  if (b < whole) {
+    t = gemm::xcd_remap(b, whole);
+  } else {
+    const int64_t u = gemm::xcd_remap(b - whole, int64_t(gridDim.x) - whole);
+    t = whole + u / parts;
+    part = u % parts;
+  }
+  const int z = __builtin_amdgcn_readfirstlane(int(t / tiles));
+  tile_at(t % tiles, TM, TN, tm, tn);
+  const Source s = source_at(g, z);
+  const Out o = out.at(z);
+  if (b < whole) {
+    unit<L, false>(s, tm * 256, tn * L::COLS, 0, steps, true, o, lds);
+    return;
+  }
+  const int64_t m0 = tm * 256 + 128 * (part & 1), n0 = tn * L::COLS + Q::COLS * (part >> 1);
+  if (m0 >= g.m || n0 >= g.n) return;
+  if (parts == 2) unit<H, false>(s, m0, n0, 0, steps, true, o, lds);
+  else unit<Q, false>(s, m0, n0, 0, steps, true, o, lds);
+}
+
 // Sums of the parts, added in their order, to the output
 template <int KIND, int NB, class Out>
 __global__ __launch_bounds__(256) void join_kernel(Out out, Split sp, int64_t m) {
@@ -524,6 +600,28 @@ __global__ __launch_bounds__(256) void join_kernel(Out out, Split sp, int64_t m)
         o.template store<1>(row, col + e, w, o.template cols<1>(col + e), o.template pre<1>(row, col + e));
       }
   }
+}
+
+// Rows of fewer than eight entries: one output per thread, straight from the definition.
+template <int NB, class Out>
+__global__ __launch_bounds__(256) void plain_kernel(Source g, Out out, int batch, bool a_kmajor, bool b_kmajor) {
+  const int64_t t = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  if (t >= g.m * g.n * batch) return;
+  const int z = int(t / (g.m * g.n));
+  const int64_t row = t / g.n % g.m, col = t % g.n;
+  float v[NB][1] = {};
+  for (int s = 0; s < g.segs; ++s)
+    for (int64_t k = 0; k < g.K; ++k) {
+      const char* a = (s || z ? g.A[1] : g.A[0]) + (a_kmajor ? k * g.lda + row * 2 : row * g.lda + k * 2);
+      const float av = bf16_to_f32(*reinterpret_cast<const bf16_t*>(a));
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        const char* p = (s || b ? g.B[1] : g.B[0]) + (b_kmajor ? k * g.ldb + col * 2 : col * g.ldb + k * 2);
+        v[b][0] = fmaf(av, bf16_to_f32(*reinterpret_cast<const bf16_t*>(p)), v[b][0]);
+      }
+    }
+  const Out o = out.at(z);
+  o.template store<1>(row, col, v, o.template cols<1>(col), o.template pre<1>(row, col));
 }
 
 // ---------------------------------------------------------------------------
@@ -628,7 +726,7 @@ constexpr int64_t kCus = 256;
 //  direct  up to 16 rows: bound by reading B once, straight from memory
 //  narrow  up to 64 rows: 64 x 128 tiles
 //  small   128 x 128 tiles where 256 x 256 ones would leave more than half the CUs idle
-//  large   256 x 256 tiles
+//  large   256 x 256 tiles, the last round in halves or quarters
 // Tiles of the first two sizes that are fewer than half the CUs are cut along the contraction
 // into `parts` of at least 8 steps, about two per CU, joined by a second kernel.
 enum PlanKind { kDirect, kNarrow, kSmall, kLarge };
@@ -666,11 +764,31 @@ int launch_tiles(const Source& g, const Out& out, const Split& sp, hipStream_t s
   launch_kernel(join_kernel<C_::KIND, C_::NB, Out>, dim3(ceil_div(g.m * sp.batch * (sp.ldp / 4), 256)), dim3(256), 0, st, out, sp, g.m);
   return launch_status();
 }
+template <int KIND, bool AT, bool BT, bool DUAL, class Out>
+int launch_mixed(const Source& g, const Out& out, int batch, hipStream_t st) {
+  using L = Config<KIND, 256, 256, 128, 128, 4, AT, BT, DUAL>;
+  auto kern = mixed_kernel<KIND, AT, BT, DUAL, Out>;
+  static std::atomic<uint64_t> configured{0};
+  if (gemm::set_lds_limit(kern, L::LDS_BYTES, configured) != MUON_OK) return MUON_ELAUNCH;
+  const int64_t tiles = ceil_div(g.m, 256) * ceil_div(g.n, L::COLS) * batch, rest = tiles % kCus;
+  const int parts = rest == 0 ? 1 : rest * 4 <= kCus ? 4 : rest * 2 <= kCus ? 2 : 1;
+  const int64_t whole = parts == 1 ? tiles : tiles - rest;
+  if (whole + (tiles - whole) * parts > INT32_MAX) return MUON_EINVAL;
+  launch_kernel(kern, dim3(whole + (tiles - whole) * parts), dim3(256), L::LDS_BYTES, st, g, out, batch, whole, parts);
+  return launch_status();
+}
 template <class C_, bool MASKED, class Out>
 int launch_sized(const Source& g, const Out& out, const Split& sp, hipStream_t st) {
   return sp.parts > 1 ? launch_tiles<C_, MASKED, true>(g, out, sp, st) : launch_tiles<C_, MASKED, false>(g, out, sp, st);
 }
 
+template <int NB, class Out>
+int launch_plain(const Source& g, const Out& out, int batch, bool a_kmajor, bool b_kmajor, hipStream_t st) {
+  const int64_t blocks = ceil_div(g.m * g.n * batch, 256);
+  if (blocks > INT32_MAX) return MUON_EINVAL;
+  launch_kernel(plain_kernel<NB, Out>, dim3(blocks), dim3(256), 0, st, g, out, batch, a_kmajor, b_kmajor);
+  return launch_status();
+}
 template <int KIND, int NB, class Out>
 int launch_direct(const Source& g, const Out& out, hipStream_t st) {
   const int64_t groups = g.K * Math<KIND>::kBytes / 128;
