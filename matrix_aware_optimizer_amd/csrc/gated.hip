@@ -94,7 +94,7 @@ int launch_tiled(const tile::Source& g, const Out& out, const tile::Plan& plan, 
   if ((AT ? g.m : g.K) < 8 || (BT ? g.n : g.K) < 8) return tile::launch_plain<DUAL ? 2 : 1>(g, out, sp.batch, AT, BT, st);
   if (!whole) return tile::launch_sized<tile::Config<kBf16, 128, 128, 64, 64, 4, AT, BT, DUAL>, true>(g, out, sp, st);
   if constexpr (!AT) {
-    if (plan.kind == tile::kNarrow) return tile::launch_sized<tile::Config<kBf16, 64, 128, 32, 64, 8, AT, BT, DUAL>, false>(g, out, sp, st);
+    if (plan.kind == tile::kNarrow) return tile::launch_sized<tile::Config<kBf16, 64, BT ? 128 : 64, 32, 64, 8, AT, BT, DUAL>, false>(g, out, sp, st);
   }
   if (plan.kind == tile::kSmall) return tile::launch_sized<tile::Config<kBf16, 128, 128, 64, 64, 4, AT, BT, DUAL>, false>(g, out, sp, st);
   return tile::launch_mixed<kBf16, AT, BT, DUAL>(g, out, sp.batch, st);

@@ -225,7 +225,7 @@ int launch_product(const tile::Source& g, const Out& out, const tile::Plan& plan
     case tile::kDirect:
       return tile::launch_direct<kI8, NB>(g, out, st);
     case tile::kNarrow:
-      return tile::launch_sized<tile::Config<kI8, 64, 128, 32, 64, 8, false, false, DUAL>, false>(g, out, sp, st);
+      return tile::launch_sized<tile::Config<kI8, 64, 64, 32, 64, 8, false, false, DUAL>, false>(g, out, sp, st);
     case tile::kSmall:
       return tile::launch_sized<tile::Config<kI8, 128, 128, 64, 64, 4, false, false, DUAL>, false>(g, out, sp, st);
     default:

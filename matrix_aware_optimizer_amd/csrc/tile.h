@@ -85,6 +85,10 @@ struct Config {
   static constexpr int LDW = WN + 4;                        // row pitch of the epilogue's slab, in floats
   static constexpr int LDS_BYTES = S * STAGE > W * 32 * LDW * 4 ? S * STAGE : W * 32 * LDW * 4;
   static constexpr int A_DMA = A_BYTES / 1024 / W, B_DMA = B_BYTES / 1024 / W, D = A_DMA + B_DMA;
+  // Tiles of few rows are bound by reading B, and all start at once: each begins at another step
+  // of the contraction, or the same offsets of many rows (one memory channel, at pitches of 8 KB
+  // and more) are wanted together.  33 x 14336 x 8192 bf16, both weights from memory: 125 -> 108 us.
+  static constexpr bool TURNED = BM == 64;
   static constexpr int CHUNKS = STAGE / 16 / NT;            // 16-byte chunks per thread of a masked step
   static_assert(A_BYTES % (1024 * W) == 0 && B_BYTES % (1024 * W) == 0, "DMA split");
   static_assert(S >= 3 && D * (S - 2) <= 63 && LDS_BYTES <= 160 * 1024, "ring");
@@ -243,9 +247,14 @@ __device__ __forceinline__ void unit(const Source& g, int64_t m0, int64_t n0, in
     const uint32_t lds_base =
         static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char*)lds));
     const int nk = s1 - s0;
+    const int turn = C_::TURNED && per > 0 ? int(n0 / C_::COLS * 5 % per) : 0;
     auto issue_one = [&](int q, int kt, uint32_t off) __attribute__((always_inline)) {
       const int seg = kt >= per ? 1 : 0;
-      const int64_t k = kt - seg * per;
+      int k = kt - seg * per;
+      if constexpr (C_::TURNED) {
+        k += turn;
+        k = k >= per ? k - per : k;
+      }
       const uint32_t st = lds_base + off;
       if (q < C_::A_DMA) {
         dma16_at(scalar((seg ? g.A[1] : g.A[0]) + a_start + k * a_step), a_off[q], st + (wave * C_::A_DMA + q) * 1024);
@@ -654,11 +663,13 @@ __global__ __launch_bounds__(512) void direct_kernel(Source g, Out out) {
     return u32x4_t{v.x, v.y, v.z, v.w};
   };
   constexpr int U = 4;   // groups whose loads are in flight together
+  const int64_t turn = groups > 0 ? int64_t(blockIdx.x) * 5 % groups : 0;
   for (int64_t kb0 = wave; kb0 < groups; kb0 += U * waves) {
     u32x4_t fb[U][NB][2], fa[U][2];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int64_t at = min(kb0 + u * waves, groups - 1) * 128;   // past the end: read again, not used
+      int64_t at = min(kb0 + u * waves, groups - 1) + turn;   // past the end: read again, not used
+      at = (at >= groups ? at - groups : at) * 128;
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
 #pragma unroll
@@ -666,6 +677,7 @@ __global__ __launch_bounds__(512) void direct_kernel(Source g, Out out) {
         fa[u][c] = load(pa + at + 64 * c);
       }
     }
+    __builtin_amdgcn_sched_barrier(0);   // all loads before the first product: the compiler would take them in turn
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (kb0 + u * waves >= groups) break;
