@@ -16,8 +16,8 @@ namespace {
 using tile::ceil_div;
 using tile::kBf16;
 
-// C <- beta C + alpha sum, one rounding to the stored type; z says which of two outputs
-template <typename TC>
+// C <- beta C + alpha sum (READS) or alpha sum, one rounding to the stored type; z says which of two outputs
+template <typename TC, bool READS>
 struct AxpbyOut {
   using sum_t = float;
   static constexpr int E = 16 / int(sizeof(TC));
@@ -26,7 +26,7 @@ struct AxpbyOut {
   float alpha, beta;
 
   template <int N> struct Cols {};
-  template <int N> struct Pre { float c[N]; };
+  template <int N> struct Pre { TC c[READS ? N : 1]; };
   __device__ __forceinline__ AxpbyOut at(int z) const {
     AxpbyOut o = *this;
     if (z) o.C = C1;
@@ -35,7 +35,14 @@ struct AxpbyOut {
   template <int N> __device__ __forceinline__ Cols<N> cols(int64_t) const { return {}; }
   template <int N> __device__ __forceinline__ Pre<N> pre(int64_t row, int64_t col) const {
     Pre<N> p;
-    if (beta != 0.0f) load_n<N>(C + row * ldc + col, p.c);
+    if constexpr (READS) {
+      const TC* src = C + row * ldc + col;
+      if constexpr (N * sizeof(TC) == 16) p = __builtin_bit_cast(Pre<N>, load16(src));
+      else if constexpr (N * sizeof(TC) == 8) p = __builtin_bit_cast(Pre<N>, load8(src));
+      else
+#pragma unroll
+        for (int k = 0; k < N; ++k) p.c[k] = src[k];
+    }
     return p;
   }
   template <int N>
@@ -43,9 +50,9 @@ struct AxpbyOut {
     float o[N];
 #pragma unroll
     for (int k = 0; k < N; ++k) o[k] = alpha * v[0][k];
-    if (beta != 0.0f)
+    if constexpr (READS)
 #pragma unroll
-      for (int k = 0; k < N; ++k) o[k] = fmaf(beta, p.c[k], o[k]);
+      for (int k = 0; k < N; ++k) o[k] = fmaf(beta, to_f32(p.c[k]), o[k]);
     store_n<N>(C + row * ldc + col, o);
   }
 };
@@ -189,7 +196,7 @@ int glu_backward(const void* dH, int64_t lddh, const void* G, const void* U, int
   const tile::Plan plan = input_plan(tokens, out, in);
   const tile::Source g{{static_cast<const char*>(dG), static_cast<const char*>(dU)},
                        {static_cast<const char*>(Wg), static_cast<const char*>(Wu)}, ldd * 2, ldw * 2, tokens, in, out, 2};
-  const AxpbyOut<bf16_t> o{static_cast<bf16_t*>(dX), nullptr, lddx, in, 1.0f, 0.0f};
+  const AxpbyOut<bf16_t, false> o{static_cast<bf16_t*>(dX), nullptr, lddx, in, 1.0f, 0.0f};
   const tile::Split sp{plan.parts, 1, workspace, ceil_div(in, 4) * 4};
   return launch_tiled<false, true, false>(g, o, plan, sp, run8(ldd) && run8(ldw) && run8(in), hs);
 }
@@ -215,12 +222,13 @@ int glu_weight_grad(const void* dG, const void* dU, int64_t ldd, const void* X, 
   const tile::Split sp{plan.parts, 2, workspace, ceil_div(in, 4) * 4};
   const bool whole = run8(ldd) && run8(ldx) && run8(out) && run8(in);
   hipStream_t hs = static_cast<hipStream_t>(stream);
-  if (m_dtype == MUON_F32) {
-    const AxpbyOut<float> o{static_cast<float*>(Mg), static_cast<float*>(Mu), ldm, in, alpha, beta};
+  auto go = [&](auto type, auto reads) {
+    using TC = decltype(type);
+    const AxpbyOut<TC, decltype(reads)::value> o{static_cast<TC*>(Mg), static_cast<TC*>(Mu), ldm, in, alpha, beta};
     return launch_tiled<true, true, false>(g, o, plan, sp, whole, hs);
-  }
-  const AxpbyOut<bf16_t> o{static_cast<bf16_t*>(Mg), static_cast<bf16_t*>(Mu), ldm, in, alpha, beta};
-  return launch_tiled<true, true, false>(g, o, plan, sp, whole, hs);
+  };
+  if (m_dtype == MUON_F32) return beta != 0.0f ? go(float{}, std::true_type{}) : go(float{}, std::false_type{});
+  return beta != 0.0f ? go(bf16_t{}, std::true_type{}) : go(bf16_t{}, std::false_type{});
 }
 
 }  // extern "C"

@@ -215,6 +215,20 @@ __device__ __forceinline__ void unit(const Source& g, int64_t m0, int64_t n0, in
     }
   };
 
+  // How the tile leaves (below): a lane takes E columns of every RPP-th row.  What the output needs
+  // from memory (a momentum's old values) is loaded a block of 32 rows ahead.
+  constexpr int E = Out::E, NB = C_::NB, HALF = WN / NB, LPR = HALF / E, RPP = 64 / LPR, PASSES = 32 / RPP;
+  using sum_t = typename Out::sum_t;
+  const int pr = lane / LPR, pc = (lane % LPR) * E;
+  const int64_t col = n0 + wn0 / NB + pc;
+  const bool inside = col + E <= out.width;
+  typename Out::template Pre<E> pre[2][PASSES];
+  auto load_pre = [&](int i) __attribute__((always_inline)) {
+    if (inside)
+#pragma unroll
+      for (int p = 0; p < PASSES; ++p) pre[i & 1][p] = out.template pre<E>(min(m0 + wm0 + 32 * i + pr + RPP * p, g.m - 1), col);
+  };
+
   if constexpr (!MASKED) {
     // sources of this wave's copies
     uint32_t a_off[C_::A_DMA], b_off[C_::B_DMA];
@@ -414,12 +428,9 @@ __device__ __forceinline__ void unit(const Source& g, int64_t m0, int64_t n0, in
   // The tile leaves through LDS, 32 rows at a time and each wave through its own part of the
   // ring, so that rows are read and written 16 bytes per lane and whole lines at a time.
   // Accumulator v of a lane: column 8 (v / 4) + 4 h + v % 4 of B's block, row fr of A's.
-  ring_barrier<0>();
-  constexpr int E = Out::E, NB = C_::NB, HALF = WN / NB, LPR = HALF / E, RPP = 64 / LPR, PASSES = 32 / RPP;
-  using sum_t = typename Out::sum_t;
+  load_pre(0);
+  ring_barrier_lds();
   sum_t* slab = reinterpret_cast<sum_t*>(lds) + wave * 32 * C_::LDW;
-  const int pr = lane / LPR, pc = (lane % LPR) * E;
-  const int64_t col = n0 + wn0 / NB + pc;
   typedef sum_t sum4_t __attribute__((ext_vector_type(4)));
   const typename Out::template Cols<E> cols = out.template cols<E>(col);
 #pragma unroll
@@ -434,10 +445,8 @@ __device__ __forceinline__ void unit(const Source& g, int64_t m0, int64_t n0, in
         *reinterpret_cast<sum4_t*>(slab + fr * C_::LDW + 32 * j + 8 * q + 4 * h) = v;
       }
     const int64_t row0 = m0 + wm0 + 32 * i + pr;
-    if (col + E <= out.width) {
-      typename Out::template Pre<E> pre[PASSES];
-#pragma unroll
-      for (int p = 0; p < PASSES; ++p) pre[p] = out.template pre<E>(min(row0 + RPP * p, g.m - 1), col);
+    if (i + 1 < FM) load_pre(i + 1);
+    if (inside) {
 #pragma unroll
       for (int p = 0; p < PASSES; ++p) {
         sum_t v[NB][E];
@@ -449,7 +458,7 @@ __device__ __forceinline__ void unit(const Source& g, int64_t m0, int64_t n0, in
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[b][k + e] = x[e];
           }
-        if (row0 + RPP * p < g.m) out.template store<E>(row0 + RPP * p, col, v, cols, pre[p]);
+        if (row0 + RPP * p < g.m) out.template store<E>(row0 + RPP * p, col, v, cols, pre[i & 1][p]);
       }
     } else {
       for (int p = 0; p < PASSES; ++p)
