@@ -743,13 +743,17 @@ __global__ __launch_bounds__(512) void direct_kernel(Source g, Out out) {
 constexpr int64_t kMaxPitch = (int64_t(1) << 24) - 16;
 constexpr int64_t kCus = 256;
 
-// How a product is cut, by its sizes alone.
+// How a product is cut, by its sizes alone (tiles counted over all B's and the batch).
 //  direct  up to 16 rows: bound by reading B once, straight from memory
-//  narrow  up to 64 rows: 64 x 128 tiles
+//  narrow  64 rows and 64 columns (128 where an operand is k-major): up to 64 rows, and where
+//          128 x 128 tiles would not be half as many as the CUs
 //  small   128 x 128 tiles where 256 x 256 ones would leave more than half the CUs idle
 //  large   256 x 256 tiles, the last round in halves or quarters
-// Tiles of the first two sizes that are fewer than half the CUs are cut along the contraction
-// into `parts` of at least 8 steps, about two per CU, joined by a second kernel.
+// Narrow and small tiles that are no more than half the CUs are cut along the contraction into
+// `parts` of 16 steps or more, so that there is at most one unit per CU; a second kernel joins them.
+// Two units per CU, as long, share its matrix cores and LDS and write twice the sums: backward to
+// the input of 777 x 2304 x 768, 42 small tiles in 6 parts 28.6 us, in 13 34.1, 78 narrow ones in 3
+// 25.5, in 6 32.0; 33 x 4096 x 14336 int8, 64 narrow tiles in 4 parts 20.5, in 8 23.1.
 enum PlanKind { kDirect, kNarrow, kSmall, kLarge };
 struct Plan {
   PlanKind kind;
@@ -759,12 +763,10 @@ struct Plan {
 inline Plan plan_product(int64_t m, int64_t n, int64_t steps, int mats, int batch, bool rows_only, bool a_rows = true) {
   if (m <= 16 && rows_only) return {kDirect, 1};
   const int64_t cols = n * mats;
-  const bool narrow = m <= 64 && a_rows;
-  const int64_t tiles = ceil_div(m, narrow ? 64 : 128) * ceil_div(cols, 128) * batch;
-  const int64_t parts = std::min<int64_t>(std::min<int64_t>(16, steps / 8), ceil_div(2 * kCus, tiles));
-  const int p = 2 * tiles <= kCus && parts > 1 ? int(parts) : 1;
-  if (narrow) return {kNarrow, p};
-  if (p > 1 || 2 * ceil_div(m, 256) * ceil_div(cols, 256) * batch < kCus) return {kSmall, p};
+  const int64_t narrow = ceil_div(m, 64) * ceil_div(cols, rows_only ? 64 : 128) * batch, small = ceil_div(m, 128) * ceil_div(cols, 128) * batch;
+  auto parts = [&](int64_t tiles) { return int(std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(16, steps / 16), kCus / tiles))); };
+  if (a_rows && (m <= 64 || (2 * small <= kCus && narrow <= kCus))) return {kNarrow, parts(narrow)};
+  if (2 * small <= kCus || 2 * ceil_div(m, 256) * ceil_div(cols, 256) * batch < kCus) return {kSmall, parts(small)};
   return {kLarge, 1};
 }
 // bytes of the parts' sums
