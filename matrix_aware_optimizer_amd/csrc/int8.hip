@@ -237,7 +237,7 @@ bool side_ok(int64_t v) { return v >= 0 && v <= MUON_GLU_MAX_SIDE; }
 
 size_t workspace_bytes(int64_t m, int64_t n, int64_t K, int mats) {
   if (m <= 0 || n <= 0 || K <= 0 || !side_ok(m) || !side_ok(n) || K > MUON_INT8_MAX_K) return 0;
-  return tile::sum_bytes(tile::plan_product(m, n, K / kStep, mats, 1, true), m, n, mats, 1);
+  return tile::sum_bytes(tile::plan_product(m, n, K / kStep, mats, 1, true, true), m, n, mats, 1);
 }
 
 }  // namespace
@@ -276,7 +276,7 @@ int int8_gemm(const void* A, int64_t lda, const float* sa, const void* B, int64_
   if (need > 0 && !aligned16(workspace)) return MUON_EALIGN;
   const char *a = static_cast<const char*>(A), *b = static_cast<const char*>(B);
   const tile::Source g{{a, a}, {b, b}, lda, ldb, m, n, K, 1};
-  const tile::Plan plan = tile::plan_product(m, n, K / kStep, 1, 1, true);
+  const tile::Plan plan = tile::plan_product(m, n, K / kStep, 1, 1, true, true);
   hipStream_t hs = static_cast<hipStream_t>(stream);
   if (c_dtype == MUON_F32) return launch_product<false>(g, ScaleOut<float>{static_cast<float*>(C), ldc, n, sa, sb}, plan, workspace, hs);
   return launch_product<false>(g, ScaleOut<bf16_t>{static_cast<bf16_t*>(C), ldc, n, sa, sb}, plan, workspace, hs);
@@ -298,7 +298,7 @@ int int8_glu(const void* A, int64_t lda, const float* sa, const void* Bg, const 
   if (need > 0 && !aligned16(workspace)) return MUON_EALIGN;
   const char* a = static_cast<const char*>(A);
   const tile::Source g{{a, a}, {static_cast<const char*>(Bg), static_cast<const char*>(Bu)}, lda, ldb, m, n, K, 1};
-  const tile::Plan plan = tile::plan_product(m, n, K / kStep, 2, 1, true);
+  const tile::Plan plan = tile::plan_product(m, n, K / kStep, 2, 1, true, true);
   hipStream_t hs = static_cast<hipStream_t>(stream);
   if (h_dtype == MUON_F32)
     return launch_product<true>(g, GluOut<float, true>{static_cast<float*>(H), nullptr, nullptr, ldh, 0, n, act, sa, sg, su}, plan, workspace, hs);

@@ -140,9 +140,8 @@ __device__ __forceinline__ u32x4_t masked16(const bf16_t* p, int64_t left) {
   return r;
 }
 
-// One tile at rows m0 and columns n0 over steps [s0, s1) of the contraction's whole steps
-// (MASKED: of all its steps, all through registers); `tail`: then the last, partial step of
-// every segment.
+// One tile at rows m0 and columns n0 over steps [s0, s1) of the contraction's whole steps (MASKED:
+// through registers); `tail`: then the last, partial step of every segment.
 template <class C_, bool MASKED, class Out>
 __device__ __forceinline__ void unit(const Source& g, int64_t m0, int64_t n0, int s0, int s1, bool tail, const Out& out, char* lds) {
   using M_ = Math<C_::KIND>;
@@ -152,7 +151,7 @@ __device__ __forceinline__ void unit(const Source& g, int64_t m0, int64_t n0, in
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int fr = lane & 31, h = lane >> 5;
   const int wm0 = (wave / (BN / WN)) * WM, wn0 = (wave % (BN / WN)) * WN;
-  const int per = __builtin_amdgcn_readfirstlane(int(MASKED ? (g.K + PER_STEP - 1) / PER_STEP : g.K / PER_STEP));
+  const int per = __builtin_amdgcn_readfirstlane(int(g.K / PER_STEP));
   // column of C of B's LDS row (or k-major column) r, and which B it is of
   auto col_of = [](int r) { return C_::DUAL ? (r / WN) * (WN / 2) + r % (WN / 2) : r; };
   auto is_up = [](int r) { return C_::DUAL && r % WN >= WN / 2; };
@@ -338,9 +337,14 @@ __device__ __forceinline__ void unit(const Source& g, int64_t m0, int64_t n0, in
   }
 
   if constexpr (C_::KIND == kBf16) {
-    // steps through registers: every step of [s0, s1) (MASKED), or the segments' partial last steps
-    const int first = MASKED ? s0 : 0, last = MASKED ? s1 : (tail && g.K % PER_STEP != 0 ? g.segs : 0);
-    // chunk i of this thread: whether it is A's, its LDS row and chunk; uniform parts stay scalar (NT divides both operands' chunks)
+    // Steps through registers.  Sixteen bytes are loaded from inside the row (rows have at least
+    // eight entries), moved back where it ends, and put right before they go to LDS: no load stands
+    // in a branch, where it would be waited for.
+    struct Held {
+      u32x4_t v[C_::CHUNKS];
+      int back[C_::CHUNKS];   // entries that the start was moved back; 8: all of it lies outside
+    };
+    // chunk i of this thread: whether it is A's, its LDS row and chunk (NT divides both operands' chunks)
     auto place = [&](int i, bool& of_a, int& r, int& c) __attribute__((always_inline)) {
       of_a = i * C_::NT < BM * 4;
       const int x = threadIdx.x + i * C_::NT - (of_a ? 0 : BM * 4);
@@ -349,80 +353,162 @@ __device__ __forceinline__ void unit(const Source& g, int64_t m0, int64_t n0, in
       r = t ? x / (side / 8) : x >> 2;
       c = t ? x % (side / 8) : x & 3;
     };
-    // Sixteen bytes are loaded from inside the row (rows have at least eight entries), moved back
-    // where it ends, and put right in put(): no load stands in a branch, where it would be waited for.
-    struct Held {
-      u32x4_t v[C_::CHUNKS];
-      int back[C_::CHUNKS];   // entries that the start was moved back; 8: all of it lies outside
+    auto put_one = [&](int i, const Held& f, char* stage) __attribute__((always_inline)) {
+      bool of_a;
+      int r, c;
+      place(i, of_a, r, c);
+      const bool t = of_a ? C_::AT : C_::BT;
+      const int at = (of_a ? 0 : C_::A_BYTES) + (t ? r * 2 * (of_a ? BM : BN) + ((c ^ (4 * (r & 3))) << 4) : gemm::krow_off(r, c));
+      *reinterpret_cast<u32x4_t*>(stage + at) = f.v[i];
     };
-    auto fetch = [&](int s, Held& f) __attribute__((always_inline)) {
-      const int seg = MASKED ? (s >= per ? 1 : 0) : s;
-      const int64_t k0 = int64_t(MASKED ? s - seg * per : per) * PER_STEP;
+    // entries down by `back`, zeros behind them
+    auto shift = [&](Held& f) __attribute__((always_inline)) {
 #pragma unroll
       for (int i = 0; i < C_::CHUNKS; ++i) {
-        bool of_a;
-        int r, c;
-        place(i, of_a, r, c);
-        const bool t = of_a ? C_::AT : C_::BT;
-        const bool second = of_a || !C_::DUAL ? seg != 0 : is_up(r);
-        const char* base = of_a ? (second ? g.A[1] : g.A[0]) : (second ? g.B[1] : g.B[0]);
-        const int64_t ld = of_a ? g.lda : g.ldb, end = of_a ? g.m : g.n;
-        // row of memory, entry in it, and how long the row is
-        const int64_t row = t ? min(k0 + r, g.K - 1) : of_a ? m0 + min(r, mlast) : n0 + min(col_of(r), nlast);
-        const int64_t at = t ? (of_a ? m0 : n0) + 8 * c : k0 + 8 * c, len = t ? end : g.K;
-        const bf16_t* p = reinterpret_cast<const bf16_t*>(base + row * ld);
-        const bool out_of = at >= len || (t && k0 + r >= g.K);
-        const int64_t from = min(at, len - 8);
-        const uint4 v = load16(p + from);
-        f.v[i] = u32x4_t{v.x, v.y, v.z, v.w};
-        f.back[i] = out_of ? 8 : int(at - from);
+        const int by = f.back[i];
+        u32x4_t v = f.v[i];
+        if (by & 4) v = u32x4_t{v[2], v[3], 0, 0};
+        if (by & 2) v = u32x4_t{v[1], v[2], v[3], 0};
+        if (by & 1) v = u32x4_t{(v[0] >> 16) | (v[1] << 16), (v[1] >> 16) | (v[2] << 16), (v[2] >> 16) | (v[3] << 16), v[3] >> 16};
+        if (by >= 8) v = u32x4_t{0, 0, 0, 0};
+        f.v[i] = v;
       }
     };
-    auto put = [&](Held& f, char* stage) __attribute__((always_inline)) {
-#pragma unroll
-      for (int i = 0; i < C_::CHUNKS; ++i) {
-        bool of_a;
-        int r, c;
-        place(i, of_a, r, c);
-        const bool t = of_a ? C_::AT : C_::BT;
-        const int side = of_a ? BM : BN;
-        if (f.back[i] != 0) {   // at the ends only: entries down by `back`, zeros behind them
-          const int by = f.back[i];
-          u32x4_t v = f.v[i];
-          if (by & 4) v = u32x4_t{v[2], v[3], 0, 0};
-          if (by & 2) v = u32x4_t{v[1], v[2], v[3], 0};
-          if (by & 1) v = u32x4_t{(v[0] >> 16) | (v[1] << 16), (v[1] >> 16) | (v[2] << 16), (v[2] >> 16) | (v[3] << 16), v[3] >> 16};
-          if (by >= 8) v = u32x4_t{0, 0, 0, 0};
-          f.v[i] = v;
-        }
-        const int at = (of_a ? 0 : C_::A_BYTES) + (t ? r * 2 * side + ((c ^ (4 * (r & 3))) << 4) : gemm::krow_off(r, c));
-        *reinterpret_cast<u32x4_t*>(stage + at) = f.v[i];
-      }
-    };
-    // Step s is read from stage s % 2 while the registers of step s + 1 go to the other one and
-    // the loads of step s + 2 are under way.
-    if (first < last) {
+
+    if constexpr (MASKED) {
+      // Whole steps [s0, s1).  At step s: the operands of s are in registers, stage (s + 1) % 2 is
+      // written, the loads of s + 2 and s + 3 are under way; its products go with the reads of the
+      // next operands, the writes of step s + 2 and the loads of step s + 4.
+      uint32_t off[C_::CHUNKS];
       Held h0, h1;
-      Frags f;
-      __syncthreads();   // everybody is done with the ring
-      fetch(first, h0);
-      if (first + 1 < last) fetch(first + 1, h1);
-      put(h0, lds);
-      ring_barrier_lds();
-      auto step = [&](int s, Held& next, Held& free) __attribute__((always_inline)) {
-        const char* st = lds + ((s - first) & 1) * C_::STAGE;
-        if (s + 2 < last) fetch(s + 2, free);
+      bool ends = false;
 #pragma unroll
-        for (int q = 0; q < READS; ++q) read_one(q, st, f);
-        mma(f, [](int) {});
-        if (s + 1 < last) put(next, lds + ((s + 1 - first) & 1) * C_::STAGE);
-        ring_barrier_lds();
+      for (int i = 0; i < C_::CHUNKS; ++i) {
+        bool of_a;
+        int r, c;
+        place(i, of_a, r, c);
+        const int64_t len = (of_a ? g.m : g.n) - (of_a ? m0 : n0);   // of a k-row from the tile's first column
+        int from = 8 * c, back = 0;
+        if (of_a ? C_::AT : C_::BT) {
+          from = int(min(int64_t(from), len - 8));   // may lie before the tile: rows have eight entries
+          back = min(8 * c - from, 8);
+          off[i] = uint32_t(r) * uint32_t(of_a ? g.lda : g.ldb) + uint32_t(from * 2 + 16);
+        } else {
+          off[i] = uint32_t(of_a ? min(r, mlast) : min(col_of(r), nlast)) * uint32_t(of_a ? g.lda : g.ldb) + uint32_t(from * 2 + 16);
+        }
+        h0.back[i] = h1.back[i] = back;
+        ends |= back != 0;
+      }
+      ends = __any(ends);
+      const int64_t a_start = C_::AT ? m0 * 2 : m0 * g.lda, b_start = C_::BT ? n0 * 2 : n0 * g.ldb;
+      const int64_t a_step = C_::AT ? 32 * g.lda : 64, b_step = C_::BT ? 32 * g.ldb : 64;
+      auto fetch = [&](int s, Held& f) __attribute__((always_inline)) {
+        const int seg = s >= per ? 1 : 0, k = s - seg * per;
+        // 16 bytes early, as off is 16 bytes late
+        const char* pa = scalar((seg ? g.A[1] : g.A[0]) + a_start + k * a_step - 16);
+        const char* pb0 = scalar((!C_::DUAL && seg ? g.B[1] : g.B[0]) + b_start + k * b_step - 16);
+        const char* pb1 = scalar(g.B[1] + b_start + k * b_step - 16);
+#pragma unroll
+        for (int i = 0; i < C_::CHUNKS; ++i) {
+          bool of_a;
+          int r, c;
+          place(i, of_a, r, c);
+          const char* p = of_a ? pa : C_::DUAL && is_up(r) ? pb1 : pb0;
+          const uint4 v = load16(reinterpret_cast<const bf16_t*>(p + off[i]));
+          f.v[i] = u32x4_t{v.x, v.y, v.z, v.w};
+        }
       };
-      for (int s = first; s < last; s += 2) {
-        step(s, h1, h0);
-        if (s + 1 < last) step(s + 1, h0, h1);
+      auto put = [&](Held& f, char* stage) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < C_::CHUNKS; ++i) put_one(i, f, stage);
+      };
+      char* stages[2] = {lds, lds + C_::STAGE};
+      Frags f0, f1;
+      if (s0 < s1) {
+        fetch(s0, h0);
+        if (s0 + 1 < s1) fetch(s0 + 1, h1);
+        if (ends) shift(h0);
+        put(h0, stages[0]);
+        if (s0 + 2 < s1) fetch(s0 + 2, h0);
+        if (s0 + 1 < s1) {
+          if (ends) shift(h1);
+          put(h1, stages[1]);
+        }
+        if (s0 + 3 < s1) fetch(s0 + 3, h1);
+        ring_barrier_lds();
+#pragma unroll
+        for (int q = 0; q < READS; ++q) read_one(q, stages[0], f0);
+      }
+      constexpr int RPM = (READS + N * 3 / 4 - 1) / (N * 3 / 4);
+      auto steady = [&](int s, const Frags& cur, Frags& nxt, Held& h, char* own, const char* other) __attribute__((always_inline)) {
+        ring_barrier_lds();
+        if (ends) shift(h);
+        mma(cur, [&](int n) __attribute__((always_inline)) {
+#pragma unroll
+          for (int r = 0; r < RPM; ++r)
+            if (RPM * n + r < READS) read_one(RPM * n + r, other, nxt);
+#pragma unroll
+          for (int i = 0; i < C_::CHUNKS; ++i)
+            if (i * (N / 2) / C_::CHUNKS == n) put_one(i, h, own);
+          if (n == N / 2) fetch(s + 4, h);
+        });
+      };
+      auto drain = [&](int s, const Frags& cur, Frags& nxt, Held& h, char* own, const char* other) __attribute__((always_inline)) {
+        ring_barrier_lds();
+        if (s + 1 < s1)
+#pragma unroll
+          for (int q = 0; q < READS; ++q) read_one(q, other, nxt);
+        if (s + 2 < s1) {
+          if (ends) shift(h);
+          put(h, own);
+        }
+        if (s + 4 < s1) fetch(s + 4, h);
+        mma(cur, [](int) {});
+      };
+      int s = s0;
+      for (; s + 5 < s1; s += 2) {
+        steady(s, f0, f1, h0, stages[0], stages[1]);
+        steady(s + 1, f1, f0, h1, stages[1], stages[0]);
+      }
+      for (; s < s1; s += 2) {
+        drain(s, f0, f1, h0, stages[0], stages[1]);
+        if (s + 1 < s1) drain(s + 1, f1, f0, h1, stages[1], stages[0]);
       }
     }
+
+    // the partial last step of every segment
+    if (tail && g.K % PER_STEP != 0)
+      for (int seg = 0; seg < g.segs; ++seg) {
+        const int64_t k0 = int64_t(per) * PER_STEP;
+        Held f;
+#pragma unroll
+        for (int i = 0; i < C_::CHUNKS; ++i) {
+          bool of_a;
+          int r, c;
+          place(i, of_a, r, c);
+          const bool t = of_a ? C_::AT : C_::BT;
+          const bool second = of_a || !C_::DUAL ? seg != 0 : is_up(r);
+          const char* base = of_a ? (second ? g.A[1] : g.A[0]) : (second ? g.B[1] : g.B[0]);
+          const int64_t ld = of_a ? g.lda : g.ldb, end = of_a ? g.m : g.n;
+          // row of memory, entry in it, and how long the row is
+          const int64_t row = t ? min(k0 + r, g.K - 1) : of_a ? m0 + min(r, mlast) : n0 + min(col_of(r), nlast);
+          const int64_t at = t ? (of_a ? m0 : n0) + 8 * c : k0 + 8 * c, len = t ? end : g.K;
+          const bool out_of = at >= len || (t && k0 + r >= g.K);
+          const int64_t from = min(at, len - 8);
+          const uint4 v = load16(reinterpret_cast<const bf16_t*>(base + row * ld) + from);
+          f.v[i] = u32x4_t{v.x, v.y, v.z, v.w};
+          f.back[i] = out_of ? 8 : int(at - from);
+        }
+        __syncthreads();   // everybody is done with the stage
+        shift(f);
+#pragma unroll
+        for (int i = 0; i < C_::CHUNKS; ++i) put_one(i, f, lds);
+        __syncthreads();
+        Frags fr_;
+#pragma unroll
+        for (int q = 0; q < READS; ++q) read_one(q, lds, fr_);
+        mma(fr_, [](int) {});
+      }
   }
 
   // The tile leaves through LDS, 32 rows at a time and each wave through its own part of the
@@ -538,7 +624,7 @@ __global__ __launch_bounds__(C_::NT) void tile_kernel(Source g, Out out, Split s
   const int z = __builtin_amdgcn_readfirstlane(int(u / tiles % sp.batch));
   int64_t tm, tn;
   tile_at(u % tiles, TM, TN, tm, tn);
-  const int steps = __builtin_amdgcn_readfirstlane(int((MASKED ? (g.K + PER_STEP - 1) / PER_STEP : g.K / PER_STEP) * g.segs));
+  const int steps = __builtin_amdgcn_readfirstlane(int(g.K / PER_STEP * g.segs));
   const Source s = source_at(g, z);
   if constexpr (SPLIT) {
     // a part's tiles are neighbours
@@ -759,12 +845,16 @@ struct Plan {
   PlanKind kind;
   int parts;
 };
-// m, n at least 1; rows_only: both operands lie in rows, a_rows: A does
-inline Plan plan_product(int64_t m, int64_t n, int64_t steps, int mats, int batch, bool rows_only, bool a_rows = true) {
-  if (m <= 16 && rows_only) return {kDirect, 1};
+// m, n at least 1; rows_only: both operands lie in rows, a_rows: A does; whole: the DMA can copy
+// (rows start at 16 bytes).  Otherwise narrow tiles have 128 columns and single rows take them too:
+// the direct kernel's loads of 64 bytes from each row, off any boundary, are four times slower
+// (8 x 14335 x 4095: 186 us against 59).  Steps through registers wait for memory, so two units
+// per CU are worth their sums there.
+inline Plan plan_product(int64_t m, int64_t n, int64_t steps, int mats, int batch, bool whole, bool rows_only, bool a_rows = true) {
+  if (m <= 16 && rows_only && whole) return {kDirect, 1};
   const int64_t cols = n * mats;
-  const int64_t narrow = ceil_div(m, 64) * ceil_div(cols, rows_only ? 64 : 128) * batch, small = ceil_div(m, 128) * ceil_div(cols, 128) * batch;
-  auto parts = [&](int64_t tiles) { return int(std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(16, steps / 16), kCus / tiles))); };
+  const int64_t narrow = ceil_div(m, 64) * ceil_div(cols, rows_only && whole ? 64 : 128) * batch, small = ceil_div(m, 128) * ceil_div(cols, 128) * batch;
+  auto parts = [&](int64_t tiles) { return int(std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(16, steps / 16), (whole ? 1 : 2) * kCus / tiles))); };
   if (a_rows && (m <= 64 || (2 * small <= kCus && narrow <= kCus))) return {kNarrow, parts(narrow)};
   if (2 * small <= kCus || 2 * ceil_div(m, 256) * ceil_div(cols, 256) * batch < kCus) return {kSmall, parts(small)};
   return {kLarge, 1};
