@@ -842,14 +842,30 @@ def _act_code(act: str) -> int:
     return code
 
 
-def _same_device(first: torch.Tensor, *rest: Optional[torch.Tensor]) -> None:
-    """All tensors on one device, the current one, whose stream and pool the call uses."""
+def _same_device(first: torch.Tensor, *rest: Optional[torch.Tensor]) -> int:
+    """The one device of all tensors: the current one, whose stream and pool the call uses."""
     where = first.get_device()
     for t in rest:
         if t is not None and t.get_device() != where:
             raise ValueError("all tensors must be on one device")
-    if where >= 0 and where != torch.cuda.current_device():
+    if where < 0:
+        raise ValueError("the tensors must be device tensors")
+    if where != torch.cuda.current_device():
         raise ValueError(f"the tensors are on cuda:{where}, which is not the current device (use torch.cuda.device)")
+    return where
+
+
+def _stream_on(stream, where: int) -> int:
+    """As _stream, for a call whose device is known to be the current one."""
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(where)
+    return _stream(stream)
+
+
+def _two_sides(t: torch.Tensor, name: str) -> Tuple[int, int]:
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D")
+    return t.shape
 
 
 def _matrix(t: torch.Tensor, dtype: torch.dtype, rows: int, cols: int, name: str) -> Tuple[int, int]:
@@ -858,6 +874,8 @@ def _matrix(t: torch.Tensor, dtype: torch.dtype, rows: int, cols: int, name: str
         raise TypeError(f"{name} must be {dtype}")
     if t.shape != (rows, cols):
         raise ValueError(f"{name} must be [{rows}, {cols}]")
+    if t.is_contiguous():
+        return t.data_ptr(), cols
     ptr, ld = _rows2(t, name)
     return ptr, ld if ld > cols else cols
 
@@ -889,8 +907,8 @@ def _int8_operand(q: torch.Tensor, s: torch.Tensor, rows: int, cols: int, name: 
     """(codes, pitch, scales) of an int8 matrix that holds rows x cols."""
     if q.dtype != torch.int8:
         raise TypeError(f"{name} must be int8")
-    ptr, ld = _rows2(q, name)
-    held, width = q.shape
+    held, width = _two_sides(q, name)
+    ptr, ld = (q.data_ptr(), width) if q.is_contiguous() else _rows2(q, name)
     need = _ceil_to(cols, MUON_INT8_STEP)
     if held != rows or width < need:
         raise ValueError(f"{name} must hold {rows} rows of at least {need} codes")
@@ -903,11 +921,11 @@ def _int8_operand(q: torch.Tensor, s: torch.Tensor, rows: int, cols: int, name: 
 
 def int8_quantize(x: torch.Tensor, q: torch.Tensor, s: torch.Tensor, stream=None) -> None:
     """Codes and scales of ``x`` [rows, cols] into (q, s): ``x / s`` rounded to nearest even, s = max |row| * (1 / 127)."""
-    _same_device(x, q, s)
+    where = _same_device(x, q, s)
     xp, ldx = _rows2(x, "x")
     rows, cols = x.shape
     qp, ldq, sp = _int8_operand(q, s, rows, cols, "q")
-    status = lib().int8_quantize(xp, dtype_code(x), rows, cols, ldx if ldx > cols else cols, qp, ldq, sp, _stream(stream))
+    status = lib().int8_quantize(xp, dtype_code(x), rows, cols, ldx if ldx > cols else cols, qp, ldq, sp, _stream_on(stream, where))
     if status:
         _check("int8_quantize", status)
 
@@ -925,17 +943,17 @@ def int8_glu_workspace_bytes(m: int, n: int, K: int) -> int:
 def int8_gemm(A: torch.Tensor, sa: torch.Tensor, B: torch.Tensor, sb: torch.Tensor, C: torch.Tensor,
               workspace: Optional[torch.Tensor] = None, stream=None) -> None:
     """``C = (A B^T) sa sb`` for int8 operands (codes, scales) with K = ``A.shape[1]`` columns; C fp32 or bf16."""
-    _same_device(C, A, sa, B, sb, workspace)
+    where = _same_device(C, A, sa, B, sb, workspace)
     m, K = A.shape
     n, kb = B.shape
     if kb != K or K % MUON_INT8_STEP or C.shape != (m, n):
         raise ValueError(f"A is m x K, B n x K and C m x n, K a multiple of {MUON_INT8_STEP}")
     ap, lda, sap = _int8_operand(A, sa, m, K, "A")
     bp, ldb, sbp = _int8_operand(B, sb, n, K, "B")
-    cp, ldc = _rows2(C, "C")
+    cp, ldc = (C.data_ptr(), n) if C.is_contiguous() else _rows2(C, "C")
     workspace, ws, nbytes = _space(int8_gemm_workspace_bytes(m, n, K), C, workspace, stream)
     status = lib().int8_gemm(ap, lda, sap, bp, ldb, sbp, cp, dtype_code(C), ldc if ldc > n else n, m, n, K, ws, nbytes,
-                             _stream(stream))
+                             _stream_on(stream, where))
     if status:
         _check("int8_gemm", status)
 
@@ -943,7 +961,7 @@ def int8_gemm(A: torch.Tensor, sa: torch.Tensor, B: torch.Tensor, sb: torch.Tens
 def int8_glu(A: torch.Tensor, sa: torch.Tensor, Bg: torch.Tensor, sg: torch.Tensor, Bu: torch.Tensor, su: torch.Tensor,
              H: torch.Tensor, act: str = "silu", workspace: Optional[torch.Tensor] = None, stream=None) -> None:
     """``H = act(g) * u``, ``g = (A Bg^T) sa sg`` and ``u = (A Bu^T) sa su``, for int8 operands; H fp32 or bf16."""
-    _same_device(H, A, sa, Bg, sg, Bu, su, workspace)
+    where = _same_device(H, A, sa, Bg, sg, Bu, su, workspace)
     m, K = A.shape
     n, kb = Bg.shape
     if kb != K or K % MUON_INT8_STEP or Bu.shape != (n, K) or H.shape != (m, n):
@@ -953,10 +971,10 @@ def int8_glu(A: torch.Tensor, sa: torch.Tensor, Bg: torch.Tensor, sg: torch.Tens
     up, ldu, sup = _int8_operand(Bu, su, n, K, "Bu")
     if ldg != ldu:
         raise ValueError("Bg and Bu must have one row pitch")
-    hp, ldh = _rows2(H, "H")
+    hp, ldh = (H.data_ptr(), n) if H.is_contiguous() else _rows2(H, "H")
     workspace, ws, nbytes = _space(int8_glu_workspace_bytes(m, n, K), H, workspace, stream)
     status = lib().int8_glu(ap, lda, sap, gp, sgp, up, sup, ldg, _act_code(act), hp, dtype_code(H), ldh if ldh > n else n, m, n, K,
-                            ws, nbytes, _stream(stream))
+                            ws, nbytes, _stream_on(stream, where))
     if status:
         _check("int8_glu", status)
 
@@ -980,16 +998,10 @@ def glu_weight_grad_workspace_bytes(tokens: int, out: int, inp: int) -> int:
     return int(lib().glu_weight_grad_workspace_bytes(tokens, out, inp))
 
 
-def _two_sides(t: torch.Tensor, name: str) -> Tuple[int, int]:
-    if t.dim() != 2:
-        raise ValueError(f"{name} must be 2-D")
-    return t.shape
-
-
 def glu_forward(x: torch.Tensor, wg: torch.Tensor, wu: torch.Tensor, h: torch.Tensor, g: Optional[torch.Tensor] = None,
                 u: Optional[torch.Tensor] = None, act: str = "silu", workspace: Optional[torch.Tensor] = None, stream=None) -> None:
     """``h = act(x wg^T) * (x wu^T)`` in bf16; ``g`` and ``u`` (both or neither) receive the two products for the backward."""
-    _same_device(h, x, wg, wu, g, u, workspace)
+    where = _same_device(h, x, wg, wu, g, u, workspace)
     tokens, inp = _two_sides(x, "x")
     out = _two_sides(wg, "wg")[0]
     if (g is None) != (u is None):
@@ -1001,7 +1013,7 @@ def glu_forward(x: torch.Tensor, wg: torch.Tensor, wu: torch.Tensor, h: torch.Te
     sg, su, lds = _pair(g, u, bf, tokens, out, "g and u") if g is not None else (None, None, 0)
     workspace, ws, nbytes = _space(glu_forward_workspace_bytes(tokens, out, inp), h, workspace, stream)
     status = lib().glu_forward(xp, ldx, gp, up, ldw, _act_code(act), hp, ldh, sg, su, lds, tokens, out, inp, ws, nbytes,
-                               _stream(stream))
+                               _stream_on(stream, where))
     if status:
         _check("glu_forward", status)
 
@@ -1012,7 +1024,7 @@ def glu_backward(dh: torch.Tensor, g: torch.Tensor, u: torch.Tensor, dg: torch.T
     """``dg = dh u act'(g)``, ``du = dh act(g)``; ``dx = dg wg + du wu`` where ``dx`` is given, and ``h`` again where it is.
 
     dg, du and h may each be dh, g or u itself."""
-    _same_device(dh, g, u, dg, du, wg, wu, dx, h, workspace)
+    where = _same_device(dh, g, u, dg, du, wg, wu, dx, h, workspace)
     tokens, out = _two_sides(dh, "dh")
     if (wg is None) != (wu is None) or (dx is not None and wg is None):
         raise ValueError("dx needs wg and wu")
@@ -1028,7 +1040,7 @@ def glu_backward(dh: torch.Tensor, g: torch.Tensor, u: torch.Tensor, dg: torch.T
         dxp, lddx = _matrix(dx, bf, tokens, inp, "dx")
         workspace, ws, nbytes = _space(glu_backward_workspace_bytes(tokens, out, inp), dx, workspace, stream)
     status = lib().glu_backward(dhp, lddh, gp, up, ldg, _act_code(act), dgp, dup, ldd, hp, ldh, wgp, wup, ldw, dxp, lddx, tokens,
-                                out, inp, ws, nbytes, _stream(stream))
+                                out, inp, ws, nbytes, _stream_on(stream, where))
     if status:
         _check("glu_backward", status)
 
@@ -1036,7 +1048,7 @@ def glu_backward(dh: torch.Tensor, g: torch.Tensor, u: torch.Tensor, dg: torch.T
 def glu_weight_grad(dg: torch.Tensor, du: torch.Tensor, x: torch.Tensor, mg: torch.Tensor, mu: torch.Tensor, alpha: float = 1.0,
                     beta: float = 0.0, workspace: Optional[torch.Tensor] = None, stream=None) -> None:
     """``mg <- beta mg + alpha dg^T x`` and ``mu <- beta mu + alpha du^T x``, mg and mu fp32 or bf16."""
-    _same_device(mg, mu, dg, du, x, workspace)
+    where = _same_device(mg, mu, dg, du, x, workspace)
     tokens, out = _two_sides(dg, "dg")
     inp = _two_sides(x, "x")[1]
     bf = torch.bfloat16
@@ -1046,6 +1058,6 @@ def glu_weight_grad(dg: torch.Tensor, du: torch.Tensor, x: torch.Tensor, mg: tor
     gp, up, ldm = _pair(mg, mu, mg.dtype, out, inp, "mg and mu")
     workspace, ws, nbytes = _space(glu_weight_grad_workspace_bytes(tokens, out, inp), mg, workspace, stream)
     status = lib().glu_weight_grad(dgp, dup, ldd, xp, ldx, gp, up, code, ldm, tokens, out, inp, alpha, beta, ws, nbytes,
-                                   _stream(stream))
+                                   _stream_on(stream, where))
     if status:
         _check("glu_weight_grad", status)

@@ -836,7 +836,7 @@ constexpr int64_t kCus = 256;
 //  small   128 x 128 tiles where 256 x 256 ones would leave more than half the CUs idle
 //  large   256 x 256 tiles, the last round in halves or quarters
 // Narrow and small tiles that are no more than half the CUs are cut along the contraction into
-// `parts` of 16 steps or more, so that there is at most one unit per CU; a second kernel joins them.
+// `parts` of 20 steps or more, so that there is at most one unit per CU; a second kernel joins them.
 // Two units per CU, as long, share its matrix cores and LDS and write twice the sums: backward to
 // the input of 777 x 2304 x 768, 42 small tiles in 6 parts 28.6 us, in 13 34.1, 78 narrow ones in 3
 // 25.5, in 6 32.0; 33 x 4096 x 14336 int8, 64 narrow tiles in 4 parts 20.5, in 8 23.1.
@@ -854,7 +854,7 @@ inline Plan plan_product(int64_t m, int64_t n, int64_t steps, int mats, int batc
   if (m <= 16 && rows_only && whole) return {kDirect, 1};
   const int64_t cols = n * mats;
   const int64_t narrow = ceil_div(m, 64) * ceil_div(cols, rows_only && whole ? 64 : 128) * batch, small = ceil_div(m, 128) * ceil_div(cols, 128) * batch;
-  auto parts = [&](int64_t tiles) { return int(std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(16, steps / 16), (whole ? 1 : 2) * kCus / tiles))); };
+  auto parts = [&](int64_t tiles) { return int(std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(16, steps / 20), (whole ? 1 : 2) * kCus / tiles))); };
   if (a_rows && (m <= 64 || (2 * small <= kCus && narrow <= kCus))) return {kNarrow, parts(narrow)};
   if (2 * small <= kCus || 2 * ceil_div(m, 256) * ceil_div(cols, 256) * batch < kCus) return {kSmall, parts(small)};
   return {kLarge, 1};
