@@ -53,7 +53,7 @@ struct AxpbyOut {
     if constexpr (READS)
 #pragma unroll
       for (int k = 0; k < N; ++k) o[k] = fmaf(beta, to_f32(p.c[k]), o[k]);
-    store_n<N>(C + row * ldc + col, o);
+    store_n<N, true>(C + row * ldc + col, o);
   }
 };
 
@@ -78,9 +78,9 @@ __device__ __forceinline__ void gradients(const GradArgs& a, int64_t row, int64_
     du[k] = dh[k] * act;
     h[k] = act * u[k];
   }
-  store_n<N>(a.dG + row * a.ldd + col, dg);
-  store_n<N>(a.dU + row * a.ldd + col, du);
-  if (a.H != nullptr) store_n<N>(a.H + row * a.ldh + col, h);
+  store_n<N, false>(a.dG + row * a.ldd + col, dg);
+  store_n<N, false>(a.dU + row * a.ldd + col, du);
+  if (a.H != nullptr) store_n<N, false>(a.H + row * a.ldh + col, h);
 }
 
 // Eight columns of one row per thread.  Bound by memory: 6 bytes read and 4 (6 with h) written

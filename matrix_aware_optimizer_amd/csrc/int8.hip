@@ -212,7 +212,7 @@ struct ScaleOut {
     float o[N];
 #pragma unroll
     for (int k = 0; k < N; ++k) o[k] = float(v[0][k]) * (p.a * c.b[k]);
-    store_n<N>(C + row * ldc + col, o);
+    store_n<N, true>(C + row * ldc + col, o);
   }
 };
 
