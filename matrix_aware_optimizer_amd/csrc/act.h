@@ -93,7 +93,8 @@ __device__ __forceinline__ float activate(int act, float x, float& slope) {
       return x * p;
     }
     case MUON_ACT_GELU_TANH: {
-      const float x2 = x * x, s = logistic(kTanh2C * x * fmaf(kTanhA, x2, 1.0f));
+      // the square is cut so that the slope of a saturated gate is 0 times a number, not 0 times infinity
+      const float x2 = fminf(x * x, 1e30f), s = logistic(kTanh2C * x * fmaf(kTanhA, x2, 1.0f));
       if (SLOPE) slope = fmaf(x * s * (1.0f - s), kTanh2C * fmaf(3.0f * kTanhA, x2, 1.0f), s);
       return x * s;
     }

@@ -42,8 +42,8 @@ class GatedLinear:
         self._codes = None              # (weights' state, codes and scales of Wg, of Wu)
 
     def _state(self):
-        """Changes whenever the weights do, by step() or by torch operations on them."""
-        return self._steps, self.Wg._version, self.Wu._version
+        """Changes whenever the weights do, by step() or by torch operations on them (inference tensors have no such count)."""
+        return (self._steps, *(0 if W.is_inference() else W._version for W in (self.Wg, self.Wu)))
 
     def _flat(self, x: torch.Tensor) -> torch.Tensor:
         if x.dim() != 2 or x.shape[1] != self.Wg.shape[1]:
@@ -87,7 +87,9 @@ class GatedLinear:
         self._accumulating = False
 
     def quantize(self) -> None:
-        """int8 codes of the current weights, for :meth:`answer`."""
+        """int8 codes of the current weights, for :meth:`answer`.
+
+        Call it again after other calls of the library wrote to the weights: those are not noticed."""
         codes = []
         for W in (self.Wg, self.Wu):
             q, s = _abi.int8_buffers(*W.shape, device=W.device)
