@@ -20,9 +20,12 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(x, bf16x2_t));
 }
 
-// 16 bytes at p; PASSING: past the caches' order of keeping.  The large products' outputs pass, so
-// that the operands' panels stay in L2: 2048 x 14336 x 4096 int8 gated 253 -> 245 us, 1999 x 4096 x
-// 14336 140 -> 134, weight gradients 857 -> 849; what the next kernel reads (dg, du) does not.
+// 16 bytes at p; PASSING: past the caches' order of keeping.  The outputs of products on large tiles
+// pass, so that the operands' panels stay in L2: 2048 x 14336 x 4096 int8 gated 253 -> 245 us, 1999
+// x 4096 x 14336 140 -> 134, weight gradients 857 -> 849.  Not what the next kernel reads (dg, du),
+// and not rows that end inside a cache line, whose halves would pass one by one (weight gradients
+// of 14335 x 4095 from 64 tokens 190 -> 235).  A choice of the type: as a branch in the store it costs
+// more than it gains (136 against 129 us for the second).
 template <bool PASSING, typename T>
 __device__ __forceinline__ void store16_as(T* p, const uint4& v) {
   typename Unaligned<T>::x4 w;
@@ -30,6 +33,7 @@ __device__ __forceinline__ void store16_as(T* p, const uint4& v) {
   if constexpr (PASSING) __builtin_nontemporal_store(w, reinterpret_cast<typename Unaligned<T>::x4*>(p));
   else *reinterpret_cast<typename Unaligned<T>::x4*>(p) = w;
 }
+inline bool whole_lines(const void* p, int64_t pitch_bytes) { return (reinterpret_cast<uintptr_t>(p) | uintptr_t(pitch_bytes)) % 128 == 0; }
 // N consecutive outputs at p, rounded once to the stored type
 template <int N, bool PASSING>
 __device__ __forceinline__ void store_n(bf16_t* p, const float (&v)[N]) {
@@ -109,7 +113,7 @@ inline bool valid_act(int a) { return a >= MUON_ACT_SILU && a <= MUON_ACT_RELU; 
 // h = act(g) u of two sums, in H and (for the backward) g and u in G and U.  SCALED: the sums
 // are of int8 codes, g = float(sum) (sa sg), with one rounding of the integer, one of the
 // product of the scales and one of theirs.
-template <typename TC, bool SCALED>
+template <typename TC, bool SCALED, bool PASSING = false>
 struct GluOut {
   using sum_t = std::conditional_t<SCALED, int, float>;
   static constexpr int E = 16 / int(sizeof(TC));
@@ -121,6 +125,8 @@ struct GluOut {
 
   template <int N> struct Cols { float g[SCALED ? N : 1], u[SCALED ? N : 1]; };
   template <int N> struct Pre { float a; };
+  GluOut<TC, SCALED, SCALED> passing() const { return {H, G, U, ldh, ldg, width, act, sa, sg, su}; }
+  bool lines() const { return whole_lines(H, ldh * int64_t(sizeof(TC))); }
   __device__ __forceinline__ GluOut at(int) const { return *this; }
   template <int N> __device__ __forceinline__ Cols<N> cols(int64_t col) const {
     Cols<N> c;
@@ -159,7 +165,7 @@ struct GluOut {
         MUON_ACT_CASE(MUON_ACT_RELU)
 #undef MUON_ACT_CASE
     }
-    store_n<N, SCALED>(H + row * ldh + col, h);
+    store_n<N, PASSING>(H + row * ldh + col, h);
     if (!SCALED && G != nullptr) {
       store_n<N, false>(G + row * ldg + col, g);
       store_n<N, false>(U + row * ldg + col, u);

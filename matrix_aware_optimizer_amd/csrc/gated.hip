@@ -17,7 +17,7 @@ using tile::ceil_div;
 using tile::kBf16;
 
 // C <- beta C + alpha sum (READS) or alpha sum, one rounding to the stored type; z says which of two outputs
-template <typename TC, bool READS>
+template <typename TC, bool READS, bool PASSING = false>
 struct AxpbyOut {
   using sum_t = float;
   static constexpr int E = 16 / int(sizeof(TC));
@@ -27,20 +27,22 @@ struct AxpbyOut {
 
   template <int N> struct Cols {};
   template <int N> struct Pre { TC c[READS ? N : 1]; };
+  AxpbyOut<TC, READS, true> passing() const { return {C, C1, ldc, width, alpha, beta}; }
+  bool lines() const { return whole_lines(C, ldc * int64_t(sizeof(TC))) && whole_lines(C1, 0); }
   __device__ __forceinline__ AxpbyOut at(int z) const {
     AxpbyOut o = *this;
     if (z) o.C = C1;
     return o;
   }
   template <int N> __device__ __forceinline__ Cols<N> cols(int64_t) const { return {}; }
-  // read once, past the caches' order of keeping (weight gradients of the largest case 848 -> 833 us)
+  // read once; PASSING: past the caches' order of keeping (weight gradients of the largest case 848 -> 833 us)
   template <int N> __device__ __forceinline__ Pre<N> pre(int64_t row, int64_t col) const {
     Pre<N> p;
     if constexpr (READS) {
       const TC* src = C + row * ldc + col;
       if constexpr (N * sizeof(TC) == 16) {
-        const auto v = __builtin_nontemporal_load(reinterpret_cast<const typename Unaligned<TC>::x4*>(src));
-        p = __builtin_bit_cast(Pre<N>, v);
+        if constexpr (PASSING) p = __builtin_bit_cast(Pre<N>, __builtin_nontemporal_load(reinterpret_cast<const typename Unaligned<TC>::x4*>(src)));
+        else p = __builtin_bit_cast(Pre<N>, load16(src));
       }
       else if constexpr (N * sizeof(TC) == 8) p = __builtin_bit_cast(Pre<N>, load8(src));
       else
@@ -57,7 +59,7 @@ struct AxpbyOut {
     if constexpr (READS)
 #pragma unroll
       for (int k = 0; k < N; ++k) o[k] = fmaf(beta, to_f32(p.c[k]), o[k]);
-    store_n<N, true>(C + row * ldc + col, o);
+    store_n<N, PASSING>(C + row * ldc + col, o);
   }
 };
 
@@ -115,7 +117,7 @@ int launch_tiled(const tile::Source& g, const Out& out, const tile::Plan& plan, 
                  : tile::launch_sized<tile::Config<kBf16, 128, 128, 64, 64, 3, AT, BT, DUAL>, true>(g, out, sp, st);
   if constexpr (!DUAL)
     if (!whole) return tile::launch_tiles<tile::Config<kBf16, 256, 256, 128, 128, 3, AT, BT, DUAL>, true, false>(g, out, sp, st);
-  return tile::launch_mixed<kBf16, AT, BT, DUAL>(g, out, sp.batch, st);
+  return tile::launch_large<kBf16, AT, BT, DUAL>(g, out, sp, st);
 }
 
 bool sides_ok(int64_t tokens, int64_t out, int64_t in) {

@@ -189,7 +189,7 @@ int quantize(const QuantArgs& g, hipStream_t st) {
 // ---------------------------------------------------------------------------
 // C = float(sum) (sa sb): one rounding of the integer, one of the product of the scales, one of
 // theirs, and one to C
-template <typename TC>
+template <typename TC, bool PASSING = false>
 struct ScaleOut {
   using sum_t = int;
   static constexpr int E = 16 / int(sizeof(TC));
@@ -199,6 +199,8 @@ struct ScaleOut {
 
   template <int N> struct Cols { float b[N]; };
   template <int N> struct Pre { float a; };
+  ScaleOut<TC, true> passing() const { return {C, ldc, width, sa, sb}; }
+  bool lines() const { return whole_lines(C, ldc * int64_t(sizeof(TC))); }
   __device__ __forceinline__ ScaleOut at(int) const { return *this; }
   template <int N> __device__ __forceinline__ Cols<N> cols(int64_t col) const {
     Cols<N> c;
@@ -212,7 +214,7 @@ struct ScaleOut {
     float o[N];
 #pragma unroll
     for (int k = 0; k < N; ++k) o[k] = float(v[0][k]) * (p.a * c.b[k]);
-    store_n<N, true>(C + row * ldc + col, o);
+    store_n<N, PASSING>(C + row * ldc + col, o);
   }
 };
 
@@ -229,7 +231,7 @@ int launch_product(const tile::Source& g, const Out& out, const tile::Plan& plan
     case tile::kSmall:
       return tile::launch_sized<tile::Config<kI8, 128, 128, 64, 64, 4, false, false, DUAL>, false>(g, out, sp, st);
     default:
-      return tile::launch_mixed<kI8, false, false, DUAL>(g, out, 1, st);
+      return tile::launch_large<kI8, false, false, DUAL>(g, out, sp, st);
   }
 }
 

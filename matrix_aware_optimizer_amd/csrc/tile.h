@@ -898,6 +898,14 @@ int launch_sized(const Source& g, const Out& out, const Split& sp, hipStream_t s
   return sp.parts > 1 ? launch_tiles<C_, MASKED, true>(g, out, sp, st) : launch_tiles<C_, MASKED, false>(g, out, sp, st);
 }
 
+// large tiles: outputs of whole cache lines pass the caches, others go out in whole tiles only
+template <int KIND, bool AT, bool BT, bool DUAL, class Out>
+int launch_large(const Source& g, const Out& out, const Split& sp, hipStream_t st) {
+  using Passing = decltype(out.passing());
+  if constexpr (std::is_same_v<Passing, Out>) return launch_mixed<KIND, AT, BT, DUAL>(g, out, sp.batch, st);
+  if (out.lines()) return launch_mixed<KIND, AT, BT, DUAL>(g, out.passing(), sp.batch, st);
+  return launch_tiles<Config<KIND, 256, 256, 128, 128, 4, AT, BT, DUAL>, false, false>(g, out, sp, st);
+}
 template <int NB, class Out>
 int launch_plain(const Source& g, const Out& out, int batch, bool a_kmajor, bool b_kmajor, hipStream_t st) {
   const int64_t blocks = ceil_div(g.m * g.n * batch, 256);

@@ -152,7 +152,7 @@ def check_forward(t, f, d, act="silu", saved=True, pad=0, seed=1):
 # one case for each way a product is cut, borders of the tiles, odd sides (rows that do not start at 16 bytes)
 FORWARD = [(1, 1, 1), (1, 16, 32), (1, 17, 40), (3, 100, 65), (16, 257, 1000), (2, 33, 4096), (5, 4096, 768), (17, 64, 8), (17, 65, 31),
            (40, 200, 8192), (64, 1152, 768), (33, 2304, 100), (65, 64, 32), (100, 1000, 328), (129, 129, 97), (130, 96, 4104), (200, 384, 4096),
-           (777, 2304, 768), (300, 301, 303), (1999, 72, 256), (2049, 2052, 360), (1100, 4096, 200)]
+           (777, 2304, 768), (300, 301, 303), (1999, 72, 256), (2049, 2052, 360), (1100, 4096, 200), (2100, 4100, 263), (2500, 2304, 1000)]
 
 
 @pytest.mark.gpu
@@ -219,7 +219,7 @@ def check_backward(t, f, d, act="silu", again=True, pad=0, seed=1, input=True):
 
 BACKWARD = [(1, 1, 1), (1, 32, 8), (1, 40, 16), (3, 100, 65), (16, 1000, 256), (17, 31, 64), (40, 4096, 200), (64, 768, 1152), (33, 104, 2304),
             (65, 32, 64), (100, 328, 1000), (129, 97, 129), (200, 4096, 384), (777, 2304, 768), (300, 303, 301), (1999, 256, 72), (2049, 360, 4104),
-            (4100, 296, 4096)]
+            (4100, 296, 4096), (2100, 2303, 4096), (2100, 1100, 4095), (2049, 320, 4096)]
 
 
 @pytest.mark.gpu
@@ -294,7 +294,8 @@ def check_weights(t, f, d, out="f32", beta=0.95, alpha=0.05, pad=0, seed=1):
         assert (got[:, d:] == 7.0).all()
 
 
-WEIGHTS = [(1, 1, 1), (1, 8, 8), (2, 40, 16), (31, 129, 65), (32, 128, 128), (33, 136, 72), (100, 328, 1000), (777, 2304, 768), (777, 301, 303),
+# large tiles with whole lines, without (2056 and 4104 columns), through registers (4095 columns, long sums)
+WEIGHTS = [(2100, 2304, 4095), (300, 2304, 4096), (2080, 4096, 2304), (1, 1, 1), (1, 8, 8), (2, 40, 16), (31, 129, 65), (32, 128, 128), (33, 136, 72), (100, 328, 1000), (777, 2304, 768), (777, 301, 303),
            (8192, 256, 136), (5000, 100, 64), (64, 4104, 2056), (200, 4096, 4096)]
 
 

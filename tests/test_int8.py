@@ -239,9 +239,9 @@ def exact_sum(a, b):
     return a.double() @ b.double().t().contiguous()
 
 
-def check_gemm(m, n, K, out, seed=1, pad=0, low=-127):
+def check_gemm(m, n, K, out, seed=1, pad=0, low=-127, more=5):
     (a, sa), (b, sb) = codes(m, K, seed, pad, low), codes(n, K, seed + 1, pad, low)
-    c = torch.full((m, n + 5), 7.0, dtype=DT[out], device="cuda")
+    c = torch.full((m, n + more), 7.0, dtype=DT[out], device="cuda")
     mao.int8_gemm(a, sa, b, sb, c[:, :n])
     ref = exact_sum(a, b) * sa.double()[:, None] * sb.double()
     err = (c[:, :n].double() - ref).abs()
@@ -267,6 +267,15 @@ def test_gemm(m, n, K, out):
 @pytest.mark.parametrize("m,n,K", [(7, 50, 500), (60, 300, 500), (300, 300, 500)])
 def test_gemm_pitches(m, n, K):
     check_gemm(m, n, K, "f32", seed=5, pad=48)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("m,n,K", [(2049, 4096, 704), (1100, 8192, 512), (3000, 2560, 128)])
+def test_outputs_of_whole_lines(m, n, K, out):
+    """Large tiles, whose outputs take another way to memory where rows are whole cache lines; last rounds in halves and quarters."""
+    check_gemm(m, n, K, out, seed=3, more=0)
+    check_glu(m, n // 2, K, "silu", out, seed=4, more=0)
 
 
 @pytest.mark.gpu
@@ -312,11 +321,11 @@ def test_a_row_that_was_not_finite_stays_visible(m):
         assert torch.isnan(c[m - 1]).all() and torch.isfinite(c[:m - 1]).all()
 
 
-def check_glu(m, n, K, act, out, seed=2, pad=0):
+def check_glu(m, n, K, act, out, seed=2, pad=0, more=3):
     (a, sa), (bg, sg), (bu, su) = codes(m, K, seed, pad), codes(n, K, seed + 1, pad), codes(n, K, seed + 2, pad)
     size = 2.0 / (K ** 0.5 * 5400 * 2.0 ** -12)      # g over a few units
     sg, su = sg * size, su * size
-    h = torch.full((m, n + 3), 7.0, dtype=DT[out], device="cuda")
+    h = torch.full((m, n + more), 7.0, dtype=DT[out], device="cuda")
     mao.int8_glu(a, sa, bg, sg, bu, su, h[:, :n], act=act)
     g = exact_sum(a, bg) * sa.double()[:, None] * sg.double()
     u = exact_sum(a, bu) * sa.double()[:, None] * su.double()
