@@ -3,8 +3,8 @@
     python -m matrix_aware_optimizer_amd.build
 
 The library is compiled with hipcc straight from ``csrc/*.hip`` into
-``matrix_aware_optimizer_amd/libmuon.so``.  Packed fp32 instructions are
-disabled for all device code (``-packed-fp32-ops``).
+``matrix_aware_optimizer_amd/libmuon.so``, one process per source.  Packed fp32
+instructions are disabled for all device code (``-packed-fp32-ops``).
 """
 from __future__ import annotations
 
@@ -12,6 +12,8 @@ import os
 import shutil
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 REPO_DIR = os.path.dirname(PKG_DIR)
@@ -38,11 +40,7 @@ def compile_flags() -> list:
     ]
 
 
-def build(verbose: bool = False) -> str:
-    """Compile every HIP source into libmuon.so; returns the library path."""
-    srcs = [os.path.join(CSRC, s) for s in SOURCES]
-    tmp = LIB_PATH + ".tmp"
-    cmd = [hipcc()] + compile_flags() + srcs + ["-o", tmp]
+def _run(cmd: list, verbose: bool) -> None:
     if verbose:
         print(" ".join(cmd), flush=True)
     proc = subprocess.run(cmd, capture_output=True, text=True)
@@ -53,6 +51,18 @@ def build(verbose: bool = False) -> str:
         raise RuntimeError(f"hipcc failed ({proc.returncode}):\n{err}")
     if err.strip() and verbose:
         print(err, file=sys.stderr)
+
+
+def build(verbose: bool = False) -> str:
+    """Compile every HIP source and link libmuon.so; returns the library path."""
+    flags = [f for f in compile_flags() if f != "-shared"]
+    tmp = LIB_PATH + ".tmp"
+    with tempfile.TemporaryDirectory() as objects:
+        outs = [os.path.join(objects, s + ".o") for s in SOURCES]
+        with ThreadPoolExecutor(min(len(SOURCES), os.cpu_count() or 1)) as pool:
+            list(pool.map(lambda so: _run([hipcc()] + flags + ["-c", os.path.join(CSRC, so[0]), "-o", so[1]], verbose),
+                          zip(SOURCES, outs)))
+        _run([hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC"] + outs + ["-o", tmp], verbose)
     os.replace(tmp, LIB_PATH)
     return LIB_PATH
 

@@ -947,7 +947,7 @@ const char* muon_status_string(int status) {
   }
 }
 
-int muon_version(void) { return 300; }
+int muon_version(void) { return 400; }
 
 int muon_time_next_launch(void* start_event, void* stop_event) {
   pending_launch_events() = LaunchEvents{static_cast<hipEvent_t>(start_event), static_cast<hipEvent_t>(stop_event)};
