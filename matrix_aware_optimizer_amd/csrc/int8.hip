@@ -115,6 +115,8 @@ template <> struct Eight<float> {
   }
 };
 
+// Bound by memory: 4096 x 14336 bf16 34.6 us, 5.1 TB/s, a large copy's rate (read twice, with a
+// division for each entry, it was 111 us; read once, with the remainders for all, 43).
 // Rows of W waves, four waves to a workgroup, eight neighbouring columns per thread and chunk.
 // Up to 512 W CH columns a row is read once and stays in registers (CH chunks of a thread);
 // longer rows (CH = 0) are read twice, the second time from the caches.
