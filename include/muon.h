@@ -648,9 +648,9 @@ int ns_blocks_update(const muon_block_problem* probs, int nprobs, float a, float
  *                bytes (may be 0), 16-byte aligned; contents on entry do not
  *                matter.  Calls that share one must not overlap in time.
  * K = 0 gives zeros.  lda and ldb are multiples of 16 under 2^24.  m, n, rows and
- * cols are at most MUON_GLU_MAX_SIDE (MUON_EINVAL).  Pointers 16-byte aligned
- * (MUON_EALIGN); unknown dtypes give MUON_EDTYPE, unknown activations
- * MUON_EINVAL, a missing or short workspace MUON_EWORKSPACE.  A zero rows, cols,
+ * cols are at most MUON_GLU_MAX_SIDE, m n at most MUON_MAX_NUMEL (MUON_EINVAL).
+ * Pointers 16-byte aligned (MUON_EALIGN); unknown dtypes give MUON_EDTYPE,
+ * unknown activations MUON_EINVAL, a missing or short workspace MUON_EWORKSPACE.  A zero rows, cols,
  * m or n is MUON_OK and launches nothing.  Outputs may not overlap inputs.
  * ------------------------------------------------------------------------- */
 #define MUON_INT8_STEP 64
@@ -700,8 +700,9 @@ int int8_glu(const void* A, int64_t lda, const float* sa, const void* Bg, const 
  * A product without terms (in = 0, out = 0 or tokens = 0 on the summed side) gives
  * zeros, or beta M.  Rows that start at 16 bytes (pitches, and sides that a product
  * walks across, multiples of 8) take the fast path; others are right and slower.
- * Sides are at most MUON_GLU_MAX_SIDE, the pitches of x, Wg, Wu, dG and dU under
- * 2^23 entries (MUON_EINVAL).  Pointers 16-byte aligned (MUON_EALIGN); unknown
+ * Sides are at most MUON_GLU_MAX_SIDE, outputs MUON_MAX_NUMEL entries, the pitches
+ * of x, Wg, Wu, dG and dU under 2^23 entries; two outputs of one call at one
+ * address, and dX at an operand's, are refused (MUON_EINVAL).  Pointers 16-byte aligned (MUON_EALIGN); unknown
  * dtypes give MUON_EDTYPE, unknown activations MUON_EINVAL, a missing or short
  * workspace MUON_EWORKSPACE.  Where there is nothing to write the call is MUON_OK
  * and launches nothing.  Outputs may not overlap inputs but where said above.

@@ -112,13 +112,13 @@ int launch_tiled(const tile::Source& g, const Out& out, const tile::Plan& plan, 
   if ((AT ? g.m : g.K) < 8 || (BT ? g.n : g.K) < 8) return tile::launch_plain<DUAL ? 2 : 1>(g, out, sp.batch, AT, BT, st);
   if constexpr (!AT) {
     if (plan.kind == tile::kNarrow)
-      return whole ? tile::launch_sized<tile::Config<kBf16, 64, BT ? 128 : 64, 32, 64, 8, AT, BT, DUAL>, false>(g, out, sp, st)
+      return whole ? tile::launch_sized<tile::Config<kBf16, 64, BT ? 128 : 64, 32, 64, BT ? 8 : 9, AT, BT, DUAL>, false>(g, out, sp, st)
                    : tile::launch_sized<tile::Config<kBf16, 64, 128, 32, 64, 3, AT, BT, DUAL>, true>(g, out, sp, st);
   }
   // through registers, 256 x 256 tiles pay over 2048 and more values (14335 x 4095 weight gradients of
   // 4096 tokens 1319 us against 1501, of 300 tokens 71 against 45), and for one B only: two spill
   if (plan.kind == tile::kSmall || (!whole && (DUAL || g.K * g.segs < 2048)))
-    return whole ? tile::launch_sized<tile::Config<kBf16, 128, 128, 64, 64, 4, AT, BT, DUAL>, false>(g, out, sp, st)
+    return whole ? tile::launch_sized<tile::Config<kBf16, 128, 128, 64, 64, tile::ring_of(AT, BT), AT, BT, DUAL>, false>(g, out, sp, st)
                  : tile::launch_sized<tile::Config<kBf16, 128, 128, 64, 64, 3, AT, BT, DUAL>, true>(g, out, sp, st);
   if constexpr (!DUAL)
     if (!whole) return tile::launch_tiles<tile::Config<kBf16, 256, 256, 128, 128, 3, AT, BT, DUAL>, true, false>(g, out, sp, st);
@@ -128,6 +128,8 @@ int launch_tiled(const tile::Source& g, const Out& out, const tile::Plan& plan, 
 bool sides_ok(int64_t tokens, int64_t out, int64_t in) {
   return tokens >= 0 && out >= 0 && in >= 0 && tokens <= MUON_GLU_MAX_SIDE && out <= MUON_GLU_MAX_SIDE && in <= MUON_GLU_MAX_SIDE;
 }
+// outputs that would be written over each other
+bool same(const void* a, const void* b) { return a != nullptr && a == b; }
 bool pitch_ok(int64_t ld, int64_t cols) { return ld >= cols && ld * 2 <= tile::kMaxPitch; }
 bool run8(int64_t v) { return v % 8 == 0; }
 
@@ -166,6 +168,7 @@ int glu_forward(const void* X, int64_t ldx, const void* Wg, const void* Wu, int6
                 void* U, int64_t ldg, int64_t tokens, int64_t out, int64_t in, void* workspace, size_t ws_bytes, void* stream) {
   if (!sides_ok(tokens, out, in) || !valid_act(act)) return MUON_EINVAL;
   if (tokens == 0 || out == 0) return MUON_OK;
+  if (!numel_ok(tokens * out) || same(H, G) || same(H, U) || same(G, U)) return MUON_EINVAL;
   if (H == nullptr || ldh < out || (in > 0 && (X == nullptr || Wg == nullptr || Wu == nullptr))) return MUON_EINVAL;
   if (!pitch_ok(ldx, in) || !pitch_ok(ldw, in) || (G == nullptr) != (U == nullptr) || (G != nullptr && ldg < out)) return MUON_EINVAL;
   if (!aligned16(X) || !aligned16(Wg) || !aligned16(Wu) || !aligned16(H) || !aligned16(G) || !aligned16(U)) return MUON_EALIGN;
@@ -196,6 +199,8 @@ int glu_backward(const void* dH, int64_t lddh, const void* G, const void* U, int
   const bool input = dX != nullptr && in > 0;
   if (tokens == 0) return MUON_OK;
   if (out > 0 && (dH == nullptr || G == nullptr || U == nullptr || dG == nullptr || dU == nullptr)) return MUON_EINVAL;
+  if (!numel_ok(tokens * out) || !numel_ok(tokens * in) || (out > 0 && (same(dG, dU) || same(H, dG) || same(H, dU)))) return MUON_EINVAL;
+  if (input && (same(dX, dG) || same(dX, dU) || same(dX, H) || same(dX, Wg) || same(dX, Wu))) return MUON_EINVAL;
   if (lddh < out || ldg < out || !pitch_ok(ldd, out) || (H != nullptr && ldh < out)) return MUON_EINVAL;
   if (input && (lddx < in || !pitch_ok(ldw, in) || (out > 0 && (Wg == nullptr || Wu == nullptr)))) return MUON_EINVAL;
   if (!aligned16(dH) || !aligned16(G) || !aligned16(U) || !aligned16(dG) || !aligned16(dU) || !aligned16(H)) return MUON_EALIGN;
@@ -239,6 +244,7 @@ int glu_weight_grad(const void* dG, const void* dU, int64_t ldd, const void* X, 
   if (!sides_ok(tokens, out, in)) return MUON_EINVAL;
   if (!valid_dtype(m_dtype)) return MUON_EDTYPE;
   if (out == 0 || in == 0) return MUON_OK;
+  if (!numel_ok(out * in) || same(Mg, Mu)) return MUON_EINVAL;
   if (Mg == nullptr || Mu == nullptr || ldm < in || (tokens > 0 && (dG == nullptr || dU == nullptr || X == nullptr))) return MUON_EINVAL;
   if (!pitch_ok(ldd, out) || !pitch_ok(ldx, in)) return MUON_EINVAL;
   if (!aligned16(dG) || !aligned16(dU) || !aligned16(X) || !aligned16(Mg) || !aligned16(Mu)) return MUON_EALIGN;

@@ -229,9 +229,9 @@ int launch_product(const tile::Source& g, const Out& out, const tile::Plan& plan
     case tile::kDirect:
       return tile::launch_direct<kI8, NB>(g, out, st);
     case tile::kNarrow:
-      return tile::launch_sized<tile::Config<kI8, 64, 64, 32, 64, 8, false, false, DUAL>, false>(g, out, sp, st);
+      return tile::launch_sized<tile::Config<kI8, 64, 64, 32, 64, 9, false, false, DUAL>, false>(g, out, sp, st);
     case tile::kSmall:
-      return tile::launch_sized<tile::Config<kI8, 128, 128, 64, 64, 4, false, false, DUAL>, false>(g, out, sp, st);
+      return tile::launch_sized<tile::Config<kI8, 128, 128, 64, 64, 5, false, false, DUAL>, false>(g, out, sp, st);
     default:
       return tile::launch_large<kI8, false, false, DUAL>(g, out, sp, st);
   }
@@ -272,6 +272,7 @@ int int8_gemm(const void* A, int64_t lda, const float* sa, const void* B, int64_
   if (!side_ok(m) || !side_ok(n) || K < 0 || K > MUON_INT8_MAX_K || K % kStep != 0) return MUON_EINVAL;
   if (!valid_dtype(c_dtype)) return MUON_EDTYPE;
   if (m == 0 || n == 0) return MUON_OK;
+  if (!numel_ok(m * n)) return MUON_EINVAL;
   if (sa == nullptr || sb == nullptr || C == nullptr || ldc < n || (K > 0 && (A == nullptr || B == nullptr))) return MUON_EINVAL;
   if (lda < K || ldb < K || lda % 16 != 0 || ldb % 16 != 0 || lda > tile::kMaxPitch || ldb > tile::kMaxPitch) return MUON_EINVAL;
   if (!aligned16(A) || !aligned16(sa) || !aligned16(B) || !aligned16(sb) || !aligned16(C)) return MUON_EALIGN;
@@ -292,6 +293,7 @@ int int8_glu(const void* A, int64_t lda, const float* sa, const void* Bg, const 
   if (!side_ok(m) || !side_ok(n) || K < 0 || K > MUON_INT8_MAX_K || K % kStep != 0 || !valid_act(act)) return MUON_EINVAL;
   if (!valid_dtype(h_dtype)) return MUON_EDTYPE;
   if (m == 0 || n == 0) return MUON_OK;
+  if (!numel_ok(m * n)) return MUON_EINVAL;
   if (sa == nullptr || sg == nullptr || su == nullptr || H == nullptr || ldh < n) return MUON_EINVAL;
   if (K > 0 && (A == nullptr || Bg == nullptr || Bu == nullptr)) return MUON_EINVAL;
   if (lda < K || ldb < K || lda % 16 != 0 || ldb % 16 != 0 || lda > tile::kMaxPitch || ldb > tile::kMaxPitch) return MUON_EINVAL;

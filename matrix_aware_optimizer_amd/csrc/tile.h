@@ -74,6 +74,9 @@ struct Source {
   int segs;           // segments of the contraction (1 or 2)
 };
 
+// stages of tiles of 128 rows and more (Config::PAIRS)
+constexpr int ring_of(bool a_kmajor, bool b_kmajor) { return a_kmajor || b_kmajor ? 4 : 5; }
+
 template <int KIND_, int BM_, int BN_, int WM_, int WN_, int S_, bool AT_, bool BT_, bool DUAL_>
 struct Config {
   static constexpr int KIND = KIND_, BM = BM_, BN = BN_, WM = WM_, WN = WN_, S = S_;
@@ -85,6 +88,12 @@ struct Config {
   static constexpr int LDW = WN + 4;                        // row pitch of the epilogue's slab, in floats
   static constexpr int LDS_BYTES = S * STAGE > W * 32 * LDW * 4 ? S * STAGE : W * 32 * LDW * 4;
   static constexpr int A_DMA = A_BYTES / 1024 / W, B_DMA = B_BYTES / 1024 / W, D = A_DMA + B_DMA;
+  // Operands in rows have 64 of a cache line's 128 bytes in a stage.  With an odd number of stages
+  // the two stages of a line are copied one right after the other, and the second half comes from
+  // the CU's own cache: forward of 4096 x 14336 x 4096 816 -> 780 us, int8 gated 2048 x 14336 x 4096
+  // 236 -> 223.  K-major rows are whole lines, and gathering two stages' copies in every other step
+  // costs them 5%.
+  static constexpr bool PAIRS = !AT && !BT && S % 2 == 1;
   // Tiles of few rows are bound by reading B, and all start at once: each begins at another step
   // of the contraction, or the same offsets of many rows (one memory channel, at pitches of 8 KB
   // and more) are wanted together.  33 x 14336 x 8192 bf16, both weights from memory: 125 -> 108 us.
@@ -260,7 +269,7 @@ __device__ __forceinline__ void unit(const Source& g, int64_t m0, int64_t n0, in
     const uint32_t lds_base =
         static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char*)lds));
     const int nk = s1 - s0;
-    const int turn = C_::TURNED && per > 0 ? int(n0 / C_::COLS * 5 % per) : 0;
+    const int turn = C_::TURNED && per > 0 ? int(n0 / C_::COLS * 6 % per) & ~1 : 0;   // even: pairs stay pairs
     auto issue_one = [&](int q, int kt, uint32_t off) __attribute__((always_inline)) {
       const int seg = kt >= per ? 1 : 0;
       int k = kt - seg * per;
@@ -282,26 +291,62 @@ __device__ __forceinline__ void unit(const Source& g, int64_t m0, int64_t n0, in
       return o == uint32_t(S * C_::STAGE) ? 0u : o;
     };
     if (nk > 0) {
-#pragma unroll
-      for (int s = 0; s < S - 1; ++s)
-        if (s < nk)
-#pragma unroll
-          for (int q = 0; q < C_::D; ++q) issue_one(q, s0 + s, uint32_t(s) * C_::STAGE);
-      if (nk >= S - 1) ring_barrier<C_::D * (S - 2)>();
-      else ring_barrier<0>();
       Frags f0, f1;
-#pragma unroll
-      for (int q = 0; q < READS; ++q) read_one(q, lds, f0);
-      uint32_t o_cur = 0, o_iss = uint32_t(S - 1) * C_::STAGE;
+      uint32_t o_cur = 0;
       int it = 0;
       constexpr int RPM = (READS + N * 3 / 4 - 1) / (N * 3 / 4);   // reads per MFMA, done after three quarters of them
+      // copies of stages kt and kt + 1: those of the same rows one after the other, so that the
+      // second finds the cache lines that the first has fetched
+      auto issue_two = [&](int q, int kt, uint32_t o0, uint32_t o1) __attribute__((always_inline)) {
+        issue_one(q >> 1, kt + (q & 1), q & 1 ? o1 : o0);
+      };
+      constexpr bool PAIRS = C_::PAIRS;
+      if (PAIRS && nk >= S - 1) {
+#pragma unroll
+        for (int s = 0; s < S - 1; s += 2)
+#pragma unroll
+          for (int q = 0; q < 2 * C_::D; ++q) issue_two(q, s0 + s, uint32_t(s) * C_::STAGE, uint32_t(s + 1) * C_::STAGE);
+        ring_barrier<C_::D * (S - 3)>();
+      } else {
+#pragma unroll
+        for (int s = 0; s < S - 1; ++s)
+          if (s < nk)
+#pragma unroll
+            for (int q = 0; q < C_::D; ++q) issue_one(q, s0 + s, uint32_t(s) * C_::STAGE);
+        if (!PAIRS && nk >= S - 1) ring_barrier<C_::D * (S - 2)>();
+        else ring_barrier<0>();
+      }
+#pragma unroll
+      for (int q = 0; q < READS; ++q) read_one(q, lds, f0);
+      auto reads_under = [&](int n, const char* st, Frags& nxt) __attribute__((always_inline)) {
+#pragma unroll
+        for (int r = 0; r < RPM; ++r)
+          if (RPM * n + r < READS) read_one(RPM * n + r, st, nxt);
+      };
+      auto ring_before = [](uint32_t o) { return o == 0 ? uint32_t((S - 1) * C_::STAGE) : o - C_::STAGE; };
+      // PAIRS: two steps, of which the first copies the stages S - 1 and S steps ahead (to where the
+      // step before and this one were read from); each finds all but the last S - 3 stages landed
+      auto two_steps = [&]() __attribute__((always_inline)) {
+        const uint32_t o1 = ring_next(o_cur), o2 = ring_next(o1), before = ring_before(o_cur);
+        ring_barrier<C_::D * (S - 3)>();
+        mma(f0, [&](int n) __attribute__((always_inline)) {
+          reads_under(n, lds + o1, f1);
+#pragma unroll
+          for (int q = 0; q < 2 * C_::D; ++q)
+            if (q * N / (2 * C_::D) == n) issue_two(q, s0 + it + S - 1, before, o_cur);
+        });
+        ring_barrier<C_::D * (S - 3)>();
+        mma(f1, [&](int n) __attribute__((always_inline)) { reads_under(n, lds + o2, f0); });
+        o_cur = o2;
+        it += 2;
+      };
+      // other rings: one step, which copies the stage S - 1 steps ahead
+      uint32_t o_iss = uint32_t(S - 1) * C_::STAGE;
       auto steady = [&](Frags& cur, Frags& nxt) __attribute__((always_inline)) {
         const char* st = lds + ring_next(o_cur);
         ring_barrier<C_::D * (S - 3)>();
         mma(cur, [&](int n) __attribute__((always_inline)) {
-#pragma unroll
-          for (int r = 0; r < RPM; ++r)
-            if (RPM * n + r < READS) read_one(RPM * n + r, st, nxt);
+          reads_under(n, st, nxt);
 #pragma unroll
           for (int q = 0; q < C_::D; ++q)
             if (q * N / C_::D == n) issue_one(q, s0 + it + S - 1, o_iss);
@@ -321,13 +366,22 @@ __device__ __forceinline__ void unit(const Source& g, int64_t m0, int64_t n0, in
         o_cur = ring_next(o_cur);
         ++it;
       };
-      while (it + S < nk) {   // two steps that both still copy a stage
-        steady(f0, f1);
-        steady(f1, f0);
-      }
-      if (it + S - 1 < nk) {   // one more copy is due
-        steady(f0, f1);
-        f0 = f1;
+      if constexpr (PAIRS) {
+        while (it + S < nk) two_steps();
+        if (it + S - 1 < nk) {   // one more copy is due
+          ring_barrier<0>();
+#pragma unroll
+          for (int q = 0; q < C_::D; ++q) issue_one(q, s0 + it + S - 1, ring_before(o_cur));
+        }
+      } else {
+        while (it + S < nk) {   // two steps that both still copy a stage
+          steady(f0, f1);
+          steady(f1, f0);
+        }
+        if (it + S - 1 < nk) {   // one more copy is due
+          steady(f0, f1);
+          f0 = f1;
+        }
       }
       while (it < nk) {
         drain(f0, f1);
@@ -632,8 +686,9 @@ __global__ __launch_bounds__(C_::NT) void tile_kernel(Source g, Out out, Split s
   if constexpr (SPLIT) {
     // a part's tiles are neighbours
     const int64_t part = u / (tiles * sp.batch);
-    const int s0 = __builtin_amdgcn_readfirstlane(int(part * steps / sp.parts));
-    const int s1 = __builtin_amdgcn_readfirstlane(int((part + 1) * steps / sp.parts));
+    // (even first steps: two steps share a cache line)
+    const int s0 = __builtin_amdgcn_readfirstlane(int(part * steps / sp.parts) & ~1);
+    const int s1 = part == sp.parts - 1 ? steps : __builtin_amdgcn_readfirstlane(int((part + 1) * steps / sp.parts) & ~1);
     using P = Partial<C_::KIND, C_::NB>;
     const P po{static_cast<typename P::sum_t*>(sp.sums) + (part * sp.batch + z) * g.m * C_::NB * sp.ldp, sp.ldp, sp.ldp};
     unit<C_, MASKED>(s, tm * C_::BM, tn * C_::COLS, s0, s1, part == sp.parts - 1, po, lds);
@@ -651,9 +706,9 @@ __global__ __launch_bounds__(C_::NT) void tile_kernel(Source g, Out out, Split s
 // 14336 x 4096 239 us (2.01 POP/s), 1999 x 4096 x 14336 127 (1.85).
 template <int KIND, bool AT, bool BT, bool DUAL, class Out>
 __global__ __launch_bounds__(256) void mixed_kernel(Source g, Out out, int batch, int64_t whole, int parts) {
-  using L = Config<KIND, 256, 256, 128, 128, 4, AT, BT, DUAL>;
-  using H = Config<KIND, 128, 256, 64, 128, 4, AT, BT, DUAL>;
-  using Q = Config<KIND, 128, 128, 64, 64, 4, AT, BT, DUAL>;
+  using L = Config<KIND, 256, 256, 128, 128, ring_of(AT, BT), AT, BT, DUAL>;
+  using H = Config<KIND, 128, 256, 64, 128, ring_of(AT, BT), AT, BT, DUAL>;
+  using Q = Config<KIND, 128, 128, 64, 64, ring_of(AT, BT), AT, BT, DUAL>;
   extern __shared__ __attribute__((aligned(1024))) char lds[];
   const int64_t TM = (g.m + 255) / 256, TN = (g.n + L::COLS - 1) / L::COLS, tiles = TM * TN;
   const int steps = __builtin_amdgcn_readfirstlane(int(g.K / (64 / Math<KIND>::kBytes) * g.segs));
@@ -889,7 +944,7 @@ int launch_tiles(const Source& g, const Out& out, const Split& sp, hipStream_t s
 }
 template <int KIND, bool AT, bool BT, bool DUAL, class Out>
 int launch_mixed(const Source& g, const Out& out, int batch, hipStream_t st) {
-  using L = Config<KIND, 256, 256, 128, 128, 4, AT, BT, DUAL>;
+  using L = Config<KIND, 256, 256, 128, 128, ring_of(AT, BT), AT, BT, DUAL>;
   auto kern = mixed_kernel<KIND, AT, BT, DUAL, Out>;
   static std::atomic<uint64_t> configured{0};
   if (gemm::set_lds_limit(kern, L::LDS_BYTES, configured) != MUON_OK) return MUON_ELAUNCH;
@@ -911,7 +966,7 @@ int launch_large(const Source& g, const Out& out, const Split& sp, hipStream_t s
   using Passing = decltype(out.passing());
   if constexpr (std::is_same_v<Passing, Out>) return launch_mixed<KIND, AT, BT, DUAL>(g, out, sp.batch, st);
   if (out.lines()) return launch_mixed<KIND, AT, BT, DUAL>(g, out.passing(), sp.batch, st);
-  return launch_tiles<Config<KIND, 256, 256, 128, 128, 4, AT, BT, DUAL>, false, false>(g, out, sp, st);
+  return launch_tiles<Config<KIND, 256, 256, 128, 128, ring_of(AT, BT), AT, BT, DUAL>, false, false>(g, out, sp, st);
 }
 template <int NB, class Out>
 int launch_plain(const Source& g, const Out& out, int batch, bool a_kmajor, bool b_kmajor, hipStream_t st) {

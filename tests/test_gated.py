@@ -66,6 +66,22 @@ def test_other_refusals():
     assert backward_call(H=BAD) == EALIGN and backward_call(dX=BAD) == EALIGN
 
 
+@pytest.mark.parametrize("call,pairs", [
+    (forward_call, ["H G", "H U", "G U"]), (weight_call, ["Mg Mu"]),
+    (backward_call, ["dG dU", "H dG", "H dU", "dX dG", "dX dU", "dX H", "dX Wg", "dX Wu"])])
+def test_outputs_over_each_other_are_refused(call, pairs):
+    for pair in pairs:
+        a, b = pair.split()
+        assert call(**{a: P[9], b: P[9]}) == EINVAL
+
+
+def test_more_entries_than_any_memory_are_refused():
+    side = mao.MUON_GLU_MAX_SIDE
+    assert forward_call(t=side, f=side, ldh=side, ldg=side) == EINVAL
+    assert backward_call(t=side, d=side, ldw=side, lddx=side) == EINVAL
+    assert weight_call(f=side, d=side, ldd=side, ldx=side, ldm=side) == EINVAL
+
+
 def test_workspace_refusals():
     L = mao.lib()
     asked = {}
