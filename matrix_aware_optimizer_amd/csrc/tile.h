@@ -75,7 +75,7 @@ struct Source {
 };
 
 // stages of tiles of 128 rows and more (Config::PAIRS)
-constexpr int ring_of(bool a_kmajor, bool b_kmajor) { return a_kmajor || b_kmajor ? 4 : 5; }
+constexpr int ring_of(bool a_kmajor) { return a_kmajor ? 4 : 5; }
 
 template <int KIND_, int BM_, int BN_, int WM_, int WN_, int S_, bool AT_, bool BT_, bool DUAL_>
 struct Config {
@@ -91,9 +91,9 @@ struct Config {
   // Operands in rows have 64 of a cache line's 128 bytes in a stage.  With an odd number of stages
   // the two stages of a line are copied one right after the other, and the second half comes from
   // the CU's own cache: forward of 4096 x 14336 x 4096 816 -> 780 us, int8 gated 2048 x 14336 x 4096
-  // 236 -> 223.  K-major rows are whole lines, and gathering two stages' copies in every other step
-  // costs them 5%.
-  static constexpr bool PAIRS = !AT && !BT && S % 2 == 1;
+  // 236 -> 223, 33 rows of it 32.2 -> 26.5, dx of 4096 x 14336 x 4096 (A only) 765 -> 750.  K-major rows
+  // are whole lines; gathering two stages' copies of them in every other step costs 5%.
+  static constexpr bool PAIRS = !AT && S % 2 == 1;
   // Tiles of few rows are bound by reading B, and all start at once: each begins at another step
   // of the contraction, or the same offsets of many rows (one memory channel, at pitches of 8 KB
   // and more) are wanted together.  33 x 14336 x 8192 bf16, both weights from memory: 125 -> 108 us.
@@ -295,17 +295,24 @@ __device__ __forceinline__ void unit(const Source& g, int64_t m0, int64_t n0, in
       uint32_t o_cur = 0;
       int it = 0;
       constexpr int RPM = (READS + N * 3 / 4 - 1) / (N * 3 / 4);   // reads per MFMA, done after three quarters of them
-      // copies of stages kt and kt + 1: those of the same rows one after the other, so that the
-      // second finds the cache lines that the first has fetched
-      auto issue_two = [&](int q, int kt, uint32_t o0, uint32_t o1) __attribute__((always_inline)) {
-        issue_one(q >> 1, kt + (q & 1), q & 1 ? o1 : o0);
+      // The copies of stages kt and kt + 1 in two steps.  The first takes those of row operands for
+      // both, the same rows one after the other, so that the second finds the cache lines that the
+      // first has fetched, and a k-major B's for kt; the second step takes a k-major B's for kt + 1.
+      constexpr int IN_FIRST = 2 * C_::A_DMA + (C_::BT ? 1 : 2) * C_::B_DMA, IN_SECOND = C_::BT ? C_::B_DMA : 0;
+      auto issue_first = [&](int q, int kt, uint32_t o0, uint32_t o1) __attribute__((always_inline)) {
+        if (C_::BT && q >= 2 * C_::A_DMA) issue_one(q - C_::A_DMA, kt, o0);
+        else issue_one(q >> 1, kt + (q & 1), q & 1 ? o1 : o0);
       };
+      auto issue_second = [&](int q, int kt, uint32_t o1) __attribute__((always_inline)) { issue_one(C_::A_DMA + q, kt + 1, o1); };
       constexpr bool PAIRS = C_::PAIRS;
       if (PAIRS && nk >= S - 1) {
 #pragma unroll
-        for (int s = 0; s < S - 1; s += 2)
+        for (int s = 0; s < S - 1; s += 2) {
 #pragma unroll
-          for (int q = 0; q < 2 * C_::D; ++q) issue_two(q, s0 + s, uint32_t(s) * C_::STAGE, uint32_t(s + 1) * C_::STAGE);
+          for (int q = 0; q < IN_FIRST; ++q) issue_first(q, s0 + s, uint32_t(s) * C_::STAGE, uint32_t(s + 1) * C_::STAGE);
+#pragma unroll
+          for (int q = 0; q < IN_SECOND; ++q) issue_second(q, s0 + s, uint32_t(s + 1) * C_::STAGE);
+        }
         ring_barrier<C_::D * (S - 3)>();
       } else {
 #pragma unroll
@@ -324,19 +331,24 @@ __device__ __forceinline__ void unit(const Source& g, int64_t m0, int64_t n0, in
           if (RPM * n + r < READS) read_one(RPM * n + r, st, nxt);
       };
       auto ring_before = [](uint32_t o) { return o == 0 ? uint32_t((S - 1) * C_::STAGE) : o - C_::STAGE; };
-      // PAIRS: two steps, of which the first copies the stages S - 1 and S steps ahead (to where the
-      // step before and this one were read from); each finds all but the last S - 3 stages landed
+      // PAIRS: two steps, which copy the stages S - 1 and S steps ahead (to where the step before and
+      // this one were read from); each finds all but the last S - 3 stages' copies landed
       auto two_steps = [&]() __attribute__((always_inline)) {
         const uint32_t o1 = ring_next(o_cur), o2 = ring_next(o1), before = ring_before(o_cur);
         ring_barrier<C_::D * (S - 3)>();
         mma(f0, [&](int n) __attribute__((always_inline)) {
           reads_under(n, lds + o1, f1);
 #pragma unroll
-          for (int q = 0; q < 2 * C_::D; ++q)
-            if (q * N / (2 * C_::D) == n) issue_two(q, s0 + it + S - 1, before, o_cur);
+          for (int q = 0; q < IN_FIRST; ++q)
+            if (q * N / IN_FIRST == n) issue_first(q, s0 + it + S - 1, before, o_cur);
         });
         ring_barrier<C_::D * (S - 3)>();
-        mma(f1, [&](int n) __attribute__((always_inline)) { reads_under(n, lds + o2, f0); });
+        mma(f1, [&](int n) __attribute__((always_inline)) {
+          reads_under(n, lds + o2, f0);
+#pragma unroll
+          for (int q = 0; q < IN_SECOND; ++q)
+            if (q * N / C_::B_DMA == n) issue_second(q, s0 + it + S - 1, o_cur);
+        });
         o_cur = o2;
         it += 2;
       };
@@ -706,9 +718,9 @@ __global__ __launch_bounds__(C_::NT) void tile_kernel(Source g, Out out, Split s
 // 14336 x 4096 239 us (2.01 POP/s), 1999 x 4096 x 14336 127 (1.85).
 template <int KIND, bool AT, bool BT, bool DUAL, class Out>
 __global__ __launch_bounds__(256) void mixed_kernel(Source g, Out out, int batch, int64_t whole, int parts) {
-  using L = Config<KIND, 256, 256, 128, 128, ring_of(AT, BT), AT, BT, DUAL>;
-  using H = Config<KIND, 128, 256, 64, 128, ring_of(AT, BT), AT, BT, DUAL>;
-  using Q = Config<KIND, 128, 128, 64, 64, ring_of(AT, BT), AT, BT, DUAL>;
+  using L = Config<KIND, 256, 256, 128, 128, ring_of(AT), AT, BT, DUAL>;
+  using H = Config<KIND, 128, 256, 64, 128, ring_of(AT), AT, BT, DUAL>;
+  using Q = Config<KIND, 128, 128, 64, 64, ring_of(AT), AT, BT, DUAL>;
   extern __shared__ __attribute__((aligned(1024))) char lds[];
   const int64_t TM = (g.m + 255) / 256, TN = (g.n + L::COLS - 1) / L::COLS, tiles = TM * TN;
   const int steps = __builtin_amdgcn_readfirstlane(int(g.K / (64 / Math<KIND>::kBytes) * g.segs));
@@ -944,7 +956,7 @@ int launch_tiles(const Source& g, const Out& out, const Split& sp, hipStream_t s
 }
 template <int KIND, bool AT, bool BT, bool DUAL, class Out>
 int launch_mixed(const Source& g, const Out& out, int batch, hipStream_t st) {
-  using L = Config<KIND, 256, 256, 128, 128, ring_of(AT, BT), AT, BT, DUAL>;
+  using L = Config<KIND, 256, 256, 128, 128, ring_of(AT), AT, BT, DUAL>;
   auto kern = mixed_kernel<KIND, AT, BT, DUAL, Out>;
   static std::atomic<uint64_t> configured{0};
   if (gemm::set_lds_limit(kern, L::LDS_BYTES, configured) != MUON_OK) return MUON_ELAUNCH;
@@ -966,7 +978,7 @@ int launch_large(const Source& g, const Out& out, const Split& sp, hipStream_t s
   using Passing = decltype(out.passing());
   if constexpr (std::is_same_v<Passing, Out>) return launch_mixed<KIND, AT, BT, DUAL>(g, out, sp.batch, st);
   if (out.lines()) return launch_mixed<KIND, AT, BT, DUAL>(g, out.passing(), sp.batch, st);
-  return launch_tiles<Config<KIND, 256, 256, 128, 128, ring_of(AT, BT), AT, BT, DUAL>, false, false>(g, out, sp, st);
+  return launch_tiles<Config<KIND, 256, 256, 128, 128, ring_of(AT), AT, BT, DUAL>, false, false>(g, out, sp, st);
 }
 template <int NB, class Out>
 int launch_plain(const Source& g, const Out& out, int batch, bool a_kmajor, bool b_kmajor, hipStream_t st) {
