@@ -182,7 +182,6 @@ int glu_forward(const void* X, int64_t ldx, const void* Wg, const void* Wu, int6
                                 nullptr, nullptr, nullptr};
   const tile::Split sp{plan.parts, 1, workspace, ceil_div(out, 4) * 4};
   hipStream_t hs = static_cast<hipStream_t>(stream);
-  if (plan.kind == tile::kDirect) return tile::launch_direct<kBf16, 2>(g, o, hs);
   return launch_tiled<false, false, true>(g, o, plan, sp, whole, hs);
 }
 

@@ -222,12 +222,11 @@ struct ScaleOut {
 
 template <bool DUAL, class Out>
 int launch_product(const tile::Source& g, const Out& out, const tile::Plan& plan, void* workspace, hipStream_t st) {
-  constexpr int NB = DUAL ? 2 : 1;
   using tile::kI8;
   const tile::Split sp{plan.parts, 1, workspace, ceil_div(g.n, 4) * 4};
+  if constexpr (!DUAL)
+    if (plan.kind == tile::kDirect) return tile::launch_direct(g, out, st);
   switch (plan.kind) {
-    case tile::kDirect:
-      return tile::launch_direct<kI8, NB>(g, out, st);
     case tile::kNarrow:
       return tile::launch_sized<tile::Config<kI8, 64, 64, 32, 64, 9, false, false, DUAL>, false>(g, out, sp, st);
     case tile::kSmall:

@@ -133,22 +133,6 @@ __device__ __forceinline__ void ring_barrier() {
 // all LDS accesses of the wave are done, then all waves meet; loads to registers stay under way
 __device__ __forceinline__ void ring_barrier_lds() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
-// 16 bytes of bf16 values at p, of which `left` lie inside the matrix: zeros past them
-__device__ __forceinline__ u32x4_t masked16(const bf16_t* p, int64_t left) {
-  u32x4_t r = {0, 0, 0, 0};
-  if (left >= 8) {
-    const uint4 v = load16(p);
-    r = u32x4_t{v.x, v.y, v.z, v.w};
-  } else if (left > 0) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t lo = 2 * j < left ? p[2 * j] : 0u, hi = 2 * j + 1 < left ? p[2 * j + 1] : 0u;
-      r[j] = lo | (hi << 16);
-    }
-  }
-  return r;
-}
-
 // One tile at rows m0 and columns n0 over steps [s0, s1) of the contraction's whole steps (MASKED:
 // through registers); `tail`: then the last, partial step of every segment.
 template <class C_, bool MASKED, class Out>
@@ -807,45 +791,36 @@ __global__ __launch_bounds__(256) void plain_kernel(Source g, Out out, int batch
 // ---------------------------------------------------------------------------
 // Few rows
 // ---------------------------------------------------------------------------
-// Up to 16 rows, bound by reading B: 1 x 4096 x 14336 int8 12.7 us (4.6 TB/s), 1 x 14336 x 4096
-// bf16, both weights, 48.9 us (4.8 TB/s).  Straight from memory: no tile is staged, each wave reads 16 rows of every B
-// and the rows of A, 128 bytes of each at a time, and multiplies them on 16 x 16 blocks.  The
-// waves of a workgroup take the 128-byte groups of the contraction in turn; their sums meet in
-// LDS and are added in the order of the waves.  B is the first operand: a lane holds four
-// consecutive columns of one row of C.
-template <int KIND, int NB, class Out>
+// Few rows (16 at most) of int8 against one B, bound by reading B: 1 x 4096 x 14336 12.7 us (4.6 TB/s).
+// Straight from memory: no tile is staged, each wave reads 16 rows of B and the rows of A, 128
+// bytes of each at a time, and multiplies them on 16 x 16 blocks.  The waves of a workgroup take
+// the 128-byte groups of the contraction in turn; their sums meet in LDS.  B is the first operand:
+// a lane holds four consecutive columns of one row of C.
+template <class Out>
 __global__ __launch_bounds__(512) void direct_kernel(Source g, Out out) {
-  using M_ = Math<KIND>;
-  using sum_t = typename M_::sum_t;
-  extern __shared__ __attribute__((aligned(16))) char lds[];
-  sum_t* red = reinterpret_cast<sum_t*>(lds);   // [waves][NB * 4][64]
+  using M_ = Math<kI8>;
+  __shared__ int red[8 * 4 * 64];   // [waves][4][64]
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
   const int r = lane & 15, kq = lane >> 4;
   const int64_t n0 = int64_t(blockIdx.x) * 16;
   // 16 bytes at 16 kq and at 64 + 16 kq of the group: the same k-values for both operands
-  const char *pb[NB], *pa = g.A[0] + min(int64_t(r), g.m - 1) * g.lda + 16 * kq;
-#pragma unroll
-  for (int b = 0; b < NB; ++b) pb[b] = g.B[b] + min(n0 + r, g.n - 1) * g.ldb + 16 * kq;
-  typename M_::acc4_t acc[NB];
-#pragma unroll
-  for (int b = 0; b < NB; ++b) acc[b] = typename M_::acc4_t{0, 0, 0, 0};
-  const int64_t bytes = g.K * M_::kBytes, groups = bytes / 128;
-  auto load = [](const char* p) __attribute__((always_inline)) {
-    const uint4 v = load16(reinterpret_cast<const bf16_t*>(p));
-    return u32x4_t{v.x, v.y, v.z, v.w};
-  };
+  const char* pa = g.A[0] + min(int64_t(r), g.m - 1) * g.lda + 16 * kq;
+  const char* pb = g.B[0] + min(n0 + r, g.n - 1) * g.ldb + 16 * kq;
+  M_::acc4_t acc = {0, 0, 0, 0};
+  const int64_t groups = g.K / 128;
+  auto load = [](const char* p) __attribute__((always_inline)) { return *reinterpret_cast<const u32x4_t*>(p); };
   constexpr int U = 4;   // groups whose loads are in flight together
+  // each workgroup begins at another group, as TURNED tiles do
   const int64_t turn = groups > 0 ? int64_t(blockIdx.x) * 5 % groups : 0;
   for (int64_t kb0 = wave; kb0 < groups; kb0 += U * waves) {
-    u32x4_t fb[U][NB][2], fa[U][2];
+    u32x4_t fb[U][2], fa[U][2];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       int64_t at = min(kb0 + u * waves, groups - 1) + turn;   // past the end: read again, not used
       at = (at >= groups ? at - groups : at) * 128;
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-#pragma unroll
-        for (int b = 0; b < NB; ++b) fb[u][b][c] = load(pb[b] + at + 64 * c);
+        fb[u][c] = load(pb + at + 64 * c);
         fa[u][c] = load(pa + at + 64 * c);
       }
     }
@@ -854,36 +829,23 @@ __global__ __launch_bounds__(512) void direct_kernel(Source g, Out out) {
     for (int u = 0; u < U; ++u) {
       if (kb0 + u * waves >= groups) break;
 #pragma unroll
-      for (int c = 0; c < 2; ++c)
-#pragma unroll
-        for (int b = 0; b < NB; ++b) acc[b] = M_::mma16(fb[u][b][c], fa[u][c], acc[b]);
+      for (int c = 0; c < 2; ++c) acc = M_::mma16(fb[u][c], fa[u][c], acc);
     }
   }
-  if (wave == waves - 1 && bytes % 128 != 0) {   // the last, partial group
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const int64_t at = groups * 128 + 64 * c, left = (bytes - at - 16 * kq) / 2;
-      const u32x4_t fa = masked16(reinterpret_cast<const bf16_t*>(pa + at), left);
-#pragma unroll
-      for (int b = 0; b < NB; ++b) acc[b] = M_::mma16(masked16(reinterpret_cast<const bf16_t*>(pb[b] + at), left), fa, acc[b]);
-    }
-  }
+  if (wave == waves - 1 && g.K % 128 != 0)   // half a group is left (K is a multiple of 64)
+    acc = M_::mma16(load(pb + groups * 128), load(pa + groups * 128), acc);
   if (waves > 1) {
 #pragma unroll
-    for (int b = 0; b < NB; ++b)
-#pragma unroll
-      for (int v = 0; v < 4; ++v) red[((wave * NB + b) * 4 + v) * 64 + lane] = acc[b][v];
+    for (int v = 0; v < 4; ++v) red[(wave * 4 + v) * 64 + lane] = acc[v];
     __syncthreads();
     if (wave > 0) return;
   }
-  sum_t o[NB][4];
+  int o[1][4];
 #pragma unroll
-  for (int b = 0; b < NB; ++b)
-#pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      o[b][v] = acc[b][v];
-      for (int w = 1; w < waves; ++w) o[b][v] += red[((w * NB + b) * 4 + v) * 64 + lane];
-    }
+  for (int v = 0; v < 4; ++v) {
+    o[0][v] = acc[v];
+    for (int w = 1; w < waves; ++w) o[0][v] += red[(w * 4 + v) * 64 + lane];
+  }
   const int64_t row = r, col = n0 + 4 * kq;
   if (row >= g.m || col >= g.n) return;
   if (col + 4 <= g.n) {
@@ -891,9 +853,7 @@ __global__ __launch_bounds__(512) void direct_kernel(Source g, Out out) {
   } else {
     for (int e = 0; e < 4; ++e)
       if (col + e < g.n) {
-        sum_t w[NB][1];
-#pragma unroll
-        for (int b = 0; b < NB; ++b) w[b][0] = o[b][e];
+        const int w[1][1] = {{o[0][e]}};
         out.template store<1>(row, col + e, w, out.template cols<1>(col + e), out.template pre<1>(row, col + e));
       }
   }
@@ -907,7 +867,9 @@ constexpr int64_t kMaxPitch = (int64_t(1) << 24) - 16;
 constexpr int64_t kCus = 256;
 
 // How a product is cut, by its sizes alone (tiles counted over all B's and the batch).
-//  direct  up to 16 rows: bound by reading B once, straight from memory
+//  direct  up to 8 rows against one B in int8: straight from memory (1 x 4096 x 14336 14.9 us
+//          against 16.9 on narrow tiles, 8 rows 16.6 and 16.9, 16 rows 19.1 and 17.2; 1 x 14336 x
+//          4096 with two B's 24.7 and 25.0, with two in bf16 49.2 and 44.4)
 //  narrow  64 rows and 64 columns (128 where an operand is k-major): up to 64 rows, and where
 //          128 x 128 tiles would not be half as many as the CUs
 //  small   128 x 128 tiles where 256 x 256 ones would leave more than half the CUs idle
@@ -923,12 +885,10 @@ struct Plan {
   int parts;
 };
 // m, n at least 1; rows_only: both operands lie in rows, a_rows: A does; whole: the DMA can copy
-// (rows start at 16 bytes).  Otherwise narrow tiles have 128 columns and single rows take them too:
-// the direct kernel's loads of 64 bytes from each row, off any boundary, are four times slower
-// (8 x 14335 x 4095: 186 us against 59).  Steps through registers wait for memory, so two units
-// per CU are worth their sums there.
+// (rows start at 16 bytes).  Otherwise narrow tiles have 128 columns, and steps through registers
+// wait for memory, so two units per CU are worth their sums.
 inline Plan plan_product(int64_t m, int64_t n, int64_t steps, int mats, int batch, bool whole, bool rows_only, bool a_rows = true) {
-  if (m <= 16 && rows_only && whole) return {kDirect, 1};
+  if (m <= 8 && mats == 1 && rows_only) return {kDirect, 1};
   const int64_t cols = n * mats;
   const int64_t narrow = ceil_div(m, 64) * ceil_div(cols, rows_only && whole ? 64 : 128) * batch, small = ceil_div(m, 128) * ceil_div(cols, 128) * batch;
   auto parts = [&](int64_t tiles) { return int(std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(16, steps / 20), (whole ? 1 : 2) * kCus / tiles))); };
@@ -987,12 +947,10 @@ int launch_plain(const Source& g, const Out& out, int batch, bool a_kmajor, bool
   launch_kernel(plain_kernel<NB, Out>, dim3(blocks), dim3(256), 0, st, g, out, batch, a_kmajor, b_kmajor);
   return launch_status();
 }
-template <int KIND, int NB, class Out>
+template <class Out>
 int launch_direct(const Source& g, const Out& out, hipStream_t st) {
-  const int64_t groups = g.K * Math<KIND>::kBytes / 128;
-  const int waves = int(std::max<int64_t>(1, std::min<int64_t>(groups / 8, 8)));   // eight groups each, up to eight waves
-  const uint32_t lds = waves > 1 ? uint32_t(waves) * NB * 4 * 64 * 4 : 0;
-  launch_kernel(direct_kernel<KIND, NB, Out>, dim3(ceil_div(g.n, 16)), dim3(64 * waves), lds, st, g, out);
+  const int waves = int(std::max<int64_t>(1, std::min<int64_t>(g.K / 128 / 8, 8)));   // eight groups each, up to eight waves
+  launch_kernel(direct_kernel<Out>, dim3(ceil_div(g.n, 16)), dim3(64 * waves), 0, st, g, out);
   return launch_status();
 }
 
