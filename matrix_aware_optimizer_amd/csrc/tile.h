@@ -695,11 +695,11 @@ __global__ __launch_bounds__(C_::NT) void tile_kernel(Source g, Out out, Split s
 
 // 256 x 256 tiles in rounds of one per CU; those of the last, partial round come in `parts`
 // (2: 128 x 256, 4: 128 x 128) so that they fill the CUs.  Workgroups [0, whole) take whole tiles.
-// Bound by the matrix cores at the clock that the chip holds under them (1.6 GHz): a step of 32 bf16
-// values takes 0.74 us, 86% of it matrix instructions; prologue and epilogue of a tile 8 us (bf16
-// outputs) to 25 (fp32 momenta read and written).  4096 x 14336 x 4096 bf16: forward with g and u
-// 826 us (1.17 PFLOP/s), dx 700 (1.37), weight gradients into fp32 817 (1.18); int8 gated 2048 x
-// 14336 x 4096 239 us (2.01 POP/s), 1999 x 4096 x 14336 127 (1.85).
+// Bound by the matrix cores at the clock that the chip holds under them (1.65 GHz, 2.0 in int8): a
+// step of 32 bf16 values takes 0.67 us (0.61 in matrix instructions); prologue and epilogue of a tile
+// 9 us (bf16 outputs) to 27 (fp32 momenta read and written).  4096 x 14336 x 4096 bf16: forward with g
+// and u 771 us (1.25 PFLOP/s), dx 700 (1.37), weight gradients into fp32 814 (1.18); int8 gated 2048 x
+// 14336 x 4096 219 us (2.2 POP/s), 1999 x 4096 x 14336 117 (2.0).
 template <int KIND, bool AT, bool BT, bool DUAL, class Out>
 __global__ __launch_bounds__(256) void mixed_kernel(Source g, Out out, int batch, int64_t whole, int parts) {
   using L = Config<KIND, 256, 256, 128, 128, ring_of(AT), AT, BT, DUAL>;
