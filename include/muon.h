@@ -647,7 +647,7 @@ int ns_blocks_update(const muon_block_problem* probs, int nprobs, float a, float
  *   workspace    int8_gemm_workspace_bytes / int8_glu_workspace_bytes(m, n, K)
  *                bytes (may be 0), 16-byte aligned; contents on entry do not
  *                matter.  Calls that share one must not overlap in time.
- * K = 0 gives zeros.  lda and ldb are multiples of 16 under 2^24.  m, n, rows and
+ * K = 0 gives zeros, whatever the scales hold.  lda and ldb are multiples of 16 under 2^24.  m, n, rows and
  * cols are at most MUON_GLU_MAX_SIDE, m n at most MUON_MAX_NUMEL (MUON_EINVAL).
  * Pointers 16-byte aligned (MUON_EALIGN); unknown dtypes give MUON_EDTYPE,
  * unknown activations MUON_EINVAL, a missing or short workspace MUON_EWORKSPACE.  A zero rows, cols,

@@ -220,6 +220,17 @@ struct ScaleOut {
   }
 };
 
+// An empty contraction: zeros whatever the scales hold, as the quantiser gives a matrix without columns none.
+template <typename TC>
+__global__ __launch_bounds__(256) void zeros_kernel(TC* C, int64_t m, int64_t n, int64_t ldc) {
+  for (int64_t t = int64_t(blockIdx.x) * 256 + threadIdx.x; t < m * n; t += int64_t(gridDim.x) * 256) C[t / n * ldc + t % n] = TC(0);
+}
+template <typename TC>
+int launch_zeros(void* C, int64_t m, int64_t n, int64_t ldc, hipStream_t st) {
+  launch_kernel(zeros_kernel<TC>, dim3(std::min<int64_t>(ceil_div(m * n, 256), 8192)), dim3(256), 0, st, static_cast<TC*>(C), m, n, ldc);
+  return launch_status();
+}
+
 template <bool DUAL, class Out>
 int launch_product(const tile::Source& g, const Out& out, const tile::Plan& plan, void* workspace, hipStream_t st) {
   using tile::kI8;
@@ -282,6 +293,7 @@ int int8_gemm(const void* A, int64_t lda, const float* sa, const void* B, int64_
   const tile::Source g{{a, a}, {b, b}, lda, ldb, m, n, K, 1};
   const tile::Plan plan = tile::plan_product(m, n, K / kStep, 1, 1, true, true);
   hipStream_t hs = static_cast<hipStream_t>(stream);
+  if (K == 0) return c_dtype == MUON_F32 ? launch_zeros<float>(C, m, n, ldc, hs) : launch_zeros<bf16_t>(C, m, n, ldc, hs);
   if (c_dtype == MUON_F32) return launch_product<false>(g, ScaleOut<float>{static_cast<float*>(C), ldc, n, sa, sb}, plan, workspace, hs);
   return launch_product<false>(g, ScaleOut<bf16_t>{static_cast<bf16_t*>(C), ldc, n, sa, sb}, plan, workspace, hs);
 }
@@ -305,6 +317,7 @@ int int8_glu(const void* A, int64_t lda, const float* sa, const void* Bg, const 
   const tile::Source g{{a, a}, {static_cast<const char*>(Bg), static_cast<const char*>(Bu)}, lda, ldb, m, n, K, 1};
   const tile::Plan plan = tile::plan_product(m, n, K / kStep, 2, 1, true, true);
   hipStream_t hs = static_cast<hipStream_t>(stream);
+  if (K == 0) return h_dtype == MUON_F32 ? launch_zeros<float>(H, m, n, ldh, hs) : launch_zeros<bf16_t>(H, m, n, ldh, hs);
   if (h_dtype == MUON_F32)
     return launch_product<true>(g, GluOut<float, true>{static_cast<float*>(H), nullptr, nullptr, ldh, 0, n, act, sa, sg, su}, plan, workspace, hs);
   return launch_product<true>(g, GluOut<bf16_t, true>{static_cast<bf16_t*>(H), nullptr, nullptr, ldh, 0, n, act, sa, sg, su}, plan, workspace, hs);
