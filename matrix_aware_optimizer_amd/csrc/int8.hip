@@ -29,13 +29,13 @@ struct QuantArgs {
 
 // rint(x / s) of the exact quotient, ties to even: r = x * (1 / s) is within 2^-22 |r| of it,
 // so rint(r) is it or its neighbour, and the sign of the remainder x - k s (exact in one fma)
-// against s / 2 says which.
+// says which, its double (exact too; half of a scale under 2^-125 need not be) against s.
 __device__ __forceinline__ int quotient(float x, float s, float inv) {
   float k = rintf(x * inv);
-  const float rem = fmaf(-k, s, x), half = 0.5f * s;
-  if (fabsf(rem) >= half) {
+  const float rem = fmaf(-k, s, x), twice = 2.0f * fabsf(rem);
+  if (twice >= s) {
     // on or past the half: the neighbour on the remainder's side, where it is nearer, or even
-    const bool past = fabsf(rem) > half, odd = (int(k) & 1) != 0;
+    const bool past = twice > s, odd = (int(k) & 1) != 0;
     if (past || odd) k += copysignf(1.0f, rem);
   }
   return int(k);
