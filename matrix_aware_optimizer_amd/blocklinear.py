@@ -27,6 +27,12 @@ def _rows(t: torch.Tensor) -> torch.Tensor:
     return t.clone(memory_format=torch.contiguous_format)
 
 
+def _no_tangent(x: torch.Tensor) -> None:
+    """Refuses a dual tensor where autograd does not: the kernels would drop its tangent."""
+    if torch.autograd.forward_ad.unpack_dual(x).tangent is not None:
+        raise RuntimeError("forward-mode differentiation is not supported")
+
+
 class BlockLinear:
     """One projection ``W`` [out, in] with its fp8 codes and its momentum.
 
@@ -121,6 +127,7 @@ class BlockLinear:
             anchor = torch.empty(0, device=x.device, requires_grad=True)
             y = _BlockLinearFn.apply(flat, anchor, self)
         else:
+            _no_tangent(flat)
             y = self.forward(flat, train=False)[0]
         return y.view(*x.shape[:-1], self.W.shape[0])
 

@@ -16,7 +16,7 @@ from typing import Optional
 import torch
 
 from . import _abi
-from .blocklinear import _rows
+from .blocklinear import _no_tangent, _rows
 
 
 class GatedLinear:
@@ -126,6 +126,7 @@ class GatedLinear:
         """h for x [tokens, in] (bf16 or fp32) on int8 codes of the tokens and of the weights as of :meth:`quantize`; no gradients."""
         if self._quantized != self._state():
             raise RuntimeError("the weights have no codes, or changed after quantize()")
+        _no_tangent(x)
         x = self._flat(x)
         q, s = _abi.int8_buffers(*x.shape, device=x.device)
         _abi.int8_quantize(x, q, s)
@@ -143,6 +144,7 @@ class GatedLinear:
             anchor = torch.empty(0, device=x.device, requires_grad=True)
             h = _GatedLinearFn.apply(flat, anchor, self)
         else:
+            _no_tangent(flat)
             h = self.forward(flat, train=False)[0]
         return h.view(*x.shape[:-1], self.Wg.shape[0])
 
