@@ -700,9 +700,10 @@ int int8_glu(const void* A, int64_t lda, const float* sa, const void* Bg, const 
  * A product without terms (in = 0, out = 0 or tokens = 0 on the summed side) gives
  * zeros, or beta M.  Rows that start at 16 bytes (pitches, and sides that a product
  * walks across, multiples of 8) take the fast path; others are right and slower.
- * Sides are at most MUON_GLU_MAX_SIDE, outputs MUON_MAX_NUMEL entries, the pitches
- * of x, Wg, Wu, dG and dU under 2^23 entries; two outputs of one call at one
- * address, and dX at an operand's, are refused (MUON_EINVAL).  Pointers 16-byte aligned (MUON_EALIGN); unknown
+ * Sides are at most MUON_GLU_MAX_SIDE, outputs MUON_MAX_NUMEL entries (on the slower
+ * path about 2^37, what one launch covers), the pitches of x, Wg, Wu, dG and dU at
+ * most 2^23 - 8 entries; two outputs of one call at one address, and dX at an
+ * operand's, are refused (MUON_EINVAL).  Pointers 16-byte aligned (MUON_EALIGN); unknown
  * dtypes give MUON_EDTYPE, unknown activations MUON_EINVAL, a missing or short
  * workspace MUON_EWORKSPACE.  Where there is nothing to write the call is MUON_OK
  * and launches nothing.  Outputs may not overlap inputs but where said above.

@@ -98,12 +98,13 @@ __device__ __forceinline__ void gradients(const GradArgs& a, int64_t row, int64_
 // per entry; 4096 x 14336 92 us, 6.3 TB/s.
 template <int ACT>
 __global__ __launch_bounds__(256) void glu_gradients_kernel(GradArgs a) {
-  const int64_t per = (a.cols + 7) / 8, t = int64_t(blockIdx.x) * 256 + threadIdx.x;
-  const int64_t row = t / per, col = (t % per) * 8;
-  if (row >= a.rows) return;
-  if (col + 8 <= a.cols) gradients<ACT, 8>(a, row, col);
-  else
-    for (int64_t c = col; c < a.cols; ++c) gradients<ACT, 1>(a, row, c);
+  const int64_t per = (a.cols + 7) / 8;
+  for (int64_t t = int64_t(blockIdx.x) * 256 + threadIdx.x; t < a.rows * per; t += int64_t(gridDim.x) * 256) {
+    const int64_t row = t / per, col = (t % per) * 8;
+    if (col + 8 <= a.cols) gradients<ACT, 8>(a, row, col);
+    else
+      for (int64_t c = col; c < a.cols; ++c) gradients<ACT, 1>(a, row, c);
+  }
 }
 
 // A product on tiles: the sizes of `plan`, through the DMA where rows start at 16 bytes (whole)
@@ -208,8 +209,6 @@ int glu_backward(const void* dH, int64_t lddh, const void* G, const void* U, int
     const int ws = workspace_status(workspace, ws_bytes, glu_backward_workspace_bytes(tokens, out, in));
     if (ws != MUON_OK) return ws;
   }
-  const int64_t blocks = ceil_div(tokens * ceil_div(out, 8), 256);
-  if (blocks > INT32_MAX) return MUON_EINVAL;
   hipStream_t hs = static_cast<hipStream_t>(stream);
   if (out > 0) {
     const GradArgs a{static_cast<const bf16_t*>(dH), static_cast<const bf16_t*>(G), static_cast<const bf16_t*>(U), static_cast<bf16_t*>(dG),
@@ -218,7 +217,7 @@ int glu_backward(const void* dH, int64_t lddh, const void* G, const void* U, int
                              : act == MUON_ACT_GELU      ? glu_gradients_kernel<MUON_ACT_GELU>
                              : act == MUON_ACT_GELU_TANH ? glu_gradients_kernel<MUON_ACT_GELU_TANH>
                                                          : glu_gradients_kernel<MUON_ACT_RELU>;
-    launch_kernel(kern, dim3(blocks), dim3(256), 0, hs, a);
+    launch_kernel(kern, tile::grid_of(tokens * ceil_div(out, 8)), dim3(256), 0, hs, a);
     const int status = launch_status();
     if (status != MUON_OK) return status;
   }

@@ -227,7 +227,7 @@ __global__ __launch_bounds__(256) void zeros_kernel(TC* C, int64_t m, int64_t n,
 }
 template <typename TC>
 int launch_zeros(void* C, int64_t m, int64_t n, int64_t ldc, hipStream_t st) {
-  launch_kernel(zeros_kernel<TC>, dim3(std::min<int64_t>(ceil_div(m * n, 256), 8192)), dim3(256), 0, st, static_cast<TC*>(C), m, n, ldc);
+  launch_kernel(zeros_kernel<TC>, tile::grid_of(m * n), dim3(256), 0, st, static_cast<TC*>(C), m, n, ldc);
   return launch_status();
 }
 

@@ -766,26 +766,26 @@ __global__ __launch_bounds__(256) void join_kernel(Out out, Split sp, int64_t m)
   }
 }
 
-// Rows of fewer than eight entries: one output per thread, straight from the definition.
+// Rows of fewer than eight entries: a thread takes an output at a time, straight from the definition.
 template <int NB, class Out>
 __global__ __launch_bounds__(256) void plain_kernel(Source g, Out out, int batch, bool a_kmajor, bool b_kmajor) {
-  const int64_t t = int64_t(blockIdx.x) * 256 + threadIdx.x;
-  if (t >= g.m * g.n * batch) return;
-  const int z = int(t / (g.m * g.n));
-  const int64_t row = t / g.n % g.m, col = t % g.n;
-  float v[NB][1] = {};
-  for (int s = 0; s < g.segs; ++s)
-    for (int64_t k = 0; k < g.K; ++k) {
-      const char* a = (s || z ? g.A[1] : g.A[0]) + (a_kmajor ? k * g.lda + row * 2 : row * g.lda + k * 2);
-      const float av = bf16_to_f32(*reinterpret_cast<const bf16_t*>(a));
+  for (int64_t t = int64_t(blockIdx.x) * 256 + threadIdx.x; t < g.m * g.n * batch; t += int64_t(gridDim.x) * 256) {
+    const int z = int(t / (g.m * g.n));
+    const int64_t row = t / g.n % g.m, col = t % g.n;
+    float v[NB][1] = {};
+    for (int s = 0; s < g.segs; ++s)
+      for (int64_t k = 0; k < g.K; ++k) {
+        const char* a = (s || z ? g.A[1] : g.A[0]) + (a_kmajor ? k * g.lda + row * 2 : row * g.lda + k * 2);
+        const float av = bf16_to_f32(*reinterpret_cast<const bf16_t*>(a));
 #pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        const char* p = (s || b ? g.B[1] : g.B[0]) + (b_kmajor ? k * g.ldb + col * 2 : col * g.ldb + k * 2);
-        v[b][0] = fmaf(av, bf16_to_f32(*reinterpret_cast<const bf16_t*>(p)), v[b][0]);
+        for (int b = 0; b < NB; ++b) {
+          const char* p = (s || b ? g.B[1] : g.B[0]) + (b_kmajor ? k * g.ldb + col * 2 : col * g.ldb + k * 2);
+          v[b][0] = fmaf(av, bf16_to_f32(*reinterpret_cast<const bf16_t*>(p)), v[b][0]);
+        }
       }
-    }
-  const Out o = out.at(z);
-  o.template store<1>(row, col, v, o.template cols<1>(col), o.template pre<1>(row, col));
+    const Out o = out.at(z);
+    o.template store<1>(row, col, v, o.template cols<1>(col), o.template pre<1>(row, col));
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -901,13 +901,16 @@ inline size_t sum_bytes(const Plan& p, int64_t m, int64_t n, int mats, int batch
   return p.parts > 1 ? size_t(p.parts) * batch * size_t(m) * mats * size_t(ceil_div(n, 4) * 4) * 4 : 0;
 }
 
+// workgroups of 256 threads that stride over n entries; a launch has to stay under 2^32 threads
+inline dim3 grid_of(int64_t n) { return dim3(unsigned(std::min<int64_t>(ceil_div(n, 256), 1 << 20))); }
+
 template <class C_, bool MASKED, bool SPLIT, class Out>
 int launch_tiles(const Source& g, const Out& out, const Split& sp, hipStream_t st) {
   auto kern = tile_kernel<C_, MASKED, SPLIT, Out>;
+  const int64_t units = ceil_div(g.m, C_::BM) * ceil_div(g.n, C_::COLS) * sp.batch * sp.parts;
+  if (units * C_::NT > UINT32_MAX) return MUON_EINVAL;
   static std::atomic<uint64_t> configured{0};   // devices with the LDS limit set
   if (gemm::set_lds_limit(kern, C_::LDS_BYTES, configured) != MUON_OK) return MUON_ELAUNCH;
-  const int64_t units = ceil_div(g.m, C_::BM) * ceil_div(g.n, C_::COLS) * sp.batch * sp.parts;
-  if (units > INT32_MAX) return MUON_EINVAL;
   launch_kernel(kern, dim3(units), dim3(C_::NT), C_::LDS_BYTES, st, g, out, sp);
   const int status = launch_status();
   if (!SPLIT || status != MUON_OK) return status;
@@ -918,12 +921,12 @@ template <int KIND, bool AT, bool BT, bool DUAL, class Out>
 int launch_mixed(const Source& g, const Out& out, int batch, hipStream_t st) {
   using L = Config<KIND, 256, 256, 128, 128, ring_of(AT), AT, BT, DUAL>;
   auto kern = mixed_kernel<KIND, AT, BT, DUAL, Out>;
-  static std::atomic<uint64_t> configured{0};
-  if (gemm::set_lds_limit(kern, L::LDS_BYTES, configured) != MUON_OK) return MUON_ELAUNCH;
   const int64_t tiles = ceil_div(g.m, 256) * ceil_div(g.n, L::COLS) * batch, rest = tiles % kCus;
   const int parts = rest == 0 ? 1 : rest * 4 <= kCus ? 4 : rest * 2 <= kCus ? 2 : 1;
   const int64_t whole = parts == 1 ? tiles : tiles - rest;
-  if (whole + (tiles - whole) * parts > INT32_MAX) return MUON_EINVAL;
+  if ((whole + (tiles - whole) * parts) * L::NT > UINT32_MAX) return MUON_EINVAL;
+  static std::atomic<uint64_t> configured{0};
+  if (gemm::set_lds_limit(kern, L::LDS_BYTES, configured) != MUON_OK) return MUON_ELAUNCH;
   launch_kernel(kern, dim3(whole + (tiles - whole) * parts), dim3(256), L::LDS_BYTES, st, g, out, batch, whole, parts);
   return launch_status();
 }
@@ -942,9 +945,7 @@ int launch_large(const Source& g, const Out& out, const Split& sp, hipStream_t s
 }
 template <int NB, class Out>
 int launch_plain(const Source& g, const Out& out, int batch, bool a_kmajor, bool b_kmajor, hipStream_t st) {
-  const int64_t blocks = ceil_div(g.m * g.n * batch, 256);
-  if (blocks > INT32_MAX) return MUON_EINVAL;
-  launch_kernel(plain_kernel<NB, Out>, dim3(blocks), dim3(256), 0, st, g, out, batch, a_kmajor, b_kmajor);
+  launch_kernel(plain_kernel<NB, Out>, grid_of(g.m * g.n * batch), dim3(256), 0, st, g, out, batch, a_kmajor, b_kmajor);
   return launch_status();
 }
 template <class Out>
