@@ -689,7 +689,8 @@ int int8_glu(const void* A, int64_t lda, const float* sa, const void* Bg, const 
  *                  gradient of what reads it.  dX (may be NULL) = dG Wg + dU Wu,
  *                  of dG and dU as stored, summed in fp32 and rounded once; Wg, Wu
  *                  and the workspace are used for dX only.  dG, dU and H may each
- *                  be one of dH, G or U itself (same pointer and pitch).
+ *                  be one of dH, G or U itself (same pointer and pitch; another
+ *                  pitch is refused, MUON_EINVAL).
  * glu_weight_grad  Mg <- beta Mg + alpha dG^T x, Mu <- beta Mu + alpha dU^T x, Mg
  *                  and Mu [out][in] F32 or BF16: the weight gradients straight
  *                  into the momentum.  Sums are fp32 over all tokens, the result

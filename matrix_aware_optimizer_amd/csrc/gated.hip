@@ -202,6 +202,11 @@ int glu_backward(const void* dH, int64_t lddh, const void* G, const void* U, int
   if (!numel_ok(tokens * out) || !numel_ok(tokens * in) || (out > 0 && (same(dG, dU) || same(H, dG) || same(H, dU)))) return MUON_EINVAL;
   if (input && (same(dX, dG) || same(dX, dU) || same(dX, H) || same(dX, Wg) || same(dX, Wu))) return MUON_EINVAL;
   if (lddh < out || ldg < out || !pitch_ok(ldd, out) || (H != nullptr && ldh < out)) return MUON_EINVAL;
+  // an output over an operand row by row: other pitches would write rows that are still to be read
+  const auto crossed = [&](const void* o, int64_t ldo) {
+    return (same(o, dH) && ldo != lddh) || ((same(o, G) || same(o, U)) && ldo != ldg);
+  };
+  if (tokens > 1 && out > 0 && (crossed(dG, ldd) || crossed(dU, ldd) || crossed(H, ldh))) return MUON_EINVAL;
   if (input && (lddx < in || !pitch_ok(ldw, in) || (out > 0 && (Wg == nullptr || Wu == nullptr)))) return MUON_EINVAL;
   if (!aligned16(dH) || !aligned16(G) || !aligned16(U) || !aligned16(dG) || !aligned16(dU) || !aligned16(H)) return MUON_EALIGN;
   if (input && (!aligned16(Wg) || !aligned16(Wu) || !aligned16(dX))) return MUON_EALIGN;
