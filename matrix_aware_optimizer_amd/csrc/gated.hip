@@ -84,7 +84,7 @@ __device__ __forceinline__ void gradients(const GradArgs& a, int64_t row, int64_
 #pragma unroll
   for (int k = 0; k < N; ++k) {
     float slope;
-    const float act = activate<true>(ACT, g[k], slope);
+    const float act = activate<true, false>(ACT, g[k], slope);
     dg[k] = dh[k] * u[k] * slope;
     du[k] = dh[k] * act;
     h[k] = act * u[k];
