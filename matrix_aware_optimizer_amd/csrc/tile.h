@@ -896,6 +896,11 @@ inline Plan plan_product(int64_t m, int64_t n, int64_t steps, int mats, int batc
   if (2 * small <= kCus || 2 * ceil_div(m, 256) * ceil_div(cols, 256) * batch < kCus) return {kSmall, parts(small)};
   return {kLarge, 1};
 }
+// how many parts each tile of mixed_kernel's last, partial round comes in (1: there is none, or it stays whole)
+inline int last_round_parts(int64_t tiles) {
+  const int64_t rest = tiles % kCus;
+  return rest == 0 ? 1 : rest * 4 <= kCus ? 4 : rest * 2 <= kCus ? 2 : 1;
+}
 // bytes of the parts' sums
 inline size_t sum_bytes(const Plan& p, int64_t m, int64_t n, int mats, int batch) {
   return p.parts > 1 ? size_t(p.parts) * batch * size_t(m) * mats * size_t(ceil_div(n, 4) * 4) * 4 : 0;
@@ -921,9 +926,9 @@ template <int KIND, bool AT, bool BT, bool DUAL, class Out>
 int launch_mixed(const Source& g, const Out& out, int batch, hipStream_t st) {
   using L = Config<KIND, 256, 256, 128, 128, ring_of(AT), AT, BT, DUAL>;
   auto kern = mixed_kernel<KIND, AT, BT, DUAL, Out>;
-  const int64_t tiles = ceil_div(g.m, 256) * ceil_div(g.n, L::COLS) * batch, rest = tiles % kCus;
-  const int parts = rest == 0 ? 1 : rest * 4 <= kCus ? 4 : rest * 2 <= kCus ? 2 : 1;
-  const int64_t whole = parts == 1 ? tiles : tiles - rest;
+  const int64_t tiles = ceil_div(g.m, 256) * ceil_div(g.n, L::COLS) * batch;
+  const int parts = last_round_parts(tiles);
+  const int64_t whole = parts == 1 ? tiles : tiles - tiles % kCus;
   if ((whole + (tiles - whole) * parts) * L::NT > UINT32_MAX) return MUON_EINVAL;
   static std::atomic<uint64_t> configured{0};
   if (gemm::set_lds_limit(kern, L::LDS_BYTES, configured) != MUON_OK) return MUON_ELAUNCH;
