@@ -118,9 +118,14 @@ int launch_tiled(const tile::Source& g, const Out& out, const tile::Plan& plan, 
   }
   // through registers, 256 x 256 tiles pay over 2048 and more values (14335 x 4095 weight gradients of
   // 4096 tokens 1319 us against 1501, of 300 tokens 71 against 45), and for one B only: two spill
-  if (plan.kind == tile::kSmall || (!whole && (DUAL || g.K * g.segs < 2048)))
-    return whole ? tile::launch_sized<tile::Config<kBf16, 128, 128, 64, 64, tile::ring_of(AT), AT, BT, DUAL>, false>(g, out, sp, st)
-                 : tile::launch_sized<tile::Config<kBf16, 128, 128, 64, 64, 3, AT, BT, DUAL>, true>(g, out, sp, st);
+  if (plan.kind == tile::kSmall || (!whole && (DUAL || g.K * g.segs < 2048))) {
+    using Copied = tile::Config<kBf16, 128, 128, 64, 64, tile::ring_of(AT), AT, BT, DUAL>;
+    using Held = tile::Config<kBf16, 128, 128, 64, 64, 3, AT, BT, DUAL>;
+    if (!whole) return tile::launch_sized<Held, true>(g, out, sp, st);
+    // one part for dx: where small tiles are no more than half the CUs, twice as many narrow ones are at most the CUs
+    if constexpr (!AT && BT) return tile::launch_tiles<Copied, false, false>(g, out, sp, st);
+    else return tile::launch_sized<Copied, false>(g, out, sp, st);
+  }
   if constexpr (!DUAL)
     if (!whole) return tile::launch_tiles<tile::Config<kBf16, 256, 256, 128, 128, 3, AT, BT, DUAL>, true, false>(g, out, sp, st);
   return tile::launch_large<kBf16, AT, BT, DUAL>(g, out, sp, st);
