@@ -21,8 +21,8 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 }
 
 // 16 bytes at p; PASSING: past the caches' order of keeping.  The outputs of products on large tiles
-// pass, so that the operands' panels stay in L2: 2048 x 14336 x 4096 int8 gated 253 -> 245 us, 1999
-// x 4096 x 14336 140 -> 134, weight gradients 857 -> 849.  Not what the next kernel reads (dg, du),
+// pass, so that the operands' panels stay in L2 (measured then: 2048 x 14336 x 4096 int8 gated 253 -> 245 us, 1999
+// x 4096 x 14336 140 -> 134, weight gradients 857 -> 849).  Not what the next kernel reads (dg, du),
 // and not rows that end inside a cache line, whose halves would pass one by one (weight gradients
 // of 14335 x 4095 from 64 tokens 190 -> 235).  A choice of the type: as a branch in the store it costs
 // more than it gains (136 against 129 us for the second).

@@ -7,8 +7,8 @@
 //
 // Sums, activations and products are fp32 and each output is rounded once.  dg and du are outputs
 // in bf16, and dx and the weight gradients take them as stored: the matrix instructions read bf16,
-// and a second part for what the rounding leaves would double the products.  It makes dx 1.4 times
-// its own rounding (2.3e-3 of its norm instead of 1.7e-3).
+// and a second part for what the rounding leaves would double the products (dx of 4096 x 14336 x 4096
+// 1400 us for 700).  It makes dx 1.4 times its own rounding (2.3e-3 of its norm instead of 1.7e-3).
 #include <algorithm>
 
 #include "act.h"
@@ -40,7 +40,7 @@ struct AxpbyOut {
     return o;
   }
   template <int N> __device__ __forceinline__ Cols<N> cols(int64_t) const { return {}; }
-  // read once; PASSING: past the caches' order of keeping (weight gradients of the largest case 848 -> 833 us)
+  // read once; PASSING: past the caches' order of keeping (weight gradients of 14336 x 4096 from 4096 tokens, 848 -> 833 us then)
   template <int N> __device__ __forceinline__ Pre<N> pre(int64_t row, int64_t col) const {
     Pre<N> p;
     if constexpr (READS) {

@@ -23,6 +23,10 @@
 //   masked    steps that the DMA cannot copy (the last one of a K that is not whole steps, and
 //             every step where rows do not start at 16 bytes) go through registers, with zeros
 //             past the ends.
+//
+// Times given as a -> b, or of one side against the other, belong to the choice that they stand
+// at: both sides on one card, when it was made.  Later changes moved both.  What the products take
+// now stands at mixed_kernel and direct_kernel, over several cards.
 #pragma once
 
 #include <algorithm>
@@ -697,9 +701,10 @@ __global__ __launch_bounds__(C_::NT) void tile_kernel(Source g, Out out, Split s
 // (2: 128 x 256, 4: 128 x 128) so that they fill the CUs.  Workgroups [0, whole) take whole tiles.
 // Bound by the matrix cores at the clock that the chip holds under them (1.65 GHz, 2.0 in int8): a
 // step of 32 bf16 values takes 0.67 us (0.61 in matrix instructions); prologue and epilogue of a tile
-// 9 us (bf16 outputs) to 27 (fp32 momenta read and written).  4096 x 14336 x 4096 bf16: forward with g
-// and u 771 us (1.25 PFLOP/s), dx 700 (1.37), weight gradients into fp32 814 (1.18); int8 gated 2048 x
-// 14336 x 4096 219 us (2.2 POP/s), 1999 x 4096 x 14336 117 (2.0).
+// 9 us (bf16 outputs) to 27 (fp32 momenta read and written).  Over several cards, 4096 x 14336 x 4096
+// bf16: forward with g and u 768 to 791 us (1.22 to 1.25 PFLOP/s), dx 700 to 725 (1.33 to 1.37), weight
+// gradients into fp32 806 to 833 (1.15 to 1.19); int8 gated 2048 x 14336 x 4096 219 to 226 us (2.1 to
+// 2.2 POP/s), 1999 x 4096 x 14336 117 to 121 (1.9 to 2.0).
 template <int KIND, bool AT, bool BT, bool DUAL, class Out>
 __global__ __launch_bounds__(256) void mixed_kernel(Source g, Out out, int batch, int64_t whole, int parts) {
   using L = Config<KIND, 256, 256, 128, 128, ring_of(AT), AT, BT, DUAL>;
@@ -791,11 +796,11 @@ __global__ __launch_bounds__(256) void plain_kernel(Source g, Out out, int batch
 // ---------------------------------------------------------------------------
 // Few rows
 // ---------------------------------------------------------------------------
-// Few rows (16 at most) of int8 against one B, bound by reading B: 1 x 4096 x 14336 12.7 us (4.6 TB/s).
-// Straight from memory: no tile is staged, each wave reads 16 rows of B and the rows of A, 128
-// bytes of each at a time, and multiplies them on 16 x 16 blocks.  The waves of a workgroup take
-// the 128-byte groups of the contraction in turn; their sums meet in LDS.  B is the first operand:
-// a lane holds four consecutive columns of one row of C.
+// Few rows (8 at most, see Plan; the blocks hold 16) of int8 against one B, bound by reading B: 1 x
+// 4096 x 14336 12.6 us (4.6 TB/s).  Straight from memory: no tile is staged, each wave reads 16 rows
+// of B and the rows of A, 128 bytes of each at a time, and multiplies them on 16 x 16 blocks.  The
+// waves of a workgroup take the 128-byte groups of the contraction in turn; their sums meet in LDS.
+// B is the first operand: a lane holds four consecutive columns of one row of C.
 template <class Out>
 __global__ __launch_bounds__(512) void direct_kernel(Source g, Out out) {
   using M_ = Math<kI8>;
@@ -867,9 +872,11 @@ constexpr int64_t kMaxPitch = (int64_t(1) << 24) - 16;
 constexpr int64_t kCus = 256;
 
 // How a product is cut, by its sizes alone (tiles counted over all B's and the batch).
-//  direct  up to 8 rows against one B in int8: straight from memory (1 x 4096 x 14336 14.9 us
-//          against 16.9 on narrow tiles, 8 rows 16.6 and 16.9, 16 rows 19.1 and 17.2; 1 x 14336 x
-//          4096 with two B's 24.7 and 25.0, with two in bf16 49.2 and 44.4)
+//  direct  up to 8 rows against one B in int8: straight from memory (4096 x 14336, 1 row 12.9 us
+//          against 15.1 on narrow tiles, 4 rows 13.8 and 15.0, 8 rows 14.8 and 15.1, 16 rows 17.2
+//          and 15.2; 14336 x 4096, 1 row 12.1 and 12.9, 4 rows 13.1 and 13.0, 8 rows 14.5 and 13.0;
+//          2304 x 768 8.1 and 8.1 for all of them).  Not two B's: 1 x 14336 x 4096 24.7 and 25.0,
+//          in bf16 49.2 and 44.4
 //  narrow  64 rows and 64 columns (128 where an operand is k-major): up to 64 rows, and where
 //          128 x 128 tiles would not be half as many as the CUs
 //  small   128 x 128 tiles where 256 x 256 ones would leave more than half the CUs idle
