@@ -138,7 +138,7 @@ class GatedLinear:
         """h for x [..., in], differentiable: backward goes through :meth:`backward`."""
         if x.dim() == 0 or x.shape[-1] != self.Wg.shape[1]:
             raise ValueError(f"x must be [..., {self.Wg.shape[1]}]")
-        flat = x.reshape(-1, x.shape[-1]) if x.shape[-1] else x.new_empty((x.shape[:-1].numel(), 0))
+        flat = x.reshape(x.shape[:-1].numel(), x.shape[-1])
         if torch.is_grad_enabled():
             # the weights are no leaves of autograd (their gradients go into the momenta), so the node hangs on x or on an empty anchor
             anchor = torch.empty(0, device=x.device, requires_grad=True)
