@@ -106,10 +106,11 @@ class GatedLinear:
 
     def step(self) -> None:
         """The update of both weights from their momenta, each orthogonalised as a whole."""
-        U = [torch.empty_like(W) for W in (self.Wg, self.Wu)]
-        _abi.ns_orthogonalize([(self.Mg, U[0], None), (self.Mu, U[1], None)], *self.coeffs, self.ns_steps)
-        for W, direction in zip((self.Wg, self.Wu), U):
-            _abi.apply_update_dense(W, direction, self.eta)
+        if self.Wg.numel() > 0:
+            U = [torch.empty_like(W) for W in (self.Wg, self.Wu)]
+            _abi.ns_orthogonalize([(self.Mg, U[0], None), (self.Mu, U[1], None)], *self.coeffs, self.ns_steps)
+            for W, direction in zip((self.Wg, self.Wu), U):
+                _abi.apply_update_dense(W, direction, self.eta)
         self.weights_changed()
         self._accumulating = False
 

@@ -15,6 +15,14 @@ def forward_and_backward(lin, device, tokens=7):
     return x
 
 
+def whole_step(lin, device, tokens=7):
+    x, out = forward_and_backward(lin, device, tokens), lin.Wg.shape[0]
+    lin.step()
+    lin.quantize()
+    h = lin.answer(x.detach())
+    assert h.shape == (tokens, out) and (h == 0).all()
+
+
 SIZES = [(40, 0), (0, 40), (0, 0)]
 
 
@@ -27,3 +35,15 @@ def test_gradients_of_empty_blocks(host, out, inp):
 @pytest.mark.parametrize("out,inp", SIZES)
 def test_gradients_of_empty_blocks_on_the_gpu(out, inp):
     forward_and_backward(block(out, inp, device="cuda"), "cuda")
+
+
+@pytest.mark.parametrize("out,inp", SIZES)
+def test_empty_blocks(host, out, inp):
+    whole_step(block(out, inp), "cpu")
+    assert not [name for name, _, _ in host if name in ("ns_orthogonalize", "apply_update_dense")]     # they refuse empty matrices
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("out,inp", SIZES)
+def test_empty_blocks_on_the_gpu(out, inp):
+    whole_step(block(out, inp, device="cuda"), "cuda")
