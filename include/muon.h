@@ -703,11 +703,11 @@ int int8_glu(const void* A, int64_t lda, const float* sa, const void* Bg, const 
  * walks across, multiples of 8) take the fast path; others are right and slower.
  * Sides are at most MUON_GLU_MAX_SIDE, outputs MUON_MAX_NUMEL entries (on the slower
  * path about 2^37, what one launch covers), the pitches of x, Wg, Wu, dG and dU at
- * most 2^23 - 8 entries; two outputs of one call at one address, and dX at an
- * operand's, are refused (MUON_EINVAL).  Pointers 16-byte aligned (MUON_EALIGN); unknown
- * dtypes give MUON_EDTYPE, unknown activations MUON_EINVAL, a missing or short
- * workspace MUON_EWORKSPACE.  Where there is nothing to write the call is MUON_OK
- * and launches nothing.  Outputs may not overlap inputs but where said above.
+ * most 2^23 - 8 entries; two outputs of one call at one address, and dX at that of
+ * Wg or Wu, are refused (MUON_EINVAL).  Pointers 16-byte aligned (MUON_EALIGN);
+ * unknown dtypes give MUON_EDTYPE, unknown activations MUON_EINVAL, a missing or
+ * short workspace MUON_EWORKSPACE.  Where there is nothing to write the call is
+ * MUON_OK and launches nothing.  Outputs may not overlap inputs but where said above.
  * ------------------------------------------------------------------------- */
 size_t glu_forward_workspace_bytes(int64_t tokens, int64_t out, int64_t in);
 int glu_forward(const void* X, int64_t ldx, const void* Wg, const void* Wu, int64_t ldw, int act, void* H, int64_t ldh, void* G,
